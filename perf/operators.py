@@ -264,7 +264,7 @@ def _own_tokens(s):
     import dense_fp32_tiled_amd as dft
 
     offsets, order, position = dft.expert_sort(s["chosen"], s["experts"])
-    rows = dft.expert_gather(s["x"], order, s["top_k"])
+    rows = dft.expert_gather(s["x"], position)
     out = dft.expert_combine(s["y"], position, s["weights"])
     dy, dweights = dft.expert_combine_grad(s["dout"], s["y"], position, s["weights"])
     dx = dft.expert_combine(s["y"], position)
