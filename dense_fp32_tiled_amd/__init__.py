@@ -126,6 +126,16 @@ EXPORTS = (
     "gemm_lds_conflict_degree",
     "gemm_lds_access_cycles",
     "gemm_lds_page_pad",
+    "gemm_linear",
+    "gemm_linear_workspace_bytes",
+    "gemm_linear_choice",
+    "gemm_linear_grad",
+    "gemm_linear_grad_workspace_bytes",
+    "gemm_expert_sort",
+    "gemm_expert_sort_workspace_bytes",
+    "gemm_expert_gather",
+    "gemm_expert_combine",
+    "gemm_expert_combine_grad",
 )
 
 
@@ -222,6 +232,9 @@ def library(path: Path | None = None):
     lib.gemm_lds_access_cycles.restype = i32
     lib.gemm_lds_page_pad.argtypes = [i32, i32, i32]
     lib.gemm_lds_page_pad.restype = i32
+    from . import products
+
+    products.declare(lib)
     if path is None:
         _lib = lib
     return lib
@@ -454,3 +467,13 @@ def matmul(a, b, out=None, variant: int = VARIANT_AUTO, stream=None):
     if st != GEMM_OK:
         raise GemmError(st, "gemm_f32_ex")
     return out
+
+
+from .products import (  # noqa: E402
+    ACT_GELU, ACT_GELU_TANH, ACT_NAMES, ACT_NONE, ACT_RELU, ACT_SILU, LINEAR_32x128, LINEAR_64x64, LINEAR_128x128,
+    LINEAR_256x256, LINEAR_AUTO, LINEAR_COUNT, LINEAR_NAMES, OUTPUT_F32, OUTPUT_SAME, LinearArgs, LinearGradArgs,
+    LinearGrads, expert_combine, expert_combine_grad, expert_gather, expert_mlp, expert_mlp_grad, expert_sort,
+    gemm_expert_combine, gemm_expert_combine_grad, gemm_expert_gather, gemm_expert_sort,
+    gemm_expert_sort_workspace_bytes, gemm_linear, gemm_linear_choice, gemm_linear_grad,
+    gemm_linear_grad_workspace_bytes, gemm_linear_workspace_bytes, grouped_linear, grouped_linear_grad, linear,
+    linear_grad)

@@ -4,8 +4,9 @@
 
 first runs the host LDS layout search (csrc/layout_gen.cpp ->
 csrc/generated/mfma_layouts.hpp), then produces
-dense_fp32_tiled_amd/libdense_fp32_tiled.so from csrc/gemm_api.hip and
-csrc/gemm_default.hip, the same library built with DFT_LDS_POISON=1
+dense_fp32_tiled_amd/libdense_fp32_tiled.so from csrc/gemm_api.hip,
+csrc/gemm_default.hip and csrc/linear_*.hip (one object per source, compiled
+at once), the same library built with DFT_LDS_POISON=1
 (libdense_fp32_tiled_poison.so, for the LDS-poison parity tests), and the
 measurement probes liblds_probe.so from csrc/lds_probe.hip.
 Packed fp32 VALU instructions are disabled for all device code
@@ -18,6 +19,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -26,6 +28,10 @@ CSRC = PKG / "csrc"
 LIB = PKG / "libdense_fp32_tiled.so"
 POISON_LIB = PKG / "libdense_fp32_tiled_poison.so"
 SOURCES = [CSRC / "gemm_api.hip", CSRC / "gemm_default.hip"]
+# The products with an epilogue and the token sort: compiled with SOURCES into the same library.  Listed apart because
+# their direct copies are buffer loads (range-checked), SOURCES' global ones; each list has its own checks of the
+# compiled code.
+LINEAR_SOURCES = [CSRC / "linear_api.hip", CSRC / "linear_bf16.hip", CSRC / "linear_f16.hip"]
 PROBE_LIB = PKG / "liblds_probe.so"
 PROBE_SOURCES = [CSRC / "lds_probe.hip"]
 ARCH = "gfx950"
@@ -35,7 +41,6 @@ HIPCC_FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall",
     "-Wno-unused-command-line-argument",
@@ -57,8 +62,6 @@ def generate_layouts() -> Path:
     with g++), writing csrc/generated/mfma_layouts.hpp for the kernels.
     Safe to run from several processes at once: the search is built in a
     private directory and the header replaced atomically."""
-    import tempfile
-
     GENERATED.mkdir(exist_ok=True)
     with tempfile.TemporaryDirectory() as work:
         exe = Path(work) / "layout_gen"
@@ -73,20 +76,33 @@ def generate_layouts() -> Path:
 
 
 def _start(out: Path, extra: list[str] | None, sources: list[Path] | None):
-    tmp = out.with_name(f"{out.name}.{os.getpid()}.tmp")
-    cmd = [hipcc(), *HIPCC_FLAGS, *(extra or []), f"-I{ROOT / 'include'}", f"-I{CSRC}",
-           *[str(s) for s in (sources or SOURCES)], "-o", str(tmp)]
-    proc = subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
-    return proc, tmp, out, cmd
+    """Starts one compiler per source; _finish links what they make."""
+    work = tempfile.TemporaryDirectory()
+    jobs = []
+    for src in sources or [*SOURCES, *LINEAR_SOURCES]:
+        obj = Path(work.name) / f"{src.stem}.o"
+        cmd = [hipcc(), *HIPCC_FLAGS, *(extra or []), f"-I{ROOT / 'include'}", f"-I{CSRC}", "-c", str(src), "-o",
+               str(obj)]
+        log = open(obj.with_suffix(".log"), "w+")
+        jobs.append((subprocess.Popen(cmd, stdout=subprocess.DEVNULL, stderr=log, text=True), log, obj, cmd))
+    return work, jobs, out
 
 
 def _finish(job) -> Path:
-    proc, tmp, out, cmd = job
-    _, err = proc.communicate()
-    if proc.returncode != 0:
-        sys.stderr.write(err)
-        raise RuntimeError(f"hipcc failed ({proc.returncode}): {' '.join(cmd)}")
-    os.replace(tmp, out)
+    work, jobs, out = job
+    with work:
+        for proc, log, _, cmd in jobs:
+            proc.wait()
+            log.seek(0)
+            err = log.read()
+            log.close()
+            if proc.returncode != 0:
+                sys.stderr.write(err)
+                raise RuntimeError(f"hipcc failed ({proc.returncode}): {' '.join(cmd)}")
+        tmp = out.with_name(f"{out.name}.{os.getpid()}.tmp")
+        subprocess.run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *[str(obj) for _, _, obj, _ in jobs],
+                        "-o", str(tmp)], check=True)
+        os.replace(tmp, out)
     return out
 
 
@@ -100,7 +116,7 @@ def build_all() -> list[Path]:
     with NaN before the first copy: DFT_LDS_POISON=1) and the probe library,
     compiled concurrently."""
     generate_layouts()
-    jobs = [_start(LIB, None, SOURCES), _start(POISON_LIB, ["-DDFT_LDS_POISON=1"], SOURCES),
+    jobs = [_start(LIB, None, None), _start(POISON_LIB, ["-DDFT_LDS_POISON=1"], None),
             _start(PROBE_LIB, None, PROBE_SOURCES)]
     return [_finish(j) for j in jobs]
 
@@ -109,8 +125,6 @@ def device_assembly(source: Path | None = None) -> str:
     """The gfx950 assembly hipcc emits for the library's device code (the
     same flags as the build), as text: of `source`, or of every library
     source concatenated."""
-    import tempfile
-
     if source is None:
         return "\n".join(device_assembly(src) for src in SOURCES)
     generate_layouts()
@@ -133,7 +147,6 @@ def resource_report(source: Path | None = None) -> dict[str, dict[str, int]]:
     "lds" (bytes per workgroup)}}, of `source` or of every library source.
     Compiles device code only, to a temporary object."""
     import re
-    import tempfile
 
     if source is None:
         merged: dict[str, dict[str, int]] = {}

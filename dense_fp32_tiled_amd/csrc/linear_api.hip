@@ -1,0 +1,587 @@
+// linear_api.hip -- the C ABI of the products with an epilogue, their
+// gradients and the token sort (include/dense_fp32_tiled.h): argument checks,
+// the choice of tile and slices, and the launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <mutex>
+#include <stdint.h>
+#include <string.h>
+
+#include "dense_fp32_tiled.h"
+#include "expert_kernels.hpp"
+#include "linear_shapes.hpp"
+#include "slope_kernels.hpp"
+
+namespace {
+
+using namespace dft;
+
+// ---- the device ---------------------------------------------------------------------
+constexpr int kMaxDevices = 64;
+int g_cus[kMaxDevices];  // 0 unknown, -1 not gfx950, else compute units
+std::mutex g_cus_mu;
+
+int current_cus(int* cus) {
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return GEMM_ERR_HIP;
+    if (dev < 0 || dev >= kMaxDevices) return GEMM_ERR_UNSUPPORTED;
+    std::lock_guard<std::mutex> lock(g_cus_mu);
+    if (g_cus[dev] == 0) {
+        hipDeviceProp_t prop;
+        if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return GEMM_ERR_HIP;
+        g_cus[dev] = strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? prop.multiProcessorCount : -1;
+    }
+    if (g_cus[dev] < 0) return GEMM_ERR_UNSUPPORTED;
+    *cus = g_cus[dev];
+    return GEMM_OK;
+}
+
+// ---- argument checks ----------------------------------------------------------------
+constexpr int64_t kMaxDim = (int64_t)1 << 40;  // products of a size, a pitch and an element's bytes stay inside int64
+constexpr int64_t kMaxGrid = 0x7fffffff;
+
+struct Matrix {
+    const void* data;
+    int64_t rows, cols, ld, elem, copies = 1, copy_stride = 0;
+
+    bool empty() const { return rows == 0 || cols == 0 || copies == 0; }
+    bool pitch_ok() const {
+        return ld >= std::max<int64_t>(cols, 1) && (copies <= 1 || rows == 0 || copy_stride >= (rows - 1) * ld + cols);
+    }
+    bool small_enough() const {
+        const int64_t lim = (int64_t)1 << 59;
+        return rows <= lim / ld && (copies <= 1 || copy_stride <= lim / copies);
+    }
+    int64_t bytes() const {
+        return empty() ? 0 : ((copies - 1) * copy_stride + (rows - 1) * ld + cols) * elem;
+    }
+    bool overlaps(const Matrix& o) const {
+        if (!data || !o.data || empty() || o.empty()) return false;
+        const uintptr_t a = (uintptr_t)data, b = (uintptr_t)o.data;
+        return a < b + (uintptr_t)o.bytes() && b < a + (uintptr_t)bytes();
+    }
+    bool same_place(const Matrix& o) const { return data == o.data && ld == o.ld && elem == o.elem; }
+    // Every row starts on 16 bytes (and every copy).
+    bool aligned16() const {
+        return ((uintptr_t)data & 15) == 0 && ld % 8 == 0 && (copies <= 1 || copy_stride % 8 == 0);
+    }
+};
+
+// Pitches, sizes and presence of every matrix; `absent` may be NULL.
+struct Use {
+    Matrix m;
+    bool optional, written;
+};
+int check_matrices(const Use* uses, int n) {
+    for (int i = 0; i < n; ++i)
+        if ((uses[i].m.data || !uses[i].optional) && !uses[i].m.pitch_ok()) return GEMM_ERR_INVALID_LD;
+    for (int i = 0; i < n; ++i)
+        if ((uses[i].m.data || !uses[i].optional) && !uses[i].m.small_enough()) return GEMM_ERR_TOO_LARGE;
+    for (int i = 0; i < n; ++i)
+        if (!uses[i].optional && !uses[i].m.empty() && !uses[i].m.data) return GEMM_ERR_NULL;
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < n; ++j)
+            if (i != j && uses[i].written && uses[i].m.overlaps(uses[j].m)) return GEMM_ERR_ALIAS;
+    return GEMM_OK;
+}
+
+int64_t elem_bytes(int output_type) { return output_type == GEMM_OUTPUT_F32 ? 4 : 2; }
+bool known_type(int input_type) { return input_type == GEMM_INPUT_BF16 || input_type == GEMM_INPUT_F16; }
+bool known_output(int t) { return t == GEMM_OUTPUT_SAME || t == GEMM_OUTPUT_F32; }
+bool known_act(int a) { return a >= 0 && a < kActCount; }
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ---- the choice of tile and slices ----------------------------------------------------
+struct Plan {
+    LinearTile tile;
+    bool direct;
+    int splits;
+    int64_t slice;
+};
+
+// Full-chip rates of the tiles (TFLOP/s, one type) and workgroups per CU.
+struct TileRate {
+    double rate;
+    int per_cu;
+};
+constexpr TileRate kDirectRates[kTileCount] = {{1200, 1}, {950, 2}, {600, 2}, {350, 2}};
+constexpr TileRate kRegisterRates[kTileCount] = {{0, 1}, {400, 2}, {250, 2}, {150, 2}};
+constexpr int kMaxSlices = 32;
+
+// Estimated microseconds of a plan: whole rounds of workgroups, each as long
+// as its multiply at the tile's rate or as its own operand stream, with a
+// fixed cost to fill and drain it; slices add the join's launch and traffic.
+double estimate(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, LinearTile t, bool direct, int splits,
+                int cus) {
+    const TileRate rate = (direct ? kDirectRates : kRegisterRates)[t];
+    if (rate.rate <= 0) return 1e30;
+    const TileSize size = kTileSizes[t];
+    double row_tiles = (double)ceil_div(R, size.bm), length = (double)L;
+    if (axis == kGroupRows)  // on average half a tile more for every group that has rows
+        row_tiles = (double)R / size.bm + 0.5 * (double)std::min<int64_t>(groups, R);
+    double tiles = row_tiles * (double)ceil_div(C, size.bn) * splits;
+    if (axis == kGroupContraction) {
+        tiles *= (double)groups;
+        length = (double)L / (double)groups;
+    }
+    const double slots = (double)cus * rate.per_cu;
+    const double rounds = std::max(1.0, tiles > 4 * slots ? tiles / slots : (double)(int64_t)(tiles / slots + 0.999));
+    const double deep = ceil_div((int64_t)(length / splits + 0.999), kTileDepth) * (double)kTileDepth;
+    const double multiply = 2.0 * size.bm * size.bn * deep / (rate.rate / slots) * 1e-6;
+    const double stream = 2.0 * (size.bm + size.bn) * deep / 60e3;  // 60 GB/s per workgroup
+    double us = rounds * (std::max(multiply, stream) + 1.5) + 2.0;
+    if (splits > 1) us += 3.0 + (splits + 1.0) * (double)R * (double)C * 4.0 / 4e6;
+    return us;
+}
+
+Plan choose(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, bool direct, int variant, int splits, int cus) {
+    Plan best{kTile128, direct, 1, L};
+    double least = 1e300;
+    for (int t = 0; t < kTileCount; ++t) {
+        if (variant != GEMM_LINEAR_AUTO && t != variant - 1) continue;
+        LinearTile tile = (LinearTile)t;
+        if (tile == kTile256 && !direct) {
+            if (variant == GEMM_LINEAR_AUTO) continue;
+            tile = kTile128;
+        }
+        for (int s = 1; s <= kMaxSlices; s *= 2) {
+            int use = splits > 0 ? splits : s;
+            if (axis != kGroupNone || L == 0) use = 1;
+            // slices of whole tiles, none of them empty, at least four deep unless asked for
+            const int64_t slice = ceil_div(ceil_div(L, kTileDepth), use) * kTileDepth;
+            if (use > 1) {
+                if (splits == 0 && slice < 4 * kTileDepth) break;
+                use = (int)ceil_div(L, slice);
+            }
+            const double us = estimate(R, C, L, groups, axis, tile, direct, use, cus);
+            if (us < least) {
+                least = us;
+                best = Plan{tile, direct, std::max(use, 1), slice};
+            }
+            if (splits > 0 || axis != kGroupNone || L == 0) break;
+        }
+    }
+    return best;
+}
+
+int64_t partial_bytes(const Plan& plan, int64_t R, int64_t C) { return plan.splits > 1 ? plan.splits * R * C * 4 : 0; }
+
+// Row tiles enough for any division of R rows into groups.
+int64_t row_tiles(int64_t R, int64_t groups, int axis, int64_t bm) {
+    if (axis != kGroupRows) return ceil_div(R, bm);
+    return (R + groups * (bm - 1)) / bm;
+}
+
+int check_grid(const Plan& plan, int64_t R, int64_t C, int64_t groups, int axis) {
+    const TileSize size = kTileSizes[plan.tile];
+    const int64_t tiles_m = row_tiles(R, groups, axis, size.bm), tiles_n = ceil_div(C, size.bn);
+    if (tiles_n > 0 && tiles_m > kMaxGrid / 512 / tiles_n) return GEMM_ERR_TOO_LARGE;
+    if (8 * tiles_n > 0x7fffffff) return GEMM_ERR_TOO_LARGE;
+    return GEMM_OK;
+}
+
+hipError_t launch(int type, const LinearProblem& p, LinearLayout layout, const Plan& plan, hipStream_t stream) {
+    const TileSize size = kTileSizes[plan.tile];
+    const uint32_t tiles_m = (uint32_t)row_tiles(p.R, p.groups, p.axis, size.bm), tiles_n = (uint32_t)ceil_div(p.C, size.bn);
+    const uint32_t grid_y = p.axis == kGroupContraction ? (uint32_t)p.groups : (uint32_t)plan.splits;
+    if (tiles_m == 0 || tiles_n == 0) return hipSuccess;
+    const hipError_t e = type == GEMM_INPUT_BF16
+                             ? launch_linear_bf16(p, layout, plan.tile, plan.direct, tiles_m, tiles_n, grid_y, stream)
+                             : launch_linear_f16(p, layout, plan.tile, plan.direct, tiles_m, tiles_n, grid_y, stream);
+    if (e != hipSuccess || plan.splits <= 1) return e;
+    LinearProblem problem = p;
+    const int64_t blocks = std::min<int64_t>(ceil_div(p.R * ceil_div(p.C, 8), 256), 16384);
+    void* args[] = {&problem};
+    const void* join = type == GEMM_INPUT_BF16 ? reinterpret_cast<const void*>(linear_join_kernel<kInputBf16>)
+                                               : reinterpret_cast<const void*>(linear_join_kernel<kInputF16>);
+    return hipLaunchKernel(join, dim3((unsigned)blocks), dim3(256), args, 0, stream);
+}
+
+// ---- gemm_linear ----------------------------------------------------------------------
+bool copies_fit(LinearTile tile, const Matrix& a, bool a_kmajor, const Matrix& b, bool b_kmajor) {
+    // OperandCopy::fits of the tile's rows: offsets within a tile below 2^31
+    const TileSize size = kTileSizes[tile];
+    const auto fits = [](int64_t ld, int64_t rows, int64_t cols) { return ld <= 0x7fffffff / (2 * rows) - cols; };
+    return fits(a.ld, a_kmajor ? size.bm : kTileDepth, a_kmajor ? kTileDepth : size.bm) &&
+           fits(b.ld, b_kmajor ? size.bn : kTileDepth, b_kmajor ? kTileDepth : size.bn);
+}
+
+// 16-byte copies of both operands: rows and widths in whole 16 bytes, and
+// offsets inside a tile that fit whatever tile is chosen.
+bool direct_ok(const Matrix& a, bool a_kmajor, const Matrix& b, bool b_kmajor) {
+    return a.aligned16() && b.aligned16() && a.cols % 8 == 0 && b.cols % 8 == 0 &&
+           copies_fit(kTile256, a, a_kmajor, b, b_kmajor);
+}
+
+struct LinearCall {
+    Matrix A, B, bias, residual, preact, out;
+    int64_t groups;
+    int axis;
+};
+
+int describe(const gemm_linear_args& a, LinearCall* c) {
+    if (!known_type(a.input_type) || !known_output(a.output_type) || !known_act(a.activation)) return GEMM_ERR_UNSUPPORTED;
+    if (a.variant < 0 || a.variant >= GEMM_LINEAR_COUNT) return GEMM_ERR_UNSUPPORTED;
+    if (a.M < 0 || a.N < 0 || a.K < 0 || a.M > kMaxDim || a.N > kMaxDim || a.K > kMaxDim) return GEMM_ERR_INVALID_DIM;
+    if (a.groups < 0 || a.groups > GEMM_LINEAR_MAX_GROUPS || a.splits < 0 || a.splits > kMaxSlices) return GEMM_ERR_INVALID_DIM;
+    if (a.groups > 0 && a.M > 0x7fffffff) return GEMM_ERR_TOO_LARGE;
+    c->groups = a.groups > 0 ? a.groups : 1;
+    c->axis = a.groups > 0 ? kGroupRows : kGroupNone;
+    const int64_t out = elem_bytes(a.output_type);
+    c->A = Matrix{a.A, a.M, a.K, a.lda, 2};
+    c->B = Matrix{a.B, a.K, a.N, a.ldb, 2, c->groups, a.b_stride};
+    c->bias = Matrix{a.bias, 1, a.N, std::max<int64_t>(a.N, 1), 2, c->groups, a.bias_stride};
+    c->residual = Matrix{a.residual, a.M, a.N, a.ldr, out};
+    c->preact = Matrix{a.preact, a.M, a.N, a.ldp, 2};
+    c->out = Matrix{a.D, a.M, a.N, a.ldd, out};
+    const bool in_place = c->residual.data && c->residual.same_place(c->out);
+    const Matrix offsets{a.groups > 0 ? a.offsets : nullptr, 1, a.groups + 1, a.groups + 1, 4};
+    const Matrix space{a.workspace, 1, a.workspace_bytes, std::max<int64_t>(a.workspace_bytes, 1), 1};
+    if (a.workspace_bytes < 0) return GEMM_ERR_WORKSPACE;
+    // an empty output: nothing is read
+    const bool work = a.M > 0 && a.N > 0;
+    const Use uses[] = {{c->A, !work, false}, {c->B, !work, false}, {c->bias, true, false},
+                        {in_place ? Matrix{nullptr, 0, 0, 1, 2} : c->residual, true, false}, {c->preact, true, true},
+                        {c->out, !work, true}, {offsets, a.groups == 0 || !work, false}, {space, true, true}};
+    return check_matrices(uses, 8);
+}
+
+Plan plan_linear(const gemm_linear_args& a, const LinearCall& c, int cus) {
+    return choose(a.M, a.N, a.K, c.groups, c.axis, direct_ok(c.A, true, c.B, false), a.variant, a.splits, cus);
+}
+
+int run_linear(const gemm_linear_args& a, hipStream_t stream) {
+    LinearCall c;
+    int st = describe(a, &c);
+    if (st != GEMM_OK) return st;
+    if (a.M == 0 || a.N == 0) return GEMM_OK;
+    int cus = 0;
+    st = current_cus(&cus);
+    if (st != GEMM_OK) return st;
+    const Plan plan = plan_linear(a, c, cus);
+    st = check_grid(plan, a.M, a.N, c.groups, c.axis);
+    if (st != GEMM_OK) return st;
+    const int64_t need = partial_bytes(plan, a.M, a.N);
+    if (need > 0 && (!a.workspace || a.workspace_bytes < need || ((uintptr_t)a.workspace & 3))) return GEMM_ERR_WORKSPACE;
+    LinearProblem p{};
+    p.R = a.M; p.C = a.N; p.L = a.K;
+    p.A = static_cast<const uint16_t*>(a.A); p.lda = a.lda;
+    p.B = static_cast<const uint16_t*>(a.B); p.ldb = a.ldb; p.b_group = a.b_stride;
+    p.offsets = a.offsets; p.groups = (int32_t)c.groups; p.axis = c.axis;
+    p.splits = plan.splits; p.slice = plan.slice; p.partial = static_cast<float*>(a.workspace);
+    p.ep.bias = static_cast<const uint16_t*>(a.bias); p.ep.bias_group = a.bias_stride;
+    p.ep.residual = a.residual; p.ep.ldr = a.ldr;
+    p.ep.preact = static_cast<uint16_t*>(a.preact); p.ep.ldp = a.ldp;
+    p.ep.out = a.D; p.ep.ldo = a.ldd;
+    p.ep.act = a.activation; p.ep.out_f32 = a.output_type == GEMM_OUTPUT_F32;
+    return launch(a.input_type, p, kForward, plan, stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+}
+
+// ---- gemm_linear_grad -------------------------------------------------------------------
+struct GradCall {
+    Matrix dY, Z, A, B, dZ, dA, dB, dbias;
+    int64_t groups;
+    int axis;
+    Matrix slope() const { return dZ.data ? dZ : dY; }  // what the products read
+};
+
+int describe(const gemm_linear_grad_args& a, GradCall* c) {
+    if (!known_type(a.input_type) || !known_act(a.activation)) return GEMM_ERR_UNSUPPORTED;
+    if (!known_output(a.a_grad_type) || !known_output(a.b_grad_type)) return GEMM_ERR_UNSUPPORTED;
+    if (a.M < 0 || a.N < 0 || a.K < 0 || a.M > kMaxDim || a.N > kMaxDim || a.K > kMaxDim) return GEMM_ERR_INVALID_DIM;
+    if (a.groups < 0 || a.groups > GEMM_LINEAR_MAX_GROUPS) return GEMM_ERR_INVALID_DIM;
+    if (a.groups > 0 && a.M > 0x7fffffff) return GEMM_ERR_TOO_LARGE;
+    c->groups = a.groups > 0 ? a.groups : 1;
+    c->axis = a.groups > 0 ? kGroupRows : kGroupNone;
+    const bool act = a.activation != GEMM_ACT_NONE;
+    c->dY = Matrix{a.dY, a.M, a.N, a.ldy, 2};
+    c->Z = Matrix{act ? a.Z : nullptr, a.M, a.N, a.ldz, 2};
+    c->dZ = Matrix{act ? a.dZ : nullptr, a.M, a.N, a.lddz, 2};
+    c->A = Matrix{a.dB ? a.A : nullptr, a.M, a.K, a.lda, 2};
+    c->B = Matrix{a.dA ? a.B : nullptr, a.K, a.N, a.ldb, 2, c->groups, a.b_stride};
+    c->dA = Matrix{a.dA, a.M, a.K, a.ldda, elem_bytes(a.a_grad_type)};
+    c->dB = Matrix{a.dB, a.K, a.N, a.lddb, elem_bytes(a.b_grad_type), c->groups, a.db_stride};
+    c->dbias = Matrix{a.dbias, c->groups, a.N, std::max<int64_t>(a.N, 1), 4};
+    const Matrix offsets{a.groups > 0 ? a.offsets : nullptr, 1, a.groups + 1, a.groups + 1, 4};
+    if (a.workspace_bytes < 0) return GEMM_ERR_WORKSPACE;
+    const Matrix space{a.workspace, 1, a.workspace_bytes, std::max<int64_t>(a.workspace_bytes, 1), 1};
+    const bool in_place = c->dZ.data && c->dZ.same_place(c->dY);  // dZ may overwrite dY
+    const Use uses[] = {{c->dY, false, false}, {c->Z, !act, false},
+                        {in_place ? Matrix{nullptr, 0, 0, 1, 2} : c->dZ, !act || in_place, true},
+                        {c->A, !a.dB, false}, {c->B, !a.dA, false}, {c->dA, true, true}, {c->dB, true, true},
+                        {c->dbias, true, true}, {offsets, a.groups == 0, false}, {space, true, true}};
+    return check_matrices(uses, 10);
+}
+
+Plan plan_a(const gemm_linear_grad_args& a, const GradCall& c, int cus) {
+    return choose(a.M, a.K, a.N, c.groups, c.axis, direct_ok(c.slope(), true, c.B, true), GEMM_LINEAR_AUTO, 0, cus);
+}
+Plan plan_b(const gemm_linear_grad_args& a, const GradCall& c, int cus) {
+    return choose(a.K, a.N, a.M, c.groups, c.axis == kGroupRows ? kGroupContraction : kGroupNone,
+                  direct_ok(c.A, false, c.slope(), false), GEMM_LINEAR_AUTO, 0, cus);
+}
+int64_t slope_chunks(const gemm_linear_grad_args& a, const GradCall& c) {
+    return row_tiles(a.M, c.groups, c.axis, kSlopeRows);
+}
+
+// The workspace holds the column sums' chunks first and each product's
+// slices after them, one use at a time (the launches run in stream order).
+int64_t grad_workspace(const gemm_linear_grad_args& a, const GradCall& c, int cus) {
+    int64_t need = a.dbias ? slope_chunks(a, c) * a.N * 4 : 0;
+    if (a.dA) need = std::max(need, partial_bytes(plan_a(a, c, cus), a.M, a.K));
+    if (a.dB) need = std::max(need, partial_bytes(plan_b(a, c, cus), a.K, a.N));
+    return need;
+}
+
+int run_slope(const gemm_linear_grad_args& a, const GradCall& c, hipStream_t stream) {
+    SlopeProblem p{};
+    p.M = a.M; p.N = a.N;
+    p.dY = static_cast<const uint16_t*>(a.dY); p.ldy = a.ldy;
+    p.Z = static_cast<const uint16_t*>(c.Z.data); p.ldz = a.ldz;
+    p.dZ = static_cast<uint16_t*>(const_cast<void*>(c.dZ.data)); p.lddz = a.lddz;
+    p.partial = a.dbias ? static_cast<float*>(a.workspace) : nullptr;
+    p.offsets = a.groups > 0 ? a.offsets : nullptr; p.groups = (int32_t)c.groups;
+    p.act = a.activation; p.dbias = a.dbias;
+    void* args[] = {&p};
+    const int64_t chunks = slope_chunks(a, c);
+    if ((p.dZ || p.partial) && chunks > 0) {
+        const void* kernel = a.input_type == GEMM_INPUT_BF16
+                                 ? reinterpret_cast<const void*>(linear_slope_kernel<kInputBf16>)
+                                 : reinterpret_cast<const void*>(linear_slope_kernel<kInputF16>);
+        if (hipLaunchKernel(kernel, dim3((unsigned)chunks, (unsigned)ceil_div(a.N, 256)), dim3(256), args, 0, stream) !=
+            hipSuccess)
+            return GEMM_ERR_HIP;
+    }
+    if (!a.dbias) return GEMM_OK;
+    return hipLaunchKernel(reinterpret_cast<const void*>(linear_bias_join_kernel),
+                           dim3((unsigned)ceil_div(a.N, 64), (unsigned)c.groups), dim3(256), args, 0, stream) == hipSuccess
+               ? GEMM_OK
+               : GEMM_ERR_HIP;
+}
+
+int run_grad(const gemm_linear_grad_args& a, hipStream_t stream) {
+    GradCall c;
+    int st = describe(a, &c);
+    if (st != GEMM_OK) return st;
+    int cus = 0;
+    st = current_cus(&cus);
+    if (st != GEMM_OK) return st;
+    const int64_t need = grad_workspace(a, c, cus);
+    if (need > 0 && (!a.workspace || a.workspace_bytes < need || ((uintptr_t)a.workspace & 3))) return GEMM_ERR_WORKSPACE;
+    const Plan pa = plan_a(a, c, cus), pb = plan_b(a, c, cus);
+    const int axis_b = c.axis == kGroupRows ? kGroupContraction : kGroupNone;
+    if (a.dA && (st = check_grid(pa, a.M, a.K, c.groups, c.axis)) != GEMM_OK) return st;
+    if (a.dB && (st = check_grid(pb, a.K, a.N, c.groups, axis_b)) != GEMM_OK) return st;
+    if (slope_chunks(a, c) > kMaxGrid / 256 || a.N > (int64_t)0xffff * 64) return GEMM_ERR_TOO_LARGE;
+    if (a.N > 0 && (c.dZ.data || a.dbias) && (st = run_slope(a, c, stream)) != GEMM_OK) return st;
+    const Matrix dz = c.slope();
+    LinearProblem p{};
+    p.offsets = a.offsets; p.groups = (int32_t)c.groups;
+    p.partial = static_cast<float*>(a.workspace);
+    if (a.dA && a.M > 0 && a.K > 0) {
+        p.R = a.M; p.C = a.K; p.L = a.N; p.axis = c.axis;
+        p.A = static_cast<const uint16_t*>(dz.data); p.lda = dz.ld;
+        p.B = static_cast<const uint16_t*>(a.B); p.ldb = a.ldb; p.b_group = a.b_stride;
+        p.splits = pa.splits; p.slice = pa.slice;
+        p.ep = LinearEpilogue{};
+        p.ep.out = a.dA; p.ep.ldo = a.ldda; p.ep.out_f32 = a.a_grad_type == GEMM_OUTPUT_F32;
+        if (launch(a.input_type, p, kGradA, pa, stream) != hipSuccess) return GEMM_ERR_HIP;
+    }
+    if (a.dB && a.K > 0 && a.N > 0) {
+        p.R = a.K; p.C = a.N; p.L = a.M; p.axis = axis_b;
+        p.A = static_cast<const uint16_t*>(a.A); p.lda = a.lda;
+        p.B = static_cast<const uint16_t*>(dz.data); p.ldb = dz.ld; p.b_group = 0;
+        p.splits = pb.splits; p.slice = pb.slice;
+        p.ep = LinearEpilogue{};
+        p.ep.out = a.dB; p.ep.ldo = a.lddb; p.ep.out_group = a.db_stride; p.ep.out_f32 = a.b_grad_type == GEMM_OUTPUT_F32;
+        if (launch(a.input_type, p, kGradB, pb, stream) != hipSuccess) return GEMM_ERR_HIP;
+    }
+    return GEMM_OK;
+}
+
+// ---- the token sort ---------------------------------------------------------------------
+int64_t sort_workgroups(int64_t pairs) { return ceil_div(pairs, kSortPairs); }
+int64_t sort_workspace(int64_t pairs, int64_t experts) {
+    return sort_workgroups(pairs) > 1 ? sort_workgroups(pairs) * experts * 4 : 0;
+}
+
+int launch_sort(const SortProblem& problem, int64_t workgroups, hipStream_t stream) {
+    SortProblem p = problem;
+    void* args[] = {&p, &workgroups};
+    const dim3 one(1), all((unsigned)std::max<int64_t>(workgroups, 1)), threads(kSortThreads);
+    hipError_t e;
+    if (workgroups <= 1) {
+        e = hipLaunchKernel(reinterpret_cast<const void*>(expert_sort_small_kernel), one, threads, args, 0, stream);
+    } else {
+        e = hipLaunchKernel(reinterpret_cast<const void*>(expert_count_kernel), all, threads, args, 0, stream);
+        if (e == hipSuccess)
+            e = hipLaunchKernel(reinterpret_cast<const void*>(expert_offsets_kernel), one, threads, args, 0, stream);
+        if (e == hipSuccess)
+            e = hipLaunchKernel(reinterpret_cast<const void*>(expert_place_kernel), all, threads, args, 0, stream);
+    }
+    return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+}
+
+// Sizes shared by the row operators; token and sorted rows.
+int check_rows(int input_type, int64_t tokens, int64_t rows, int32_t top_k, int64_t cols) {
+    if (!known_type(input_type)) return GEMM_ERR_UNSUPPORTED;
+    if (tokens < 0 || rows < 0 || cols < 0 || top_k < 1 || top_k > GEMM_EXPERT_MAX_CHOICES) return GEMM_ERR_INVALID_DIM;
+    if (tokens > 0x7fffffff / top_k || rows > 0x7fffffff || cols > (int64_t)0xffff * kRowCols) return GEMM_ERR_TOO_LARGE;
+    return GEMM_OK;
+}
+
+int launch_rows(const void* kernel, const RowsProblem& problem, bool per_token, hipStream_t stream) {
+    int cus = 0;
+    const int st = current_cus(&cus);
+    if (st != GEMM_OK) return st;
+    RowsProblem p = problem;
+    void* args[] = {&p};
+    const dim3 grid(per_token ? (unsigned)p.tokens : (unsigned)ceil_div(p.tokens, kRowWaves),
+                    per_token ? 1 : (unsigned)ceil_div(p.cols, kRowCols));
+    return hipLaunchKernel(kernel, grid, dim3(kRowWaves * kWave), args, 0, stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+}
+
+}  // namespace
+
+// ---- exported C ABI ---------------------------------------------------------------------
+extern "C" {
+
+int gemm_linear(const gemm_linear_args* args, void* stream) {
+    return args ? run_linear(*args, (hipStream_t)stream) : GEMM_ERR_NULL;
+}
+
+int64_t gemm_linear_workspace_bytes(const gemm_linear_args* args, int32_t num_cus) {
+    if (!args) return GEMM_ERR_NULL;
+    if (num_cus < 1) return GEMM_ERR_INVALID_DIM;
+    gemm_linear_args a = *args;
+    a.workspace = nullptr;
+    a.workspace_bytes = 0;
+    LinearCall c;
+    const int st = describe(a, &c);
+    if (st != GEMM_OK) return st;
+    return a.M == 0 || a.N == 0 ? 0 : partial_bytes(plan_linear(a, c, num_cus), a.M, a.N);
+}
+
+int gemm_linear_choice(const gemm_linear_args* args, int32_t num_cus, int32_t* variant, int32_t* splits) {
+    if (!args || !variant || !splits) return GEMM_ERR_NULL;
+    if (num_cus < 1) return GEMM_ERR_INVALID_DIM;
+    LinearCall c;
+    const int st = describe(*args, &c);
+    if (st != GEMM_OK) return st;
+    const Plan plan = plan_linear(*args, c, num_cus);
+    *variant = plan.tile + 1;
+    *splits = plan.splits;
+    return GEMM_OK;
+}
+
+int gemm_linear_grad(const gemm_linear_grad_args* args, void* stream) {
+    return args ? run_grad(*args, (hipStream_t)stream) : GEMM_ERR_NULL;
+}
+
+int64_t gemm_linear_grad_workspace_bytes(const gemm_linear_grad_args* args, int32_t num_cus) {
+    if (!args) return GEMM_ERR_NULL;
+    if (num_cus < 1) return GEMM_ERR_INVALID_DIM;
+    gemm_linear_grad_args a = *args;
+    a.workspace = nullptr;
+    a.workspace_bytes = 0;
+    GradCall c;
+    const int st = describe(a, &c);
+    return st != GEMM_OK ? st : grad_workspace(a, c, num_cus);
+}
+
+int64_t gemm_expert_sort_workspace_bytes(int64_t tokens, int32_t top_k, int32_t num_experts) {
+    if (tokens < 0 || top_k < 1 || top_k > GEMM_EXPERT_MAX_CHOICES || num_experts < 1 || num_experts > kMaxExperts)
+        return GEMM_ERR_INVALID_DIM;
+    if (tokens > 0x7fffffff / top_k) return GEMM_ERR_TOO_LARGE;
+    return sort_workspace(tokens * top_k, num_experts);
+}
+
+int gemm_expert_sort(int64_t tokens, int32_t top_k, int32_t num_experts, const int32_t* experts, int32_t* offsets,
+                     int32_t* order, int32_t* position, void* workspace, int64_t workspace_bytes, void* stream) {
+    const int64_t need = gemm_expert_sort_workspace_bytes(tokens, top_k, num_experts);
+    if (need < 0) return (int)need;
+    const int64_t pairs = tokens * top_k;
+    if (workspace_bytes < 0) return GEMM_ERR_WORKSPACE;
+    const auto list = [](const void* p, int64_t n) { return Matrix{p, 1, n, std::max<int64_t>(n, 1), 4}; };
+    const Use uses[] = {{list(experts, pairs), false, false}, {list(offsets, num_experts + 1), false, true},
+                        {list(order, pairs), false, true}, {list(position, pairs), false, true},
+                        {list(workspace, workspace_bytes / 4), true, true}};
+    int st = check_matrices(uses, 5);
+    if (st != GEMM_OK) return st;
+    if (need > 0 && (!workspace || workspace_bytes < need || ((uintptr_t)workspace & 3))) return GEMM_ERR_WORKSPACE;
+    int cus = 0;
+    st = current_cus(&cus);
+    if (st != GEMM_OK) return st;
+    return launch_sort(SortProblem{experts, pairs, num_experts, offsets, order, position, static_cast<int32_t*>(workspace)},
+                       sort_workgroups(pairs), (hipStream_t)stream);
+}
+
+int gemm_expert_gather(int input_type, int64_t tokens, int64_t rows, int32_t top_k, int64_t cols, const void* X,
+                       int64_t ldx, const int32_t* position, void* sorted, int64_t lds, void* stream) {
+    int st = check_rows(input_type, tokens, rows, top_k, cols);
+    if (st != GEMM_OK) return st;
+    const bool work = tokens > 0 && rows > 0 && cols > 0;
+    const Use uses[] = {{Matrix{X, tokens, cols, ldx, 2}, !work, false},
+                        {Matrix{position, 1, tokens * top_k, std::max<int64_t>(tokens * top_k, 1), 4}, !work, false},
+                        {Matrix{sorted, rows, cols, lds, 2}, !work, true}};
+    st = check_matrices(uses, 3);
+    if (st != GEMM_OK || !work) return st;
+    RowsProblem p{};
+    p.tokens = tokens; p.rows = rows; p.cols = cols; p.top_k = top_k; p.position = position;
+    p.x = static_cast<const uint16_t*>(X); p.ldx = ldx;
+    p.sorted = static_cast<uint16_t*>(sorted); p.lds = lds;
+    return launch_rows(reinterpret_cast<const void*>(expert_gather_kernel), p, false, (hipStream_t)stream);
+}
+
+int gemm_expert_combine(int input_type, int64_t tokens, int64_t rows, int32_t top_k, int64_t cols, const void* Y,
+                        int64_t ldy, const int32_t* position, const float* weights, void* out, int64_t ldo,
+                        void* stream) {
+    int st = check_rows(input_type, tokens, rows, top_k, cols);
+    if (st != GEMM_OK) return st;
+    const bool work = tokens > 0 && cols > 0;
+    const int64_t pairs = tokens * top_k, width = std::max<int64_t>(pairs, 1);
+    const Use uses[] = {{Matrix{Y, rows, cols, ldy, 2}, !work, false},
+                        {Matrix{position, 1, pairs, width, 4}, !work, false},
+                        {Matrix{weights, 1, pairs, width, 4}, true, false},
+                        {Matrix{out, tokens, cols, ldo, 2}, !work, true}};
+    st = check_matrices(uses, 4);
+    if (st != GEMM_OK || !work) return st;
+    RowsProblem p{};
+    p.tokens = tokens; p.rows = rows; p.cols = cols; p.top_k = top_k; p.position = position; p.weights = weights;
+    p.y = static_cast<const uint16_t*>(Y); p.ldy = ldy;
+    p.out = static_cast<uint16_t*>(out); p.ldo = ldo;
+    return launch_rows(input_type == GEMM_INPUT_BF16 ? reinterpret_cast<const void*>(expert_combine_kernel<kInputBf16>)
+                                                     : reinterpret_cast<const void*>(expert_combine_kernel<kInputF16>),
+                       p, false, (hipStream_t)stream);
+}
+
+int gemm_expert_combine_grad(int input_type, int64_t tokens, int64_t rows, int32_t top_k, int64_t cols,
+                             const void* dout, int64_t ldd, const void* Y, int64_t ldy, const int32_t* position,
+                             const float* weights, void* dY, int64_t lddy, float* dweights, void* stream) {
+    int st = check_rows(input_type, tokens, rows, top_k, cols);
+    if (st != GEMM_OK) return st;
+    const bool work = tokens > 0;
+    const int64_t pairs = tokens * top_k, width = std::max<int64_t>(pairs, 1);
+    const Use uses[] = {{Matrix{dout, tokens, cols, ldd, 2}, !work, false},
+                        {Matrix{dweights ? Y : nullptr, rows, cols, ldy, 2}, !work || !dweights, false},
+                        {Matrix{position, 1, pairs, width, 4}, !work, false},
+                        {Matrix{weights, 1, pairs, width, 4}, true, false},
+                        {Matrix{dY, rows, cols, lddy, 2}, true, true},
+                        {Matrix{dweights, 1, pairs, width, 4}, true, true}};
+    st = check_matrices(uses, 6);
+    if (st != GEMM_OK || !work || (!dY && !dweights)) return st;
+    RowsProblem p{};
+    p.tokens = tokens; p.rows = rows; p.cols = cols; p.top_k = top_k; p.position = position; p.weights = weights;
+    p.x = static_cast<const uint16_t*>(dout); p.ldx = ldd;
+    p.y = static_cast<const uint16_t*>(Y); p.ldy = ldy;
+    p.sorted = static_cast<uint16_t*>(dY); p.lds = lddy;
+    p.dweights = dweights;
+    return launch_rows(input_type == GEMM_INPUT_BF16
+                           ? reinterpret_cast<const void*>(expert_combine_grad_kernel<kInputBf16>)
+                           : reinterpret_cast<const void*>(expert_combine_grad_kernel<kInputF16>),
+                       p, true, (hipStream_t)stream);
+}
+
+}  // extern "C"

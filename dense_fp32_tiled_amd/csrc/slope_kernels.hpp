@@ -1,0 +1,108 @@
+// slope_kernels.hpp -- gfx950 kernels of the epilogue's gradient.
+//
+// dZ = dY act'(Z), rounded to 16 bits for the two products that read it, and
+// the column sums of the unrounded values (dbias): each workgroup sums a
+// chunk of kSlopeRows rows of one group over 256 columns into
+// partial[chunk][column]; linear_bias_join_kernel adds a group's chunks in
+// ascending order.  Bound by bytes: dY and Z read once, dZ written once.
+#pragma once
+
+#include "linear_kernels.hpp"
+
+namespace dft {
+
+constexpr int kSlopeRows = 64;
+
+struct SlopeProblem {
+    int64_t M, N;
+    const uint16_t* dY;
+    int64_t ldy;
+    const uint16_t* Z;
+    int64_t ldz;
+    uint16_t* dZ;                // nullptr: the sums alone (no activation)
+    int64_t lddz;
+    float* partial;              // nullptr: no sums wanted
+    const int32_t* offsets;
+    int32_t groups;
+    int32_t act;
+    float* dbias;                // groups x N, rows N apart
+};
+
+template <int TYPE>
+__global__ __launch_bounds__(256) void linear_slope_kernel(SlopeProblem p) {
+    __shared__ float sums[8][256 + 8];
+    const int c = threadIdx.x % 32, r = threadIdx.x / 32;
+    const int64_t chunk = blockIdx.x, col = (int64_t)blockIdx.y * 256 + c * 8, left = p.N - col;
+    int64_t lo = chunk * kSlopeRows, hi = p.M;
+    if (p.offsets) {
+        const GroupTile gt = find_group_tile(p.offsets, p.groups, p.M, kSlopeRows, chunk);
+        if (gt.group < 0) return;
+        lo = gt.row0;
+        hi = gt.row_end;
+    }
+    if (hi > lo + kSlopeRows) hi = lo + kSlopeRows;
+    float sum[8] = {};
+    if (left > 0) {
+        for (int64_t row = lo + r; row < hi; row += 8) {
+            const Row8 dy = load8(p.dY + row * p.ldy + col, left);
+            float d[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] = widen<TYPE>(dy.v[e]);
+            if (p.dZ) {
+                const Row8 z = load8(p.Z + row * p.ldz + col, left);
+                Row8 out;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    d[e] *= act_slope(widen<TYPE>(z.v[e]), p.act);
+                    out.v[e] = narrow<TYPE>(d[e]);
+                }
+                store8(p.dZ + row * p.lddz + col, out, left);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += d[e];
+        }
+    }
+    if (!p.partial) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[r][c * 8 + e] = sum[e];
+    __syncthreads();
+    const int64_t at = (int64_t)blockIdx.y * 256 + threadIdx.x;
+    if (at < p.N) {
+        float total = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) total += sums[k][threadIdx.x];
+        p.partial[chunk * p.N + at] = total;
+    }
+}
+
+// dbias[group][column] over that group's chunks: 64 columns by 4 strides of
+// chunks per workgroup.
+__global__ __launch_bounds__(256) void linear_bias_join_kernel(SlopeProblem p) {
+    __shared__ float sums[4][64];
+    const int c = threadIdx.x % 64, r = threadIdx.x / 64;
+    const int64_t col = (int64_t)blockIdx.x * 64 + c;
+    const int group = blockIdx.y;
+    int64_t first = 0, rows = p.M;
+    if (p.offsets) {
+        // chunks of the groups before this one, by the same rule as find_group_tile
+        int64_t before = 0;
+        for (int g = c; g < group; g += 64) {
+            const RowRange range = group_rows(p.offsets, g, p.M);
+            before += (range.hi - range.lo + kSlopeRows - 1) / kSlopeRows;
+        }
+#pragma unroll
+        for (int d = 32; d > 0; d /= 2) before += __shfl_xor((int)before, d);
+        first = before;
+        const RowRange own = group_rows(p.offsets, group, p.M);
+        rows = own.hi - own.lo;
+    }
+    const int64_t chunks = (rows + kSlopeRows - 1) / kSlopeRows;
+    float sum = 0.0f;
+    if (col < p.N)
+        for (int64_t k = r; k < chunks; k += 4) sum += p.partial[(first + k) * p.N + col];
+    sums[r][c] = sum;
+    __syncthreads();
+    if (r == 0 && col < p.N) p.dbias[group * p.N + col] = sums[0][c] + sums[1][c] + sums[2][c] + sums[3][c];
+}
+
+}  // namespace dft

@@ -441,6 +441,164 @@ int gemm_mixed_tile_config(int variant, gemm_tile_config *out);
  * GEMM_ERR_INVALID_DIM for negative sizes or num_cus < 1. */
 int gemm_mixed_auto_variant(int64_t M, int64_t N, int64_t K, int32_t num_cus);
 
+/* ---- Products with an epilogue, and their gradients ---------------------------
+ * The layer of a model around the product: with A, B of `input_type` and sums
+ * in fp32,
+ *     Z = A @ B + bias          (bias per column, of the input type; optional)
+ *     D = act(Z) + residual     (residual of D's type; optional)
+ * for one B, or for one B per group of A's rows (the experts of a routed
+ * layer): group g covers rows [offsets[g], offsets[g+1]).  Nothing is rounded
+ * before D is stored; Z is stored as well, rounded to the input type, when
+ * `preact` is given (the gradients read it).
+ *
+ * Gradients, from dY = the gradient of D (of the residual too, unchanged):
+ *     dZ = dY * act'(Z)         rounded to the input type: what the products read
+ *     dA = dZ @ B^T,  dB = A^T @ dZ (per group),  dbias = column sums of dY * act'(Z) (per group, fp32, unrounded)
+ *
+ * Conventions are those at the top of this header, and:
+ *   - `offsets` is read on the device: groups + 1 ascending row numbers.  Rows
+ *     before the first and from the last on belong to no group: their D, Z
+ *     and dA are left as they were and they add nothing to dB and dbias.  An
+ *     empty group's dB and dbias are zero.  Values outside [0, M], or smaller
+ *     than one before them, are taken as the nearest ones that are not.
+ *   - D may be the residual itself (same address and pitch), and dZ may be dY;
+ *     no other output may overlap any operand (GEMM_ERR_ALIAS).
+ *   - K == 0 gives Z = bias; M == 0 gives dB = 0 and dbias = 0; N == 0 gives dA = 0.
+ *   - The activations' limits hold for large |Z|: no infinite intermediate
+ *     makes a NaN of a finite Z. */
+typedef enum {
+    GEMM_ACT_NONE = 0,
+    GEMM_ACT_RELU = 1,       /* max(z, 0); slope 0 at 0 */
+    GEMM_ACT_GELU = 2,       /* z (1 + erf(z / sqrt 2)) / 2 */
+    GEMM_ACT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+    GEMM_ACT_SILU = 4        /* z / (1 + exp(-z)) */
+} gemm_activation;
+
+typedef enum {
+    GEMM_OUTPUT_SAME = 0,  /* the input type */
+    GEMM_OUTPUT_F32 = 1
+} gemm_output_type;
+
+/* Workgroup tiles (AUTO picks one and a number of slices of K from the sizes;
+ * gemm_linear_choice).  Operands whose address, pitch or width is not a
+ * multiple of 16 bytes go through registers, with 128x128 in place of
+ * 256x256. */
+typedef enum {
+    GEMM_LINEAR_AUTO = 0,
+    GEMM_LINEAR_256x256 = 1,
+    GEMM_LINEAR_128x128 = 2,
+    GEMM_LINEAR_64x64 = 3,
+    GEMM_LINEAR_32x128 = 4,  /* few rows: B is streamed through four stages */
+    GEMM_LINEAR_COUNT = 5
+} gemm_linear_variant;
+
+enum { GEMM_LINEAR_MAX_GROUPS = 65535, GEMM_EXPERT_MAX_CHOICES = 64 };
+
+typedef struct {
+    int32_t input_type;   /* gemm_input_type of A, B, bias and preact */
+    int32_t output_type;  /* gemm_output_type of D and residual */
+    int32_t activation;   /* gemm_activation */
+    int32_t variant;      /* gemm_linear_variant */
+    int32_t splits;       /* slices of K joined in ascending order: 0 automatic, 1..32 (1 with groups) */
+    int32_t groups;       /* 0: one B */
+    int64_t M, N, K;
+    const void *A;
+    int64_t lda;
+    const void *B;            /* group g's at B + g * b_stride elements */
+    int64_t ldb, b_stride;
+    const void *bias;         /* N values, group g's at bias + g * bias_stride; or NULL */
+    int64_t bias_stride;
+    const int32_t *offsets;   /* DEVICE, groups + 1 values; ignored when groups is 0 */
+    const void *residual;     /* M x N, or NULL */
+    int64_t ldr;
+    void *preact;             /* M x N, or NULL */
+    int64_t ldp;
+    void *D;                  /* M x N */
+    int64_t ldd;
+    void *workspace;          /* DEVICE, 4-byte aligned; may be NULL when gemm_linear_workspace_bytes is 0 */
+    int64_t workspace_bytes;
+} gemm_linear_args;
+
+/* Z, D as above, enqueued on `stream`.  Returns a gemm_status. */
+int gemm_linear(const gemm_linear_args *args, void *stream);
+
+/* Bytes gemm_linear needs for these arguments (workspace fields ignored) on a
+ * device with num_cus compute units: the slices' partial products, splits * M
+ * * N * 4, or 0.  Pure host call; a negative gemm_status on bad arguments. */
+int64_t gemm_linear_workspace_bytes(const gemm_linear_args *args, int32_t num_cus);
+
+/* The tile and the number of slices gemm_linear runs these arguments with.
+ * Pure host call. */
+int gemm_linear_choice(const gemm_linear_args *args, int32_t num_cus, int32_t *variant, int32_t *splits);
+
+typedef struct {
+    int32_t input_type;   /* of dY, Z, A, B and dZ */
+    int32_t activation;
+    int32_t a_grad_type;  /* gemm_output_type of dA */
+    int32_t b_grad_type;  /* gemm_output_type of dB */
+    int32_t groups;
+    int64_t M, N, K;
+    const int32_t *offsets;
+    const void *dY;       /* M x N */
+    int64_t ldy;
+    const void *Z;        /* M x N: the forward pass's preact; ignored without an activation */
+    int64_t ldz;
+    const void *A;        /* M x K; ignored when dB is NULL */
+    int64_t lda;
+    const void *B;        /* K x N per group; ignored when dA is NULL */
+    int64_t ldb, b_stride;
+    void *dZ;             /* M x N, needed with an activation; else ignored (dZ is dY) */
+    int64_t lddz;
+    void *dA;             /* M x K, or NULL: not wanted */
+    int64_t ldda;
+    void *dB;             /* K x N per group, or NULL */
+    int64_t lddb, db_stride;
+    float *dbias;         /* groups x N packed, or NULL */
+    void *workspace;
+    int64_t workspace_bytes;
+} gemm_linear_grad_args;
+
+/* The gradients above, enqueued on `stream`.  Sums run in a fixed order: the
+ * same inputs give the same bits.  Returns a gemm_status. */
+int gemm_linear_grad(const gemm_linear_grad_args *args, void *stream);
+
+/* Bytes gemm_linear_grad needs, as gemm_linear_workspace_bytes. */
+int64_t gemm_linear_grad_workspace_bytes(const gemm_linear_grad_args *args, int32_t num_cus);
+
+/* ---- Tokens sorted by expert and back --------------------------------------------
+ * A router gives each of `tokens` tokens top_k experts (1..64).  The sort puts
+ * the tokens * top_k pairs in expert order, pairs of one expert staying in
+ * token order:
+ *     offsets[e]                    first sorted row of expert e; offsets[num_experts]: rows in all
+ *     order[s]                      pair (token * top_k + choice) of sorted row s; -1 from offsets[num_experts] on
+ *     position[token * top_k + j]   sorted row of that pair; -1 when its expert is outside [0, num_experts) (dropped)
+ * num_experts is 1..1024.  All arrays are on the device; workspace as
+ * gemm_expert_sort_workspace_bytes says (0 up to 4096 pairs). */
+int gemm_expert_sort(int64_t tokens, int32_t top_k, int32_t num_experts, const int32_t *experts, int32_t *offsets,
+                     int32_t *order, int32_t *position, void *workspace, int64_t workspace_bytes, void *stream);
+int64_t gemm_expert_sort_workspace_bytes(int64_t tokens, int32_t top_k, int32_t num_experts);
+
+/* sorted[position[t][j]] = X[t], `rows` sorted rows of `cols` 16-bit values.
+ * Rows that no pair has are left as they were.  A position outside [0, rows)
+ * counts as dropped, here and below. */
+int gemm_expert_gather(int input_type, int64_t tokens, int64_t rows, int32_t top_k, int64_t cols, const void *X,
+                       int64_t ldx, const int32_t *position, void *sorted, int64_t lds, void *stream);
+
+/* out[t] = sum over j of weights[t][j] * Y[position[t][j]], summed in fp32 in
+ * ascending j and rounded once; weights NULL: ones (the gather's gradient).
+ * A token whose choices are all dropped gets zeros. */
+int gemm_expert_combine(int input_type, int64_t tokens, int64_t rows, int32_t top_k, int64_t cols, const void *Y,
+                        int64_t ldy, const int32_t *position, const float *weights, void *out, int64_t ldo,
+                        void *stream);
+
+/* dY[position[t][j]] = weights[t][j] * dout[t] and dweights[t][j] = Y[position[t][j]] . dout[t]
+ * (0 when dropped).  Either output may be NULL; Y is read only for dweights.
+ * Rows of dY that no pair has are left as they were.  dout, X, out: tokens x
+ * cols; Y, dY, sorted: rows x cols. */
+int gemm_expert_combine_grad(int input_type, int64_t tokens, int64_t rows, int32_t top_k, int64_t cols,
+                             const void *dout, int64_t ldd, const void *Y, int64_t ldy, const int32_t *position,
+                             const float *weights, void *dY, int64_t lddy, float *dweights, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
