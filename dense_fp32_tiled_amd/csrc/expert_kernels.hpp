@@ -227,14 +227,12 @@ __global__ __launch_bounds__(kRowWaves* kWave) void expert_combine_kernel(RowsPr
         const int64_t s = slot_of(p, token, j);
         if (s < 0) continue;
         const float w = p.weights ? p.weights[token * p.top_k + j] : 1.0f;
-        const Row8 v = load8(p.y + s * p.ldy + col, left);
+        float v[8];
+        load8(p.y + s * p.ldy + col, left).widen<TYPE>(v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += w * widen<TYPE>(v.v[e]);
+        for (int e = 0; e < 8; ++e) sum[e] += w * v[e];
     }
-    Row8 out;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) out.v[e] = narrow<TYPE>(sum[e]);
-    store8(p.out + token * p.ldo + col, out, left);
+    store8(p.out + token * p.ldo + col, Row8::narrow<TYPE>(sum), left);
 }
 
 // One workgroup per token: dy of each of its slots, and each choice's dot product.
@@ -250,16 +248,19 @@ __global__ __launch_bounds__(kRowWaves* kWave) void expert_combine_grad_kernel(R
             const float w = p.weights ? p.weights[pair] : 1.0f;
             for (int64_t col = threadIdx.x * 8; col < p.cols; col += kRowWaves * kRowCols) {
                 const int64_t left = p.cols - col;
-                const Row8 d = load8(p.x + token * p.ldx + col, left);
-                Row8 out;
+                float d[8];
+                load8(p.x + token * p.ldx + col, left).widen<TYPE>(d);
                 if (p.dweights) {
-                    const Row8 v = load8(p.y + s * p.ldy + col, left);
+                    float v[8];
+                    load8(p.y + s * p.ldy + col, left).widen<TYPE>(v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dot += widen<TYPE>(d.v[e]) * widen<TYPE>(v.v[e]);
+                    for (int e = 0; e < 8; ++e) dot += d[e] * v[e];
                 }
+                if (p.sorted) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) out.v[e] = narrow<TYPE>(w * widen<TYPE>(d.v[e]));
-                if (p.sorted) store8(p.sorted + s * p.lds + col, out, left);
+                    for (int e = 0; e < 8; ++e) d[e] *= w;
+                    store8(p.sorted + s * p.lds + col, Row8::narrow<TYPE>(d), left);
+                }
             }
         }
         if (!p.dweights) continue;

@@ -177,19 +177,20 @@ int64_t row_tiles(int64_t R, int64_t groups, int axis, int64_t bm) {
 int check_grid(const Plan& plan, int64_t R, int64_t C, int64_t groups, int axis) {
     const TileSize size = kTileSizes[plan.tile];
     const int64_t tiles_m = row_tiles(R, groups, axis, size.bm), tiles_n = ceil_div(C, size.bn);
-    if (tiles_n > 0 && tiles_m > kMaxGrid / 512 / tiles_n) return GEMM_ERR_TOO_LARGE;
-    if (8 * tiles_n > 0x7fffffff) return GEMM_ERR_TOO_LARGE;
+    const int64_t y = axis == kGroupContraction ? groups : plan.splits;
+    if (tiles_n > 0 && tiles_m > kMaxGrid / 512 / tiles_n / y) return GEMM_ERR_TOO_LARGE;
     return GEMM_OK;
 }
 
-hipError_t launch(int type, const LinearProblem& p, LinearLayout layout, const Plan& plan, hipStream_t stream) {
+hipError_t launch(int type, const LinearProblem& p, LinearLayout layout, const Plan& plan, int cus,
+                  hipStream_t stream) {
     const TileSize size = kTileSizes[plan.tile];
     const uint32_t tiles_m = (uint32_t)row_tiles(p.R, p.groups, p.axis, size.bm), tiles_n = (uint32_t)ceil_div(p.C, size.bn);
     const uint32_t grid_y = p.axis == kGroupContraction ? (uint32_t)p.groups : (uint32_t)plan.splits;
     if (tiles_m == 0 || tiles_n == 0) return hipSuccess;
     const hipError_t e = type == GEMM_INPUT_BF16
-                             ? launch_linear_bf16(p, layout, plan.tile, plan.direct, tiles_m, tiles_n, grid_y, stream)
-                             : launch_linear_f16(p, layout, plan.tile, plan.direct, tiles_m, tiles_n, grid_y, stream);
+                             ? launch_linear_bf16(p, layout, plan.tile, plan.direct, tiles_m, tiles_n, grid_y, cus, stream)
+                             : launch_linear_f16(p, layout, plan.tile, plan.direct, tiles_m, tiles_n, grid_y, cus, stream);
     if (e != hipSuccess || plan.splits <= 1) return e;
     LinearProblem problem = p;
     const int64_t blocks = std::min<int64_t>(ceil_div(p.R * ceil_div(p.C, 8), 256), 16384);
@@ -276,7 +277,7 @@ int run_linear(const gemm_linear_args& a, hipStream_t stream) {
     p.ep.preact = static_cast<uint16_t*>(a.preact); p.ep.ldp = a.ldp;
     p.ep.out = a.D; p.ep.ldo = a.ldd;
     p.ep.act = a.activation; p.ep.out_f32 = a.output_type == GEMM_OUTPUT_F32;
-    return launch(a.input_type, p, kForward, plan, stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
+    return launch(a.input_type, p, kForward, plan, cus, stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }
 
 // ---- gemm_linear_grad -------------------------------------------------------------------
@@ -387,7 +388,7 @@ int run_grad(const gemm_linear_grad_args& a, hipStream_t stream) {
         p.splits = pa.splits; p.slice = pa.slice;
         p.ep = LinearEpilogue{};
         p.ep.out = a.dA; p.ep.ldo = a.ldda; p.ep.out_f32 = a.a_grad_type == GEMM_OUTPUT_F32;
-        if (launch(a.input_type, p, kGradA, pa, stream) != hipSuccess) return GEMM_ERR_HIP;
+        if (launch(a.input_type, p, kGradA, pa, cus, stream) != hipSuccess) return GEMM_ERR_HIP;
     }
     if (a.dB && a.K > 0 && a.N > 0) {
         p.R = a.K; p.C = a.N; p.L = a.M; p.axis = axis_b;
@@ -396,7 +397,7 @@ int run_grad(const gemm_linear_grad_args& a, hipStream_t stream) {
         p.splits = pb.splits; p.slice = pb.slice;
         p.ep = LinearEpilogue{};
         p.ep.out = a.dB; p.ep.ldo = a.lddb; p.ep.out_group = a.db_stride; p.ep.out_f32 = a.b_grad_type == GEMM_OUTPUT_F32;
-        if (launch(a.input_type, p, kGradB, pb, stream) != hipSuccess) return GEMM_ERR_HIP;
+        if (launch(a.input_type, p, kGradB, pb, cus, stream) != hipSuccess) return GEMM_ERR_HIP;
     }
     return GEMM_OK;
 }

@@ -54,13 +54,50 @@ struct LinearProblem {
 };
 
 // ---- activations --------------------------------------------------------------------
+// The epilogue's arithmetic is not small beside its product: 65536 values of
+// a 256x256 tile cost a CU 1024 cycles per instruction (4096 for exp2 and
+// rcp), so these use the hardware's exp2 and reciprocal (one unit in the last
+// place each) and no library functions.
+
+// 1 / (1 + exp(-u)); exp2 overflows to infinity and the reciprocal to 0, the
+// limit, for u below -128.
+__device__ inline float logistic(float u) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * u));
+}
+
+// The normal distribution's upper tail at |z| >= 0, erfc(x) / 2 at x = |z| /
+// sqrt 2, and its density's exponential exp(-x^2): erfc(x) = exp(-x^2) t P(t)
+// with t = 1 / (1 + 0.3 x), P of degree 8 fitted to erfc's own ratio over
+// 0 <= x <= 10 for least relative error (2e-8; 5e-7 as evaluated in fp32).
+__device__ inline float normal_tail(float z, float* density) {
+    const float x = fabsf(z) * 0.70710678118654752f;
+    const float t = __builtin_amdgcn_rcpf(1.0f + 0.3f * x);
+    float q = -0.1295222492f;
+    q = q * t + 0.4855600595f;
+    q = q * t - 0.5122715831f;
+    q = q * t + 0.5477126241f;
+    q = q * t - 0.0946455896f;
+    q = q * t + 0.2149238437f;
+    q = q * t + 0.1483397484f;
+    q = q * t + 0.1707151383f;
+    q = q * t + 0.1691880077f;
+    *density = __builtin_amdgcn_exp2f(-1.4426950408889634f * (x * x));
+    return 0.5f * q * t * *density;
+}
+
+__device__ inline float gelu_tanh_argument(float z) { return 1.5957691216057308f * z * (1.0f + 0.044715f * z * z); }
+
 __device__ inline float act_value(float z, int kind) {
     switch (kind) {
         case kActRelu: return z > 0.0f ? z : 0.0f;
-        case kActGelu: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+        case kActGelu: {
+            float density;
+            const float tail = normal_tail(z, &density);
+            return z * (z < 0.0f ? tail : 1.0f - tail);
+        }
         // (1 + tanh(u)) / 2 is the logistic function of 2 u
-        case kActGeluTanh: return z / (1.0f + expf(-1.5957691216057308f * (z + 0.044715f * z * z * z)));
-        case kActSilu: return z / (1.0f + expf(-z));
+        case kActGeluTanh: return z * logistic(gelu_tanh_argument(z));
+        case kActSilu: return z * logistic(z);
         default: return z;
     }
 }
@@ -70,61 +107,88 @@ __device__ inline float act_slope(float z, int kind) {
     if (kind == kActNone) return 1.0f;
     if (kind == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
     z = z > 128.0f ? 128.0f : z < -128.0f ? -128.0f : z;
-    if (kind == kActGelu)
-        return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+    if (kind == kActGelu) {
+        float density;
+        const float tail = normal_tail(z, &density);
+        return (z < 0.0f ? tail : 1.0f - tail) + z * 0.39894228040143268f * density;
+    }
     float u = z, du = 1.0f;
     if (kind == kActGeluTanh) {
-        u = 1.5957691216057308f * (z + 0.044715f * z * z * z);
+        u = gelu_tanh_argument(z);
         du = 1.5957691216057308f * (1.0f + 0.134145f * z * z);
     }
-    const float gate = 1.0f / (1.0f + expf(-u));
+    const float gate = logistic(u);
     return gate + z * gate * (1.0f - gate) * du;
 }
 
 // ---- 16-bit values ------------------------------------------------------------------
-template <int TYPE>
-__device__ inline float widen(uint16_t v) {
-    if constexpr (TYPE == kInputBf16)
-        return __builtin_bit_cast(float, (uint32_t)v << 16);
-    else
-        return (float)__builtin_bit_cast(_Float16, v);
-}
-// Rounds to nearest, ties to even.
-template <int TYPE>
-__device__ inline uint16_t narrow(float v) {
-    if constexpr (TYPE == kInputBf16)
-        return __builtin_bit_cast(uint16_t, (__bf16)v);
-    else
-        return __builtin_bit_cast(uint16_t, (_Float16)v);
-}
-
-// Eight consecutive 16-bit values, at any 2-byte alignment: one 16-byte
-// access when all are in range, else one access each.
+// Eight consecutive 16-bit values in four words, so that they move as one
+// 16-byte access at any 2-byte alignment.
 struct Row8 {
-    uint16_t v[8];
+    u32x4 w;
+    template <int TYPE>
+    __device__ void widen(float (&v)[8]) const {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (TYPE == kInputBf16) {
+                v[2 * e] = __builtin_bit_cast(float, w[e] << 16);
+                v[2 * e + 1] = __builtin_bit_cast(float, w[e] & 0xffff0000u);
+            } else {
+                v[2 * e] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[e] & 0xffffu));
+                v[2 * e + 1] = (float)__builtin_bit_cast(_Float16, (uint16_t)(w[e] >> 16));
+            }
+        }
+    }
+    // Rounded to nearest, ties to even.
+    template <int TYPE>
+    __device__ static Row8 narrow(const float (&v)[8]) {
+        typedef float pair __attribute__((ext_vector_type(2)));
+        typedef __bf16 bf16_pair __attribute__((ext_vector_type(2)));
+        typedef _Float16 f16_pair __attribute__((ext_vector_type(2)));
+        Row8 r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const pair x{v[2 * e], v[2 * e + 1]};
+            if constexpr (TYPE == kInputBf16)
+                r.w[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16_pair));
+            else
+                r.w[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, f16_pair));
+        }
+        return r;
+    }
 };
+// The first `in_range` of the eight, zeros for the others; one access when all are in range, else one each.
 __device__ inline Row8 load8(const uint16_t* p, int64_t in_range) {
     Row8 r;
     if (in_range >= 8) {
-        __builtin_memcpy(&r, p, sizeof(r));
+        __builtin_memcpy(&r.w, p, sizeof(r.w));
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) r.v[e] = e < in_range ? p[e] : (uint16_t)0;
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = 2 * e < in_range ? p[2 * e] : 0u, hi = 2 * e + 1 < in_range ? p[2 * e + 1] : 0u;
+            r.w[e] = lo | (hi << 16);
+        }
     }
     return r;
 }
 __device__ inline void store8(uint16_t* p, const Row8& r, int64_t in_range) {
     if (in_range >= 8) {
-        __builtin_memcpy(p, &r, sizeof(r));
+        __builtin_memcpy(p, &r.w, sizeof(r.w));
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (e < in_range) p[e] = r.v[e];
+            if (e < in_range) p[e] = (uint16_t)(r.w[e / 2] >> (e % 2 * 16));
     }
 }
 __device__ inline void load8(float (&v)[8], const float* p, int64_t in_range) {
     if (in_range >= 8) {
-        __builtin_memcpy(&v, p, sizeof(v));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            floatx4 x;
+            __builtin_memcpy(&x, p + 4 * h, sizeof(x));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * h + e] = x[e];
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = e < in_range ? p[e] : 0.0f;
@@ -132,7 +196,11 @@ __device__ inline void load8(float (&v)[8], const float* p, int64_t in_range) {
 }
 __device__ inline void store8(float* p, const float (&v)[8], int64_t in_range) {
     if (in_range >= 8) {
-        __builtin_memcpy(p, &v, sizeof(v));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const floatx4 x{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+            __builtin_memcpy(p + 4 * h, &x, sizeof(x));
+        }
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -140,27 +208,31 @@ __device__ inline void store8(float* p, const float (&v)[8], int64_t in_range) {
     }
 }
 
-// The epilogue of eight consecutive columns of one output row: z holds their
-// sums; `left` of them lie inside the matrix.
+// The epilogue of eight consecutive columns of one output row, in two parts
+// so that what it reads can be on its way while earlier columns are finished.
+// `left` of the columns lie inside the matrix.
+__device__ inline Row8 bias_reads(const LinearEpilogue& ep, int64_t group, int64_t col, int64_t left) {
+    return ep.bias ? load8(ep.bias + group * ep.bias_group + col, left) : Row8{};
+}
+__device__ inline Row8 residual_reads(const LinearEpilogue& ep, int64_t row, int64_t col, int64_t left) {
+    if (!ep.residual || ep.out_f32) return Row8{};  // (an fp32 residual is read as it is added)
+    return load8(static_cast<const uint16_t*>(ep.residual) + row * ep.ldr + col, left);
+}
 template <int TYPE>
-__device__ inline void epilogue8(const LinearEpilogue& ep, int64_t group, int64_t row, int64_t col, int64_t left,
-                                 float (&z)[8]) {
+__device__ inline void epilogue8(const LinearEpilogue& ep, const Row8& bias, const Row8& residual, int64_t group,
+                                 int64_t row, int64_t col, int64_t left, float (&z)[8]) {
     if (ep.bias) {
-        const Row8 b = load8(ep.bias + group * ep.bias_group + col, left);
+        float b[8];
+        bias.widen<TYPE>(b);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] += widen<TYPE>(b.v[e]);
+        for (int e = 0; e < 8; ++e) z[e] += b[e];
     }
-    if (ep.preact) {
-        Row8 r;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r.v[e] = narrow<TYPE>(z[e]);
-        store8(ep.preact + row * ep.ldp + col, r, left);
-    }
+    if (ep.preact) store8(ep.preact + row * ep.ldp + col, Row8::narrow<TYPE>(z), left);
     if (ep.act != kActNone) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[e] = act_value(z[e], ep.act);
     }
-    const int64_t at = row * ep.ldo + col + (group * ep.out_group);
+    const int64_t at = row * ep.ldo + col + group * ep.out_group;
     if (ep.out_f32) {
         if (ep.residual) {
             float r[8];
@@ -170,15 +242,13 @@ __device__ inline void epilogue8(const LinearEpilogue& ep, int64_t group, int64_
         }
         store8(static_cast<float*>(ep.out) + at, z, left);
     } else {
-        Row8 o;
         if (ep.residual) {
-            const Row8 r = load8(static_cast<const uint16_t*>(ep.residual) + row * ep.ldr + col, left);
+            float r[8];
+            residual.widen<TYPE>(r);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] += widen<TYPE>(r.v[e]);
+            for (int e = 0; e < 8; ++e) z[e] += r[e];
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o.v[e] = narrow<TYPE>(z[e]);
-        store8(static_cast<uint16_t*>(ep.out) + at, o, left);
+        store8(static_cast<uint16_t*>(ep.out) + at, Row8::narrow<TYPE>(z), left);
     }
 }
 
@@ -222,11 +292,12 @@ __device__ inline GroupTile find_group_tile(const int32_t* offsets, int groups, 
         const uint64_t found = __ballot(here);
         if (found) {
             const int l = __builtin_ctzll(found);
-            const int64_t first = before + __shfl(upto - own, l);
-            const int64_t lo = __shfl((int)r.lo, l), hi = __shfl((int)r.hi, l);
+            // (lane l's values, uniform: the tile's addresses stay in scalar registers)
+            const int64_t first = before + __builtin_amdgcn_readlane(upto - own, l);
+            const int64_t lo = __builtin_amdgcn_readlane((int)r.lo, l), hi = __builtin_amdgcn_readlane((int)r.hi, l);
             return GroupTile{g0 + l, lo + (tile - first) * tile_rows, hi, first};
         }
-        before += __shfl(upto, kWave - 1);
+        before += __builtin_amdgcn_readlane(upto, kWave - 1);
     }
     return GroupTile{-1, 0, 0, 0};
 }
@@ -244,10 +315,10 @@ __device__ inline void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "
 // the banks, so the row's second bit decides; rows of 32: four rows do).
 template <bool KMAJOR, int OUT, int DEPTH, int STAGES>
 struct OperandTile {
-    static_assert(DEPTH == 64 && OUT % 32 == 0, "rows of 128 bytes, k-major");
+    static_assert((DEPTH == 64 || DEPTH == 32) && OUT % 32 == 0, "k-major rows of 128 or 64 bytes");
     static constexpr int unit = KMAJOR ? 4 : OUT >= 64 ? 16 : 0;
-    static constexpr int shift = KMAJOR ? 1 : OUT == 64 ? 1 : 0;
-    static constexpr int mask = KMAJOR ? 7 : OUT >= 128 ? 3 : OUT == 64 ? 1 : 0;
+    static constexpr int shift = KMAJOR ? (DEPTH == 64 ? 1 : 2) : OUT == 64 ? 1 : 0;
+    static constexpr int mask = KMAJOR ? (DEPTH == 64 ? 7 : 3) : OUT >= 128 ? 3 : OUT == 64 ? 1 : 0;
     using Tile = LdsTile<KMAJOR ? OUT : DEPTH, (KMAJOR ? DEPTH : OUT) / 2, 0, STAGES, unit, shift, mask>;
     static constexpr int row_groups = Tile::cols / 4;  // 16-byte groups per row
 };
@@ -310,9 +381,14 @@ struct OperandCopy {
     __host__ __device__ static constexpr bool fits(int64_t ld) {
         return ld <= (((int64_t)1 << 31) - 1) / (2 * Tile::rows) - 2 * Tile::cols;
     }
-    // Copies of contraction tile t into `stage`; `left`: contraction elements from that tile's first on (a tile
-    // past the end fills the stage with zeros).
-    __device__ void issue(int64_t t, int64_t left, uint32_t* lds, int stage) const {
+    // The copies of contraction tile t into `stage`, one instruction at a time; `left`: contraction elements from
+    // that tile's first on (a tile past the end fills the stage with zeros).
+    struct Issue {
+        u32x4 buffer;
+        uint32_t from, step, to;
+        __device__ void operator()(int i) const { copy16_checked(buffer, from + i * step, to + i * (WAVES * 1024)); }
+    };
+    __device__ Issue tile(int64_t t, int64_t left, uint32_t* lds, int stage) const {
         typedef __attribute__((address_space(3))) uint32_t lds_word;
         const char* tile = base + t * tile_bytes;
         int64_t bytes = end - tile;
@@ -321,9 +397,12 @@ struct OperandCopy {
         const u32x4 buffer{first_lane((uint32_t)b), first_lane((uint32_t)(b >> 32) & 0xffffu),
                            first_lane((uint32_t)bytes), 0x00020000u};
         const uint32_t to = first_lane((uint32_t)(uintptr_t)(lds_word*)lds + stage * (Tile::stage_elems * 4) + lds_piece);
-        const uint32_t from = KMAJOR && (int64_t)depth >= left ? kBeyond : offset;
+        return Issue{buffer, KMAJOR && (int64_t)depth >= left ? kBeyond : offset, step, to};
+    }
+    __device__ void issue(int64_t t, int64_t left, uint32_t* lds, int stage) const {
+        const Issue copy = tile(t, left, lds, stage);
 #pragma unroll
-        for (int i = 0; i < PER_WAVE; ++i) copy16_checked(buffer, from + i * step, to + i * (WAVES * 1024));
+        for (int i = 0; i < PER_WAVE; ++i) copy(i);
     }
 };
 
@@ -356,22 +435,22 @@ struct OperandLoad {
 #pragma unroll
         for (int i = 0; i < PER_THREAD; ++i) {
             const int at = tid + i * THREADS, row = at / OT::row_groups, col = at % OT::row_groups * 8;
-            *reinterpret_cast<u32x4*>(lds + Tile::offset(stage, row, col / 2)) = __builtin_bit_cast(u32x4, held[i]);
+            *reinterpret_cast<u32x4*>(lds + Tile::offset(stage, row, col / 2)) = held[i].w;
         }
     }
 };
 
 // A wave's fragments of one operand: block i (32 output rows or columns) of
 // MFMA step st, 8 contraction elements per lane.
-template <class OT, bool KMAJOR, int BLOCKS>
+template <class OT, bool KMAJOR, int BLOCKS, int STEPS>
 struct OperandRead {
     using Tile = typename OT::Tile;
-    int at[KMAJOR ? 4 : BLOCKS];  // k-major: by step; else by block
+    int at[KMAJOR ? STEPS : BLOCKS];  // k-major: by step; else by block
 
     __device__ OperandRead(int out0, int lane) {
         if constexpr (KMAJOR) {
 #pragma unroll
-            for (int st = 0; st < 4; ++st) at[st] = Tile::offset(0, out0 + lane % 32, st * 8 + 4 * (lane / 32));
+            for (int st = 0; st < STEPS; ++st) at[st] = Tile::offset(0, out0 + lane % 32, st * 8 + 4 * (lane / 32));
         } else {
             const int row = 8 * (lane / 32) + (lane % 16) / 4, col = 16 * ((lane / 16) % 2) + 4 * (lane % 4);
 #pragma unroll
@@ -397,10 +476,15 @@ struct OperandRead {
 };
 
 // ---- the product --------------------------------------------------------------------
-template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int MIN_WAVES_>
+// PERSISTENT: one workgroup per place on the chip works through many tiles;
+// the first copies of the next tile are issued before the epilogue of this
+// one, whose rows pass through LDS of their own.
+template <int BM_, int BN_, int BK_, int WM_, int WN_, int STAGES_, int MIN_WAVES_, bool PERSISTENT_ = false>
 struct LinearShape {
+    static constexpr bool PERSISTENT = PERSISTENT_;
+    static constexpr int COPY_SHARE = 4;  // eighths of a tile's copies issued in the last step of the tile before
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_, MIN_WAVES = MIN_WAVES_;
-    static constexpr int BK = 64;
+    static constexpr int BK = BK_;
     static constexpr int WAVES_N = BN / WN, THREADS = BM / WM * WAVES_N * kWave;
     static constexpr int MI = WM / 32, NI = WN / 32;
 };
@@ -419,198 +503,332 @@ __device__ inline TilePlace place_of_block(uint32_t block, uint32_t blocks, uint
     return TilePlace{8 * p + in % high, in / high};
 }
 
-// One workgroup per BM x BN output tile (and slice of the contraction, and
-// group).  S LDS stages: during the multiply of contraction tile t the copies
-// of tiles t+1 .. t+S-1 are in flight; one barrier per tile.  The fragments of
-// an MFMA step are read during the MFMAs of the step before, the first of a
-// tile during the last step of the tile before it, after the barrier.
+// The kernel's own LinearProblem argument, read again from the argument
+// segment (scalar loads).  Kept live from the kernel's start, its fields and
+// the K loop's would not fit the scalar registers together, and what does not
+// fit is moved to vector registers that the sums need.
+__device__ inline LinearProblem problem_again() {
+    typedef __attribute__((address_space(4))) const LinearProblem constant_problem;
+    auto* at = (constant_problem*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(at));
+    LinearProblem p;
+    __builtin_memcpy(&p, at, sizeof(p));
+    return p;
+}
+
+// The same value, which the compiler may not know to be: what is computed from
+// it stays inside the loop over tiles instead of being kept for all of them.
+__device__ inline int afresh(int lane) {
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+__device__ inline int afresh_uniform(int wave) {
+    asm volatile("" : "+s"(wave));
+    return wave;
+}
+
+// A workgroup's share of the work: one output tile of one matrix, group or slice.
+struct LinearWork {
+    int64_t m0, m_end, n0, group, L;
+    const uint16_t* A;  // first element of the operands' rows and contraction
+    const uint16_t* B;
+    float* partial;
+    bool none;          // past the last group's tiles
+};
+template <bool AK, bool BK_, int BM, int BN>
+__device__ inline LinearWork linear_work(const LinearProblem& p, uint32_t tile, uint32_t tiles_m, uint32_t tiles_n,
+                                         uint32_t y) {
+    const TilePlace place = place_of_block(tile, tiles_m * tiles_n, tiles_m, tiles_n);
+    LinearWork w{place.row * BM, p.R, place.col * BN, 0, p.L, p.A, p.B, nullptr, false};
+    if (p.axis == kGroupRows) {
+        const GroupTile gt = find_group_tile(p.offsets, p.groups, p.R, BM, place.row);
+        if (gt.group < 0) {
+            w.none = true;
+            return w;
+        }
+        w.group = gt.group;
+        w.m0 = gt.row0;
+        w.m_end = gt.row_end;
+        w.B += w.group * p.b_group;
+    } else if (p.axis == kGroupContraction) {
+        w.group = y;
+        const RowRange r = group_rows(p.offsets, (int)y, p.L);
+        w.A += r.lo * p.lda;
+        w.B += r.lo * p.ldb;
+        w.L = r.hi - r.lo;
+    } else if (p.splits > 1) {
+        const int64_t l0 = y * p.slice;
+        w.A += AK ? l0 : l0 * p.lda;
+        w.B += BK_ ? l0 : l0 * p.ldb;
+        w.L = w.L - l0 < p.slice ? w.L - l0 : p.slice;
+        w.partial = p.partial + y * p.R * p.C;
+    }
+    w.A += AK ? w.m0 * p.lda : w.m0;
+    w.B += BK_ ? w.n0 * p.ldb : w.n0;
+    return w;
+}
+
+// One BM x BN output tile (of a slice of the contraction, or of a group) at a
+// time.  S LDS stages with one barrier per contraction tile: every wave has
+// read all of tile t by the barrier inside iteration t, so the copies of tile
+// t+S go into its stage from there on, spread over the MFMAs of that
+// iteration's last step and of the next iteration's first ones (COPY_SHARE).
+// The fragments of an MFMA step are read between the MFMAs of the step
+// before, the first of a tile between those of the last step of the tile
+// before it, after the barrier.
 // The MFMAs take B as their row operand, so a lane's four consecutive results
 // are four consecutive columns of one output row; each wave passes its
-// results through LDS, 32 rows at a time, to give every lane eight columns of
-// a row and the epilogue's loads and stores 16 bytes per lane.
+// results through LDS in blocks of 32x32 to give every lane eight columns of
+// a row, and the epilogue's loads and stores 16 bytes per lane.
 template <int TYPE, bool AK, bool BK_, class Shape, bool DIRECT>
-__global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_kernel(LinearProblem p, uint32_t tiles_m,
-                                                                                   uint32_t tiles_n) {
+__global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_kernel(LinearProblem, uint32_t tiles_m,
+                                                                                   uint32_t tiles_n, uint32_t grid_y) {
     using Op = Mfma16Op<TYPE, 32>;
+    static_assert(Shape::BK % 32 == 0, "steps alternate between two fragment buffers");
     constexpr int BM = Shape::BM, BN = Shape::BN, BK = Shape::BK, S = DIRECT ? Shape::STAGES : 2;
-    constexpr int MI = Shape::MI, NI = Shape::NI, THREADS = Shape::THREADS;
+    constexpr int MI = Shape::MI, NI = Shape::NI, THREADS = Shape::THREADS, STEPS = BK / 16;
+    constexpr bool PERSISTENT = Shape::PERSISTENT && DIRECT;
     using OA = OperandTile<AK, BM, BK, S>;
     using OB = OperandTile<BK_, BN, BK, S>;
     using TileA = typename OA::Tile;
     using TileB = typename OB::Tile;
-    constexpr int STAGE_ROW = Shape::WN + 4;  // words per staged output row
-    constexpr int STAGE_WORDS = 32 * STAGE_ROW;
-    constexpr int WORDS = TileA::total_elems + TileB::total_elems;
-    static_assert(THREADS / kWave * STAGE_WORDS <= WORDS, "the staged rows fit the operand stages");
+    constexpr int OPERANDS = TileA::total_elems + TileB::total_elems;
+    constexpr int BLOCK_WORDS = 32 * 32, STAGED = THREADS / kWave * BLOCK_WORDS;
+    static_assert(PERSISTENT || STAGED <= OPERANDS, "the staged blocks fit the operand stages");
+    constexpr int WORDS = OPERANDS + (PERSISTENT ? STAGED : 0);
 
     __shared__ __attribute__((aligned(16))) uint32_t lds[WORDS];
     poison_lds(lds, WORDS);
     uint32_t* const lds_a = lds;
     uint32_t* const lds_b = lds + TileA::total_elems;
 
-    const int tid = threadIdx.x, lane = tid % kWave;
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int wm0 = wave / Shape::WAVES_N * Shape::WM, wn0 = wave % Shape::WAVES_N * Shape::WN;
+    const int tid = threadIdx.x, every_lane = tid % kWave;
+    const int every_wave = __builtin_amdgcn_readfirstlane(tid / kWave);
 
-    // This workgroup's tile: rows [m0, m_end) of the output, columns from n0, contraction [l0, l0 + L).
-    const TilePlace place = place_of_block(blockIdx.x, gridDim.x, tiles_m, tiles_n);
-    int64_t m0 = place.row * BM, m_end = p.R, n0 = place.col * BN, group = 0, L = p.L;
-    const uint16_t* A = p.A;
-    const uint16_t* B = p.B;
-    float* partial = nullptr;
-    if (p.axis == kGroupRows) {
-        const GroupTile gt = find_group_tile(p.offsets, p.groups, p.R, BM, place.row);
-        if (gt.group < 0) return;
-        group = gt.group;
-        m0 = gt.row0;
-        m_end = gt.row_end;
-        B += group * p.b_group;
-    } else if (p.axis == kGroupContraction) {
-        group = blockIdx.y;
-        const RowRange r = group_rows(p.offsets, (int)group, p.L);
-        A += r.lo * p.lda;
-        B += r.lo * p.ldb;
-        L = r.hi - r.lo;
-    } else if (p.splits > 1) {
-        const int64_t l0 = blockIdx.y * p.slice;
-        A += AK ? l0 : l0 * p.lda;
-        B += BK_ ? l0 : l0 * p.ldb;
-        L = L - l0 < p.slice ? L - l0 : p.slice;
-        partial = p.partial + blockIdx.y * p.R * p.C;
-    }
-    const int64_t T = L > 0 ? (L + BK - 1) / BK : 0;
-    const uint16_t* a_origin = AK ? A + m0 * p.lda : A + m0;
-    const uint16_t* b_origin = BK_ ? B + n0 * p.ldb : B + n0;
+    const uint32_t tiles = tiles_m * tiles_n, total = tiles * grid_y;
+    auto work_of = [&](uint32_t id) {
+        return linear_work<AK, BK_, BM, BN>(problem_again(), id % tiles, tiles_m, tiles_n, id / tiles);
+    };
+    // The next share that exists from id on (grouped rows may need fewer tiles than were counted for them).
+    auto find_work = [&](uint32_t& id, LinearWork& w) {
+        for (; id < total; id += gridDim.x) {
+            w = work_of(id);
+            if (!w.none) return true;
+        }
+        return false;
+    };
+    uint32_t id = blockIdx.x;
+    LinearWork w;
+    if (!find_work(id, w)) return;
 
     using acc_t = typename Op::acc_t;
-    acc_t acc[MI][NI];
+    using CA = OperandCopy<AK, BM, BK, S, THREADS>;
+    using CB = OperandCopy<BK_, BN, BK, S, THREADS>;
+    constexpr int COPIES = CA::PER_WAVE + CB::PER_WAVE;
+    constexpr int EARLY = (COPIES * Shape::COPY_SHARE + 7) / 8;  // copies issued in the last step
+    // The first copies of a share: its first S-1 contraction tiles and the early ones of the next.
+    auto start_copies = [&](const LinearWork& w) {
+        if constexpr (DIRECT) {
+            const LinearProblem p = problem_again();
+            const int lane = afresh(every_lane), wave = afresh_uniform(every_wave);
+            const CA copy_a(w.A, p.lda, w.m_end - w.m0, w.L, wave, lane);
+            const CB copy_b(w.B, p.ldb, p.C - w.n0, w.L, wave, lane);
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NI; ++j)
-#pragma unroll
-            for (int v = 0; v < Op::ACC; ++v) acc[i][j][v] = 0.0f;
-
-    const OperandRead<OA, AK, MI> read_a(wm0, lane);
-    const OperandRead<OB, BK_, NI> read_b(wn0, lane);
-    auto read_fragments = [&](int stage, int st, u32x4 (&af)[MI], u32x4 (&bf)[NI]) {
-#pragma unroll
-        for (int i = 0; i < MI; ++i) af[i] = read_a.read(lds_a, stage, st, i);
-#pragma unroll
-        for (int j = 0; j < NI; ++j) bf[j] = read_b.read(lds_b, stage, st, j);
+            for (int s = 0; s < S - 1; ++s) {
+                copy_a.issue(s, w.L - s * BK, lds_a, s);
+                copy_b.issue(s, w.L - s * BK, lds_b, s);
+            }
+            const auto a = copy_a.tile(S - 1, w.L - (S - 1) * BK, lds_a, S - 1);
+            const auto b = copy_b.tile(S - 1, w.L - (S - 1) * BK, lds_b, S - 1);
+            static_for<EARLY>([&](auto X_) {
+                constexpr int X = decltype(X_)::value;
+                if constexpr (X < CA::PER_WAVE)
+                    a(X);
+                else
+                    b(X - CA::PER_WAVE);
+            });
+        }
     };
-    auto multiply_step = [&](const u32x4 (&af)[MI], const u32x4 (&bf)[NI]) {
+    start_copies(w);
+    bool landed = false;  // the first copies of this share are known to have landed
+
+    for (;;) {
+        const int lane = afresh(every_lane), wave = afresh_uniform(every_wave);
+        const int wm0 = wave / Shape::WAVES_N * Shape::WM, wn0 = wave % Shape::WAVES_N * Shape::WN;
+        const OperandRead<OA, AK, MI, STEPS> read_a(wm0, lane);
+        const OperandRead<OB, BK_, NI, STEPS> read_b(wn0, lane);
+        auto read_fragments = [&](int stage, int st, u32x4 (&af)[MI], u32x4 (&bf)[NI]) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i) af[i] = read_a.read(lds_a, stage, st, i);
+#pragma unroll
+            for (int j = 0; j < NI; ++j) bf[j] = read_b.read(lds_b, stage, st, j);
+        };
+        const int64_t T = w.L > 0 ? (w.L + BK - 1) / BK : 0;
+        acc_t acc[MI][NI];
 #pragma unroll
         for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < NI; ++j) acc[i][j] = Op::mma(bf[j], af[i], acc[i][j]);
-    };
-    u32x4 af[2][MI], bf[2][NI];
-
-    if constexpr (DIRECT) {
-        using CA = OperandCopy<AK, BM, BK, S, THREADS>;
-        using CB = OperandCopy<BK_, BN, BK, S, THREADS>;
-        constexpr int COPIES = CA::PER_WAVE + CB::PER_WAVE;
-        const CA copy_a(a_origin, p.lda, m_end - m0, L, wave, lane);
-        const CB copy_b(b_origin, p.ldb, p.C - n0, L, wave, lane);
-        auto issue = [&](int64_t t, int stage) {
-            copy_a.issue(t, L - t * BK, lds_a, stage);
-            copy_b.issue(t, L - t * BK, lds_b, stage);
-        };
-#pragma unroll
-        for (int s = 0; s < S - 1; ++s) issue(s, s);
-        wait_vector_memory_at_most<(S - 2) * COPIES>();
-        __syncthreads();
-        int s = 0;  // stage of tile t
-        if (T > 0) read_fragments(0, 0, af[0], bf[0]);
-        for (int64_t t = 0; t < T; ++t) {
-            const int free_stage = s == 0 ? S - 1 : s - 1, next = s + 1 == S ? 0 : s + 1;
-            issue(t + S - 1, free_stage);
-#pragma unroll
-            for (int st = 0; st + 1 < 4; ++st) {
-                read_fragments(s, st + 1, af[(st + 1) & 1], bf[(st + 1) & 1]);
-                multiply_step(af[st & 1], bf[st & 1]);
-                alternate_mfma_and_lds_reads<MI * NI>();
-            }
-            wait_vector_memory_at_most<(S - 2) * COPIES>();
-            __syncthreads();
-            read_fragments(next, 0, af[0], bf[0]);  // (of the last tile: zeros)
-            multiply_step(af[1], bf[1]);
-            alternate_mfma_and_lds_reads<MI * NI>();
-            s = next;
-        }
-        wait_vector_memory();
-    } else {
-        // Two stages; the loads of tile t+1 are issued before the multiply
-        // of tile t and stored to LDS after it.
-        OperandLoad<AK, BM, BK, S, THREADS> load_a(a_origin, p.lda, m_end - m0);
-        OperandLoad<BK_, BN, BK, S, THREADS> load_b(b_origin, p.ldb, p.C - n0);
-        if (T > 0) {
-            load_a.load(0, L, tid);
-            load_b.load(0, L, tid);
-            load_a.store(lds_a, 0, tid);
-            load_b.store(lds_b, 0, tid);
-        }
-        __syncthreads();
-        for (int64_t t = 0; t < T; ++t) {
-            const int s = (int)(t & 1);
-            if (t + 1 < T) {
-                load_a.load(t + 1, L - (t + 1) * BK, tid);
-                load_b.load(t + 1, L - (t + 1) * BK, tid);
-            }
-            read_fragments(s, 0, af[0], bf[0]);
-#pragma unroll
-            for (int st = 0; st < 4; ++st) {
-                if (st + 1 < 4) read_fragments(s, st + 1, af[(st + 1) & 1], bf[(st + 1) & 1]);
-                multiply_step(af[st & 1], bf[st & 1]);
-            }
-            if (t + 1 < T) {
-                load_a.store(lds_a, s ^ 1, tid);
-                load_b.store(lds_b, s ^ 1, tid);
-            }
-            __syncthreads();
-        }
-    }
-    __syncthreads();  // every read and copy of the operand stages is done
-
-    float* const staged = reinterpret_cast<float*>(lds) + wave * STAGE_WORDS;
-    constexpr int ROW_LANES = Shape::WN / 8, ROWS = kWave / ROW_LANES;
-    const int r = lane / ROW_LANES, c = lane % ROW_LANES * 8;
-    const int64_t col = n0 + wn0 + c, left = p.C - col;
-#pragma unroll 1
-    for (int i = 0; i < MI; ++i) {
-        // (one copy of the epilogue's code for all blocks: only this choice of registers is unrolled)
-        static_for<MI>([&](auto I_) {
-            constexpr int I = decltype(I_)::value;
-            if (i != I) return;
-#pragma unroll
             for (int j = 0; j < NI; ++j)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const floatx4 x{acc[I][j][4 * q], acc[I][j][4 * q + 1], acc[I][j][4 * q + 2], acc[I][j][4 * q + 3]};
-                    *reinterpret_cast<floatx4*>(staged + lane % 32 * STAGE_ROW + j * 32 + 8 * q + 4 * (lane / 32)) = x;
-                }
-        });
-        wave_fence();
-#pragma unroll 1
-        for (int k = 0; k < 32; k += ROWS) {
-            const int64_t row = m0 + wm0 + i * 32 + k + r;
-            const float* src = staged + (k + r) * STAGE_ROW + c;
-            float z[8];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const floatx4 x = *reinterpret_cast<const floatx4*>(src + 4 * h);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) z[4 * h + e] = x[e];
+                for (int v = 0; v < Op::ACC; ++v) acc[i][j][v] = 0.0f;
+        u32x4 af[2][MI], bf[2][NI];
+
+        if constexpr (DIRECT) {
+            const LinearProblem p = problem_again();
+            const CA copy_a(w.A, p.lda, w.m_end - w.m0, w.L, wave, lane);
+            const CB copy_b(w.B, p.ldb, p.C - w.n0, w.L, wave, lane);
+            if (!landed) wait_vector_memory_at_most<(S - 2) * COPIES + EARLY>();
+            __syncthreads();
+            int s = 0;  // stage of tile t
+            // the copies being issued: those of tile t+S-1, then of t+S
+            auto issue_a = copy_a.tile(S - 1, w.L - (S - 1) * BK, lds_a, S - 1);
+            auto issue_b = copy_b.tile(S - 1, w.L - (S - 1) * BK, lds_b, S - 1);
+            if (T > 0) read_fragments(0, 0, af[0], bf[0]);
+            for (int64_t t = 0; t < T; ++t) {
+                const int next = s + 1 == S ? 0 : s + 1;
+                static_for<STEPS>([&](auto ST_) {
+                    constexpr int ST = decltype(ST_)::value, NOW = ST & 1, THEN = NOW ^ 1;
+                    constexpr bool LAST = ST + 1 == STEPS;
+                    // this step's copies: [FROM, TO) of the list A's then B's
+                    constexpr int REST = COPIES - EARLY, OVER = STEPS > 2 ? 2 : 1;
+                    constexpr int FROM = LAST ? 0 : ST < OVER ? EARLY + REST * ST / OVER : COPIES;
+                    constexpr int TO = LAST ? EARLY : ST < OVER ? EARLY + REST * (ST + 1) / OVER : COPIES;
+                    constexpr int ITEMS = MI + NI + TO - FROM;
+                    if constexpr (LAST) {
+                        wait_vector_memory_at_most<(S - 2) * COPIES>();
+                        __syncthreads();
+                        issue_a = copy_a.tile(t + S, w.L - (t + S) * BK, lds_a, s);
+                        issue_b = copy_b.tile(t + S, w.L - (t + S) * BK, lds_b, s);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    static_for<MI * NI>([&](auto Q_) {
+                        constexpr int Q = decltype(Q_)::value, I = Q / NI, J = Q % NI;
+                        acc[I][J] = Op::mma(bf[NOW][J], af[NOW][I], acc[I][J]);
+                        static_for<ITEMS>([&](auto X_) {
+                            constexpr int X = decltype(X_)::value;
+                            if constexpr (X * MI * NI / ITEMS == Q) {
+                                if constexpr (X < NI)
+                                    bf[THEN][X] = read_b.read(lds_b, LAST ? next : s, LAST ? 0 : ST + 1, X);
+                                else if constexpr (X < NI + MI)
+                                    af[THEN][X - NI] = read_a.read(lds_a, LAST ? next : s, LAST ? 0 : ST + 1, X - NI);
+                                else if constexpr (FROM + X - NI - MI < CA::PER_WAVE)
+                                    issue_a(FROM + X - NI - MI);
+                                else
+                                    issue_b(FROM + X - NI - MI - CA::PER_WAVE);
+                            }
+                        });
+                        __builtin_amdgcn_sched_barrier(0);
+                    });
+                });
+                s = next;
             }
-            if (row < m_end && left > 0) {
-                if (partial)
-                    store8(partial + row * p.C + col, z, left);
-                else
-                    epilogue8<TYPE>(p.ep, group, row, col, left, z);
+            wait_vector_memory();  // (copies past the last tile, which write zeros)
+        } else {
+            // Two stages; the loads of tile t+1 are issued before the
+            // multiply of tile t and stored to LDS after it.
+            const LinearProblem p = problem_again();
+            OperandLoad<AK, BM, BK, S, THREADS> load_a(w.A, p.lda, w.m_end - w.m0);
+            OperandLoad<BK_, BN, BK, S, THREADS> load_b(w.B, p.ldb, p.C - w.n0);
+            if (T > 0) {
+                load_a.load(0, w.L, tid);
+                load_b.load(0, w.L, tid);
+                load_a.store(lds_a, 0, tid);
+                load_b.store(lds_b, 0, tid);
+            }
+            __syncthreads();
+            for (int64_t t = 0; t < T; ++t) {
+                const int s = (int)(t & 1);
+                if (t + 1 < T) {
+                    load_a.load(t + 1, w.L - (t + 1) * BK, tid);
+                    load_b.load(t + 1, w.L - (t + 1) * BK, tid);
+                }
+                read_fragments(s, 0, af[0], bf[0]);
+#pragma unroll
+                for (int st = 0; st < STEPS; ++st) {
+                    if (st + 1 < STEPS) read_fragments(s, st + 1, af[(st + 1) & 1], bf[(st + 1) & 1]);
+#pragma unroll
+                    for (int i = 0; i < MI; ++i)
+#pragma unroll
+                        for (int j = 0; j < NI; ++j) acc[i][j] = Op::mma(bf[st & 1][j], af[st & 1][i], acc[i][j]);
+                }
+                if (t + 1 < T) {
+                    load_a.store(lds_a, s ^ 1, tid);
+                    load_b.store(lds_b, s ^ 1, tid);
+                }
+                __syncthreads();
             }
         }
-        wave_fence();
+        __syncthreads();  // every read and copy of the operand stages is done
+
+        LinearWork then;
+        bool more = false;
+        if constexpr (PERSISTENT) {
+            id += gridDim.x;
+            more = find_work(id, then);
+            if (more) start_copies(then);
+        }
+
+        // The epilogue, 32x32 results at a time: a lane has 8 columns of rows r and r + 16 of the block.  What block
+        // k+1 reads from memory is fetched while block k is finished.
+        const LinearProblem p = problem_again();
+        const int out_lane = afresh(every_lane), r = out_lane / 4, c = out_lane % 4 * 8;
+        float* const staged = reinterpret_cast<float*>(lds) + (PERSISTENT ? OPERANDS : 0) + wave * BLOCK_WORDS;
+        auto block_reads = [&](int k, Row8& bias, Row8 (&residual)[2]) {
+            const int64_t row = w.m0 + wm0 + k / NI * 32 + r, col = w.n0 + wn0 + k % NI * 32 + c, left = p.C - col;
+            if (w.partial || left <= 0) return;
+            bias = bias_reads(p.ep, w.group, col, left);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (row + 16 * h < w.m_end) residual[h] = residual_reads(p.ep, row + 16 * h, col, left);
+        };
+        auto staged_at = [&](int row, int group16) { return staged + row * 32 + 4 * (group16 ^ (((row & 1) << 2) | ((row >> 1) & 3))); };
+        Row8 bias{}, residual[2] = {};
+        block_reads(0, bias, residual);
+#pragma unroll 1
+        for (int k = 0; k < MI * NI; ++k) {
+            Row8 next_bias{}, next_residual[2] = {};
+            if (k + 1 < MI * NI) block_reads(k + 1, next_bias, next_residual);
+            // (one copy of the epilogue's code for all blocks: only this choice of registers is unrolled)
+            static_for<MI * NI>([&](auto K_) {
+                constexpr int K = decltype(K_)::value;
+                if (k != K) return;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const acc_t& x = acc[K / NI][K % NI];
+                    *reinterpret_cast<floatx4*>(staged_at(out_lane % 32, 2 * q + out_lane / 32)) =
+                        floatx4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+                }
+            });
+            wave_fence();
+            const int64_t row = w.m0 + wm0 + k / NI * 32 + r, col = w.n0 + wn0 + k % NI * 32 + c, left = p.C - col;
+            float z[2][8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const floatx4 x = *reinterpret_cast<const floatx4*>(staged_at(r + 16 * h, c / 4 + g));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) z[h][4 * g + e] = x[e];
+                }
+            wave_fence();
+            // Before the last block's stores, so that the next share's copies are known to have landed without
+            // waiting for those stores.
+            if (PERSISTENT && k + 1 == MI * NI) wait_vector_memory();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (left > 0 && row + 16 * h < w.m_end) {
+                    if (w.partial)
+                        store8(w.partial + (row + 16 * h) * p.C + col, z[h], left);
+                    else
+                        epilogue8<TYPE>(p.ep, bias, residual[h], w.group, row + 16 * h, col, left, z[h]);
+                }
+            bias = next_bias;
+            residual[0] = next_residual[0];
+            residual[1] = next_residual[1];
+        }
+        if (!more) return;
+        w = then;
+        landed = true;
     }
 }
 
@@ -622,6 +840,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearProblem p) {
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t row = i / row_groups, col = i % row_groups * 8, left = p.C - col;
         const float* src = p.partial + row * p.C + col;
+        const Row8 bias = bias_reads(p.ep, 0, col, left), residual = residual_reads(p.ep, row, col, left);
         float z[8];
         load8(z, src, left);
         for (int s = 1; s < p.splits; ++s) {
@@ -630,7 +849,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearProblem p) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[e] += more[e];
         }
-        epilogue8<TYPE>(p.ep, 0, row, col, left, z);
+        epilogue8<TYPE>(p.ep, bias, residual, 0, row, col, left, z);
     }
 }
 

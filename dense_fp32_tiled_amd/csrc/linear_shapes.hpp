@@ -21,63 +21,63 @@ constexpr int kTileDepth = 64;  // contraction elements per tile
 template <int TILE>
 struct ShapeOf;
 template <>
-struct ShapeOf<kTile256> { using type = LinearShape<256, 256, 128, 64, 2, 2>; };
+struct ShapeOf<kTile256> { using type = LinearShape<256, 256, 64, 128, 64, 2, 2, true>; };
 template <>
-struct ShapeOf<kTile128> { using type = LinearShape<128, 128, 64, 64, 2, 2>; };
+struct ShapeOf<kTile128> { using type = LinearShape<128, 128, 64, 64, 64, 2, 2>; };
 template <>
-struct ShapeOf<kTile64> { using type = LinearShape<64, 64, 32, 32, 4, 2>; };
+struct ShapeOf<kTile64> { using type = LinearShape<64, 64, 64, 32, 32, 4, 2>; };
 template <>
-struct ShapeOf<kTile32x128> { using type = LinearShape<32, 128, 32, 32, 4, 2>; };
+struct ShapeOf<kTile32x128> { using type = LinearShape<32, 128, 64, 32, 32, 4, 2>; };
 
 // Which operands run along the contraction.
 enum LinearLayout { kForward = 0, kGradA = 1, kGradB = 2 };
 
 // Launches the product of `tile`; `direct`: every row and width of both
-// operands is a multiple of 16 bytes.
-using LinearLaunchFn = hipError_t (*)(const LinearProblem&, LinearLayout, LinearTile, bool direct, uint32_t tiles_m,
-                                      uint32_t tiles_n, uint32_t grid_y, hipStream_t);
-
+// operands is a multiple of 16 bytes.  grid_y: groups of the contraction, or
+// slices.
 template <int TYPE, bool AK, bool BK_, int TILE, bool DIRECT>
 hipError_t launch_linear_tile(const LinearProblem& p, uint32_t tiles_m, uint32_t tiles_n, uint32_t grid_y,
-                              hipStream_t stream) {
+                              int cus, hipStream_t stream) {
     using Shape = typename ShapeOf<TILE>::type;
     LinearProblem problem = p;
-    void* args[] = {&problem, &tiles_m, &tiles_n};
+    void* args[] = {&problem, &tiles_m, &tiles_n, &grid_y};
+    uint32_t blocks = tiles_m * tiles_n * grid_y;
+    if (Shape::PERSISTENT && DIRECT && blocks > (uint32_t)cus) blocks = (uint32_t)cus;
     return hipLaunchKernel(reinterpret_cast<const void*>(linear_tile_kernel<TYPE, AK, BK_, Shape, DIRECT>),
-                           dim3(tiles_m * tiles_n, grid_y), dim3(Shape::THREADS), args, 0, stream);
+                           dim3(blocks), dim3(Shape::THREADS), args, 0, stream);
 }
 
 template <int TYPE, bool AK, bool BK_>
 hipError_t launch_linear_layout(const LinearProblem& p, LinearTile tile, bool direct, uint32_t tiles_m,
-                                uint32_t tiles_n, uint32_t grid_y, hipStream_t stream) {
+                                uint32_t tiles_n, uint32_t grid_y, int cus, hipStream_t stream) {
     switch (tile) {
         // (through registers the 256x256 tile's staged groups would not fit beside its sums: 128x128 is the largest)
-        case kTile256: return launch_linear_tile<TYPE, AK, BK_, kTile256, true>(p, tiles_m, tiles_n, grid_y, stream);
+        case kTile256: return launch_linear_tile<TYPE, AK, BK_, kTile256, true>(p, tiles_m, tiles_n, grid_y, cus, stream);
         case kTile128:
-            return direct ? launch_linear_tile<TYPE, AK, BK_, kTile128, true>(p, tiles_m, tiles_n, grid_y, stream)
-                          : launch_linear_tile<TYPE, AK, BK_, kTile128, false>(p, tiles_m, tiles_n, grid_y, stream);
+            return direct ? launch_linear_tile<TYPE, AK, BK_, kTile128, true>(p, tiles_m, tiles_n, grid_y, cus, stream)
+                          : launch_linear_tile<TYPE, AK, BK_, kTile128, false>(p, tiles_m, tiles_n, grid_y, cus, stream);
         case kTile64:
-            return direct ? launch_linear_tile<TYPE, AK, BK_, kTile64, true>(p, tiles_m, tiles_n, grid_y, stream)
-                          : launch_linear_tile<TYPE, AK, BK_, kTile64, false>(p, tiles_m, tiles_n, grid_y, stream);
+            return direct ? launch_linear_tile<TYPE, AK, BK_, kTile64, true>(p, tiles_m, tiles_n, grid_y, cus, stream)
+                          : launch_linear_tile<TYPE, AK, BK_, kTile64, false>(p, tiles_m, tiles_n, grid_y, cus, stream);
         default:
-            return direct ? launch_linear_tile<TYPE, AK, BK_, kTile32x128, true>(p, tiles_m, tiles_n, grid_y, stream)
-                          : launch_linear_tile<TYPE, AK, BK_, kTile32x128, false>(p, tiles_m, tiles_n, grid_y, stream);
+            return direct ? launch_linear_tile<TYPE, AK, BK_, kTile32x128, true>(p, tiles_m, tiles_n, grid_y, cus, stream)
+                          : launch_linear_tile<TYPE, AK, BK_, kTile32x128, false>(p, tiles_m, tiles_n, grid_y, cus, stream);
     }
 }
 
 template <int TYPE>
 hipError_t launch_linear(const LinearProblem& p, LinearLayout layout, LinearTile tile, bool direct, uint32_t tiles_m,
-                         uint32_t tiles_n, uint32_t grid_y, hipStream_t stream) {
+                         uint32_t tiles_n, uint32_t grid_y, int cus, hipStream_t stream) {
     switch (layout) {
-        case kForward: return launch_linear_layout<TYPE, true, false>(p, tile, direct, tiles_m, tiles_n, grid_y, stream);
-        case kGradA: return launch_linear_layout<TYPE, true, true>(p, tile, direct, tiles_m, tiles_n, grid_y, stream);
-        default: return launch_linear_layout<TYPE, false, false>(p, tile, direct, tiles_m, tiles_n, grid_y, stream);
+        case kForward: return launch_linear_layout<TYPE, true, false>(p, tile, direct, tiles_m, tiles_n, grid_y, cus, stream);
+        case kGradA: return launch_linear_layout<TYPE, true, true>(p, tile, direct, tiles_m, tiles_n, grid_y, cus, stream);
+        default: return launch_linear_layout<TYPE, false, false>(p, tile, direct, tiles_m, tiles_n, grid_y, cus, stream);
     }
 }
 
-hipError_t launch_linear_bf16(const LinearProblem&, LinearLayout, LinearTile, bool, uint32_t, uint32_t, uint32_t,
+hipError_t launch_linear_bf16(const LinearProblem&, LinearLayout, LinearTile, bool, uint32_t, uint32_t, uint32_t, int,
                               hipStream_t);
-hipError_t launch_linear_f16(const LinearProblem&, LinearLayout, LinearTile, bool, uint32_t, uint32_t, uint32_t,
+hipError_t launch_linear_f16(const LinearProblem&, LinearLayout, LinearTile, bool, uint32_t, uint32_t, uint32_t, int,
                              hipStream_t);
 
 }  // namespace dft

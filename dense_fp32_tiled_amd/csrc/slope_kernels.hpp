@@ -46,17 +46,13 @@ __global__ __launch_bounds__(256) void linear_slope_kernel(SlopeProblem p) {
         for (int64_t row = lo + r; row < hi; row += 8) {
             const Row8 dy = load8(p.dY + row * p.ldy + col, left);
             float d[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = widen<TYPE>(dy.v[e]);
+            dy.widen<TYPE>(d);
             if (p.dZ) {
-                const Row8 z = load8(p.Z + row * p.ldz + col, left);
-                Row8 out;
+                float z[8];
+                load8(p.Z + row * p.ldz + col, left).widen<TYPE>(z);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    d[e] *= act_slope(widen<TYPE>(z.v[e]), p.act);
-                    out.v[e] = narrow<TYPE>(d[e]);
-                }
-                store8(p.dZ + row * p.lddz + col, out, left);
+                for (int e = 0; e < 8; ++e) d[e] *= act_slope(z[e], p.act);
+                store8(p.dZ + row * p.lddz + col, Row8::narrow<TYPE>(d), left);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[e] += d[e];
