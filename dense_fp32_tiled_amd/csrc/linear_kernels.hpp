@@ -87,38 +87,70 @@ __device__ inline float normal_tail(float z, float* density) {
 
 __device__ inline float gelu_tanh_argument(float z) { return 1.5957691216057308f * z * (1.0f + 0.044715f * z * z); }
 
-__device__ inline float act_value(float z, int kind) {
+__device__ inline float gelu(float z) {
+    float density;
+    const float tail = normal_tail(z, &density);
+    return z * (z < 0.0f ? tail : 1.0f - tail);
+}
+// Eight values at a time: one branch on the (uniform) kind for all of them.
+__device__ inline void act_values(float (&z)[8], int kind) {
     switch (kind) {
-        case kActRelu: return z > 0.0f ? z : 0.0f;
-        case kActGelu: {
-            float density;
-            const float tail = normal_tail(z, &density);
-            return z * (z < 0.0f ? tail : 1.0f - tail);
-        }
-        // (1 + tanh(u)) / 2 is the logistic function of 2 u
-        case kActGeluTanh: return z * logistic(gelu_tanh_argument(z));
-        case kActSilu: return z * logistic(z);
-        default: return z;
+        case kActRelu:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = z[e] < 0.0f ? 0.0f : z[e];
+            break;
+        case kActGelu:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = gelu(z[e]);
+            break;
+        case kActGeluTanh:  // (1 + tanh(u)) / 2 is the logistic function of 2 u
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] *= logistic(gelu_tanh_argument(z[e]));
+            break;
+        case kActSilu:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] *= logistic(z[e]);
+            break;
+        default: break;
     }
 }
 // The slope at z.  Beyond |z| = 128 every slope has reached its limit in
 // fp32; stopping there keeps 0 * infinity out of the products (a NaN z stays).
-__device__ inline float act_slope(float z, int kind) {
-    if (kind == kActNone) return 1.0f;
-    if (kind == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
-    z = z > 128.0f ? 128.0f : z < -128.0f ? -128.0f : z;
-    if (kind == kActGelu) {
-        float density;
-        const float tail = normal_tail(z, &density);
-        return (z < 0.0f ? tail : 1.0f - tail) + z * 0.39894228040143268f * density;
+__device__ inline void act_slopes(float (&z)[8], int kind) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = z[e] > 128.0f ? 128.0f : z[e] < -128.0f ? -128.0f : z[e];
+    switch (kind) {
+        case kActRelu:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = z[e] > 0.0f ? 1.0f : 0.0f;
+            break;
+        case kActGelu:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float density;
+                const float tail = normal_tail(z[e], &density);
+                z[e] = (z[e] < 0.0f ? tail : 1.0f - tail) + z[e] * 0.39894228040143268f * density;
+            }
+            break;
+        case kActGeluTanh:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float gate = logistic(gelu_tanh_argument(z[e]));
+                const float du = 1.5957691216057308f * (1.0f + 0.134145f * z[e] * z[e]);
+                z[e] = gate + z[e] * gate * (1.0f - gate) * du;
+            }
+            break;
+        case kActSilu:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float gate = logistic(z[e]);
+                z[e] = gate + z[e] * gate * (1.0f - gate);
+            }
+            break;
+        default:
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = 1.0f;
     }
-    float u = z, du = 1.0f;
-    if (kind == kActGeluTanh) {
-        u = gelu_tanh_argument(z);
-        du = 1.5957691216057308f * (1.0f + 0.134145f * z * z);
-    }
-    const float gate = logistic(u);
-    return gate + z * gate * (1.0f - gate) * du;
 }
 
 // ---- 16-bit values ------------------------------------------------------------------
@@ -208,48 +240,45 @@ __device__ inline void store8(float* p, const float (&v)[8], int64_t in_range) {
     }
 }
 
-// The epilogue of eight consecutive columns of one output row, in two parts
-// so that what it reads can be on its way while earlier columns are finished.
-// `left` of the columns lie inside the matrix.
-__device__ inline Row8 bias_reads(const LinearEpilogue& ep, int64_t group, int64_t col, int64_t left) {
-    return ep.bias ? load8(ep.bias + group * ep.bias_group + col, left) : Row8{};
+// The epilogue of eight consecutive columns of one output row.  `bias` and
+// `residual` (of 16 bits) have been read ahead, so that they are on their way
+// while earlier columns are finished; an fp32 residual is read here.  Element
+// offsets: those of the eight in the output, the residual and the
+// pre-activation; `left` of them lie inside the matrix.
+__device__ inline Row8 bias_reads(const LinearEpilogue& ep, int64_t at, int64_t left) {
+    return ep.bias ? load8(ep.bias + at, left) : Row8{};
 }
-__device__ inline Row8 residual_reads(const LinearEpilogue& ep, int64_t row, int64_t col, int64_t left) {
-    if (!ep.residual || ep.out_f32) return Row8{};  // (an fp32 residual is read as it is added)
-    return load8(static_cast<const uint16_t*>(ep.residual) + row * ep.ldr + col, left);
+__device__ inline Row8 residual_reads(const LinearEpilogue& ep, int64_t at, int64_t left) {
+    if (!ep.residual || ep.out_f32) return Row8{};
+    return load8(static_cast<const uint16_t*>(ep.residual) + at, left);
 }
+struct EpilogueAt {
+    int64_t out, residual, preact;
+};
 template <int TYPE>
-__device__ inline void epilogue8(const LinearEpilogue& ep, const Row8& bias, const Row8& residual, int64_t group,
-                                 int64_t row, int64_t col, int64_t left, float (&z)[8]) {
+__device__ inline void epilogue8(const LinearEpilogue& ep, const Row8& bias, const Row8& residual, const EpilogueAt& at,
+                                 int64_t left, float (&z)[8]) {
     if (ep.bias) {
         float b[8];
         bias.widen<TYPE>(b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[e] += b[e];
     }
-    if (ep.preact) store8(ep.preact + row * ep.ldp + col, Row8::narrow<TYPE>(z), left);
-    if (ep.act != kActNone) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = act_value(z[e], ep.act);
-    }
-    const int64_t at = row * ep.ldo + col + group * ep.out_group;
-    if (ep.out_f32) {
-        if (ep.residual) {
-            float r[8];
-            load8(r, static_cast<const float*>(ep.residual) + row * ep.ldr + col, left);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] += r[e];
-        }
-        store8(static_cast<float*>(ep.out) + at, z, left);
-    } else {
-        if (ep.residual) {
-            float r[8];
+    if (ep.preact) store8(ep.preact + at.preact, Row8::narrow<TYPE>(z), left);
+    act_values(z, ep.act);
+    if (ep.residual) {
+        float r[8];
+        if (ep.out_f32)
+            load8(r, static_cast<const float*>(ep.residual) + at.residual, left);
+        else
             residual.widen<TYPE>(r);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] += r[e];
-        }
-        store8(static_cast<uint16_t*>(ep.out) + at, Row8::narrow<TYPE>(z), left);
+        for (int e = 0; e < 8; ++e) z[e] += r[e];
     }
+    if (ep.out_f32)
+        store8(static_cast<float*>(ep.out) + at.out, z, left);
+    else
+        store8(static_cast<uint16_t*>(ep.out) + at.out, Row8::narrow<TYPE>(z), left);
 }
 
 // ---- groups of rows -----------------------------------------------------------------
@@ -397,7 +426,8 @@ struct OperandCopy {
         const u32x4 buffer{first_lane((uint32_t)b), first_lane((uint32_t)(b >> 32) & 0xffffu),
                            first_lane((uint32_t)bytes), 0x00020000u};
         const uint32_t to = first_lane((uint32_t)(uintptr_t)(lds_word*)lds + stage * (Tile::stage_elems * 4) + lds_piece);
-        return Issue{buffer, KMAJOR && (int64_t)depth >= left ? kBeyond : offset, step, to};
+        const int inside = left > DEPTH ? DEPTH : (int)left;
+        return Issue{buffer, KMAJOR && (int)depth >= inside ? kBeyond : offset, step, to};
     }
     __device__ void issue(int64_t t, int64_t left, uint32_t* lds, int stage) const {
         const Issue copy = tile(t, left, lds, stage);
@@ -578,8 +608,8 @@ __device__ inline LinearWork linear_work(const LinearProblem& p, uint32_t tile, 
 // before it, after the barrier.
 // The MFMAs take B as their row operand, so a lane's four consecutive results
 // are four consecutive columns of one output row; each wave passes its
-// results through LDS in blocks of 32x32 to give every lane eight columns of
-// a row, and the epilogue's loads and stores 16 bytes per lane.
+// results through LDS, 16 or 32 rows at a time, to give every lane eight
+// columns of a row, and the epilogue's loads and stores 16 bytes per lane.
 template <int TYPE, bool AK, bool BK_, class Shape, bool DIRECT>
 __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_kernel(LinearProblem, uint32_t tiles_m,
                                                                                    uint32_t tiles_n, uint32_t grid_y) {
@@ -593,7 +623,8 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
     using TileA = typename OA::Tile;
     using TileB = typename OB::Tile;
     constexpr int OPERANDS = TileA::total_elems + TileB::total_elems;
-    constexpr int BLOCK_WORDS = 32 * 32, STAGED = THREADS / kWave * BLOCK_WORDS;
+    constexpr int BR = PERSISTENT ? 16 : 32;  // rows that a wave stages at a time
+    constexpr int BLOCK_WORDS = BR * Shape::WN, STAGED = THREADS / kWave * BLOCK_WORDS;
     static_assert(PERSISTENT || STAGED <= OPERANDS, "the staged blocks fit the operand stages");
     constexpr int WORDS = OPERANDS + (PERSISTENT ? STAGED : 0);
 
@@ -768,64 +799,84 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
             if (more) start_copies(then);
         }
 
-        // The epilogue, 32x32 results at a time: a lane has 8 columns of rows r and r + 16 of the block.  What block
-        // k+1 reads from memory is fetched while block k is finished.
+        // The epilogue, BR rows of a wave's WN columns at a time: a lane has 8 columns of every ROWS-th row, and a
+        // row's lanes cover whole 128-byte lines of a 16-bit output (64-byte pieces cost the stores up to a fifth more
+        // time).  The residual of the next rows is fetched while these are finished.  A tile wholly inside the matrix
+        // takes a copy of the code without masks.
         const LinearProblem p = problem_again();
-        const int out_lane = afresh(every_lane), r = out_lane / 4, c = out_lane % 4 * 8;
+        constexpr int LANES = Shape::WN / 8, ROWS = kWave / LANES, PARTS = BR / ROWS;
+        const int out_lane = afresh(every_lane), r = out_lane / LANES, c = out_lane % LANES * 8;
         float* const staged = reinterpret_cast<float*>(lds) + (PERSISTENT ? OPERANDS : 0) + wave * BLOCK_WORDS;
-        auto block_reads = [&](int k, Row8& bias, Row8 (&residual)[2]) {
-            const int64_t row = w.m0 + wm0 + k / NI * 32 + r, col = w.n0 + wn0 + k % NI * 32 + c, left = p.C - col;
-            if (w.partial || left <= 0) return;
-            bias = bias_reads(p.ep, w.group, col, left);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (row + 16 * h < w.m_end) residual[h] = residual_reads(p.ep, row + 16 * h, col, left);
+        auto staged_at = [&](int row, int group16) {
+            return staged + row * Shape::WN + 4 * (group16 ^ (((row & 1) << 2) | ((row >> 1) & 3)));
         };
-        auto staged_at = [&](int row, int group16) { return staged + row * 32 + 4 * (group16 ^ (((row & 1) << 2) | ((row >> 1) & 3))); };
-        Row8 bias{}, residual[2] = {};
-        block_reads(0, bias, residual);
+        const int64_t tile_row = w.m0 + wm0, tile_col = w.n0 + wn0;  // (uniform)
+        const EpilogueAt lane_at{r * p.ep.ldo + c, r * p.ep.ldr + c, r * p.ep.ldp + c};
+        auto finish = [&](auto WHOLE_) {
+            constexpr bool WHOLE = decltype(WHOLE_)::value;
+            const int64_t left = WHOLE ? (int64_t)8 : p.C - (tile_col + c);
+            // part m: rows r, r + 1, ... of the wave's tile from m * ROWS on
+            auto inside = [&](int m) { return WHOLE || (left > 0 && tile_row + m * ROWS + r < w.m_end); };
+            auto at = [&](int m) {
+                const int64_t row = tile_row + m * ROWS;
+                return EpilogueAt{row * p.ep.ldo + tile_col + w.group * p.ep.out_group + lane_at.out,
+                                  row * p.ep.ldr + tile_col + lane_at.residual,
+                                  row * p.ep.ldp + tile_col + lane_at.preact};
+            };
+            auto read_residual = [&](int m) {
+                return !w.partial && inside(m) ? residual_reads(p.ep, at(m).residual, left) : Row8{};
+            };
+            Row8 bias{}, residual = read_residual(0);
+            if (!w.partial && left > 0) bias = bias_reads(p.ep, w.group * p.ep.bias_group + tile_col + c, left);
 #pragma unroll 1
-        for (int k = 0; k < MI * NI; ++k) {
-            Row8 next_bias{}, next_residual[2] = {};
-            if (k + 1 < MI * NI) block_reads(k + 1, next_bias, next_residual);
-            // (one copy of the epilogue's code for all blocks: only this choice of registers is unrolled)
-            static_for<MI * NI>([&](auto K_) {
-                constexpr int K = decltype(K_)::value;
-                if (k != K) return;
+            for (int m = 0; m < Shape::WM / ROWS; ++m) {
+                Row8 next_residual{};
+                if (m + 1 < Shape::WM / ROWS) next_residual = read_residual(m + 1);
+                if (m % PARTS == 0) {
+                    const int k = m / PARTS;  // the staged block
+                    wave_fence();
+                    // Only this choice of registers is unrolled; the comments keep the compiler from merging the
+                    // choices into one sequence behind copies of all of a block's registers.
+                    static_for<MI>([&](auto I_) {
+                        constexpr int I = decltype(I_)::value;
+                        if (k * BR / 32 != I) return;
+                        if (BR == 32 || out_lane % 32 / BR == k % (32 / BR)) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const acc_t& x = acc[K / NI][K % NI];
-                    *reinterpret_cast<floatx4*>(staged_at(out_lane % 32, 2 * q + out_lane / 32)) =
-                        floatx4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+                            for (int j = 0; j < NI; ++j)
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const acc_t& x = acc[I][j];
+                                    *reinterpret_cast<floatx4*>(staged_at(out_lane % BR, 8 * j + 2 * q + out_lane / 32)) =
+                                        floatx4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
+                                }
+                        }
+                        asm volatile("; rows %0" ::"i"(I) : "memory");
+                    });
+                    wave_fence();
                 }
-            });
-            wave_fence();
-            const int64_t row = w.m0 + wm0 + k / NI * 32 + r, col = w.n0 + wn0 + k % NI * 32 + c, left = p.C - col;
-            float z[2][8];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
+                float z[8];
 #pragma unroll
                 for (int g = 0; g < 2; ++g) {
-                    const floatx4 x = *reinterpret_cast<const floatx4*>(staged_at(r + 16 * h, c / 4 + g));
+                    const floatx4 x = *reinterpret_cast<const floatx4*>(staged_at(r + ROWS * (m % PARTS), c / 4 + g));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) z[h][4 * g + e] = x[e];
+                    for (int e = 0; e < 4; ++e) z[4 * g + e] = x[e];
                 }
-            wave_fence();
-            // Before the last block's stores, so that the next share's copies are known to have landed without
-            // waiting for those stores.
-            if (PERSISTENT && k + 1 == MI * NI) wait_vector_memory();
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                if (left > 0 && row + 16 * h < w.m_end) {
+                // Before the last stores, so that the next share's copies are known to have landed without waiting
+                // for those stores.
+                if (PERSISTENT && m + 1 == Shape::WM / ROWS) wait_vector_memory();
+                if (inside(m)) {
                     if (w.partial)
-                        store8(w.partial + (row + 16 * h) * p.C + col, z[h], left);
+                        store8(w.partial + (tile_row + m * ROWS + r) * p.C + tile_col + c, z, left);
                     else
-                        epilogue8<TYPE>(p.ep, bias, residual[h], w.group, row + 16 * h, col, left, z[h]);
+                        epilogue8<TYPE>(p.ep, bias, residual, at(m), left, z);
                 }
-            bias = next_bias;
-            residual[0] = next_residual[0];
-            residual[1] = next_residual[1];
-        }
+                residual = next_residual;
+            }
+        };
+        if (w.m0 + BM <= w.m_end && w.n0 + BN <= p.C)
+            finish(std::true_type{});
+        else
+            finish(std::false_type{});
         if (!more) return;
         w = then;
         landed = true;
@@ -840,7 +891,8 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearProblem p) {
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t row = i / row_groups, col = i % row_groups * 8, left = p.C - col;
         const float* src = p.partial + row * p.C + col;
-        const Row8 bias = bias_reads(p.ep, 0, col, left), residual = residual_reads(p.ep, row, col, left);
+        const EpilogueAt at{row * p.ep.ldo + col, row * p.ep.ldr + col, row * p.ep.ldp + col};
+        const Row8 bias = bias_reads(p.ep, col, left), residual = residual_reads(p.ep, at.residual, left);
         float z[8];
         load8(z, src, left);
         for (int s = 1; s < p.splits; ++s) {
@@ -849,7 +901,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearProblem p) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[e] += more[e];
         }
-        epilogue8<TYPE>(p.ep, bias, residual, 0, row, col, left, z);
+        epilogue8<TYPE>(p.ep, bias, residual, at, left, z);
     }
 }
 

@@ -50,8 +50,9 @@ __global__ __launch_bounds__(256) void linear_slope_kernel(SlopeProblem p) {
             if (p.dZ) {
                 float z[8];
                 load8(p.Z + row * p.ldz + col, left).widen<TYPE>(z);
+                act_slopes(z, p.act);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] *= act_slope(z[e], p.act);
+                for (int e = 0; e < 8; ++e) d[e] *= z[e];
                 store8(p.dZ + row * p.lddz + col, Row8::narrow<TYPE>(d), left);
             }
 #pragma unroll
