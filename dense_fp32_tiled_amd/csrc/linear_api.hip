@@ -202,9 +202,9 @@ hipError_t launch(int type, const LinearProblem& p, LinearLayout layout, const P
 
 // ---- gemm_linear ----------------------------------------------------------------------
 bool copies_fit(LinearTile tile, const Matrix& a, bool a_kmajor, const Matrix& b, bool b_kmajor) {
-    // OperandCopy::fits of the tile's rows: offsets within a tile below 2^31
+    // OperandCopy::fits of the tile's rows: offsets within a tile below 2^30
     const TileSize size = kTileSizes[tile];
-    const auto fits = [](int64_t ld, int64_t rows, int64_t cols) { return ld <= 0x7fffffff / (2 * rows) - cols; };
+    const auto fits = [](int64_t ld, int64_t rows, int64_t cols) { return ld <= 0x3fffffff / (2 * rows) - cols; };
     return fits(a.ld, a_kmajor ? size.bm : kTileDepth, a_kmajor ? kTileDepth : size.bm) &&
            fits(b.ld, b_kmajor ? size.bn : kTileDepth, b_kmajor ? kTileDepth : size.bn);
 }

@@ -336,20 +336,27 @@ __device__ inline GroupTile find_group_tile(const int32_t* offsets, int groups, 
 __device__ inline void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 // ---- operand tiles ------------------------------------------------------------------
-// One operand's tile of OUT output rows (or columns) by DEPTH contraction
-// elements, in 4-byte words.  K-major: OUT rows of DEPTH elements, 16-byte
-// groups swizzled by (row >> 1) & 7.  Else DEPTH rows of OUT elements, 64-byte
-// groups swizzled by the row so that the four rows of a transposing read fall
-// on four different quarters of the banks (rows of 64 elements: two rows span
-// the banks, so the row's second bit decides; rows of 32: four rows do).
-template <bool KMAJOR, int OUT, int DEPTH, int STAGES>
+// One operand's tile of OUT output rows (or columns) by 64 contraction
+// elements in LDS, in 4-byte words.  K-major: OUT rows of 64 elements; else 64
+// rows of OUT elements.  16-byte groups are swizzled within a row so that each
+// pass of the fragment reads falls on different banks (of 64): a 16-byte read
+// takes 16 lanes a pass, four from each of four rows r with r & 1 and (r >> 1)
+// & 7 between them telling 16 places apart; an 8-byte transposing read takes
+// 32 lanes a pass, eight rows (4 and 4, eight rows apart) of 32 bytes each.
+constexpr int kDepth = 64;
+
+template <bool KMAJOR, int OUT, int STAGES>
 struct OperandTile {
-    static_assert((DEPTH == 64 || DEPTH == 32) && OUT % 32 == 0, "k-major rows of 128 or 64 bytes");
-    static constexpr int unit = KMAJOR ? 4 : OUT >= 64 ? 16 : 0;
-    static constexpr int shift = KMAJOR ? (DEPTH == 64 ? 1 : 2) : OUT == 64 ? 1 : 0;
-    static constexpr int mask = KMAJOR ? (DEPTH == 64 ? 7 : 3) : OUT >= 128 ? 3 : OUT == 64 ? 1 : 0;
-    using Tile = LdsTile<KMAJOR ? OUT : DEPTH, (KMAJOR ? DEPTH : OUT) / 2, 0, STAGES, unit, shift, mask>;
-    static constexpr int row_groups = Tile::cols / 4;  // 16-byte groups per row
+    static_assert(OUT % 32 == 0, "whole fragments");
+    static constexpr int rows = KMAJOR ? OUT : kDepth, cols = (KMAJOR ? kDepth : OUT) / 2;  // words
+    static constexpr int stage_words = rows * cols, total_words = STAGES * stage_words;
+    static constexpr int row_groups = cols / 4;  // 16-byte groups per row
+    static constexpr int period = 16;            // rows after which the swizzle repeats
+    __host__ __device__ static constexpr int swizzle(int row) {
+        if (KMAJOR) return 4 * ((row >> 1) & 7);
+        return 16 * (OUT >= 128 ? row & 3 : OUT == 64 ? (row >> 1) & 1 : 0) + 8 * ((row >> 3) & 1);
+    }
+    __host__ __device__ static constexpr int at(int row, int col) { return row * cols + (col ^ swizzle(row)); }
 };
 
 // One direct global->LDS copy: each lane 16 bytes from byte `offset` of the
@@ -370,67 +377,87 @@ __device__ inline void copy16_checked(const u32x4& buffer, uint32_t offset, uint
 
 constexpr uint32_t kBeyond = 0x80000000u;  // past every buffer's last byte (buffers stop at 2^31 - 1)
 
-// The copies of one operand's tiles, 16 bytes per lane.  A wave's copies of a
-// tile are WAVES pieces of 1 KiB apart, which is a whole number of swizzle
-// periods, so one offset per lane and a constant step describe them all.
-template <bool KMAJOR, int OUT, int DEPTH, int STAGES, int THREADS>
+// The copies of one operand's tiles, 16 bytes per lane, tile after tile.  A
+// wave's copies of a tile are WAVES pieces of 1 KiB apart, which is a whole
+// number of swizzle periods, so one offset per lane and a constant step
+// describe them all.  The next tile is one addition to that offset: the
+// buffer stays where it is, except that a contraction along the rows moves it
+// on before offsets could pass 2^31.  (Setting up a buffer for every tile
+// cost the K loop a tenth: its scalar arithmetic stands between the barriers.)
+template <bool KMAJOR, int OUT, int STAGES, int THREADS>
 struct OperandCopy {
-    using OT = OperandTile<KMAJOR, OUT, DEPTH, STAGES>;
-    using Tile = typename OT::Tile;
+    using Tile = OperandTile<KMAJOR, OUT, STAGES>;
     static constexpr int WAVES = THREADS / kWave;
-    static constexpr int PIECE_ROWS = kWave / OT::row_groups;
-    static constexpr int PER_WAVE = Tile::stage_elems * 4 / 1024 / WAVES;
-    static_assert(PER_WAVE * WAVES * 1024 == Tile::stage_elems * 4, "whole pieces per wave");
-    static_assert((WAVES * PIECE_ROWS) % ((OT::mask + 1) << OT::shift) == 0, "whole swizzle periods per step");
+    static constexpr int PIECE_ROWS = kWave / Tile::row_groups;
+    static constexpr int PER_WAVE = Tile::stage_words * 4 / 1024 / WAVES;
+    static_assert(PER_WAVE * WAVES * 1024 == Tile::stage_words * 4, "whole pieces per wave");
+    static_assert((WAVES * PIECE_ROWS) % Tile::period == 0, "whole swizzle periods per step");
 
-    const char* base;      // first byte of contraction tile 0 (uniform)
-    const char* end;       // past the last byte of the operand's rows (uniform)
-    int64_t tile_bytes;    // between contraction tiles
-    uint32_t offset;       // this lane's first copy
-    uint32_t step;         // between its copies of one tile
-    uint32_t depth;        // k-major: contraction index of the lane's 16 bytes within a tile
+    const char* base;   // the buffer's first byte (uniform), `size` bytes long
+    int64_t size;
+    u32x4 buffer;
+    uint32_t offset;    // this lane's first copy of the tile, from `base`
+    uint32_t step;      // between its copies of one tile
+    uint32_t advance;   // between tiles
+    int depth, left;    // k-major: contraction index of the lane's 16 bytes in the tile; elements from the tile on
+    int until;          // rows along the contraction: tiles before the buffer moves
+    int period;
     uint32_t lds_piece;
 
     // `origin`: the element at contraction index 0 and the tile's first output row (column); `outs`: output rows
-    // (columns) from there; `left`: contraction elements.
-    __device__ OperandCopy(const uint16_t* origin, int64_t ld, int64_t outs, int64_t left, int wave, int lane) {
+    // (columns) from there; `length`: contraction elements.
+    __device__ OperandCopy(const uint16_t* origin, int64_t ld, int64_t outs, int64_t length, int wave, int lane) {
         base = reinterpret_cast<const char*>(origin);
-        const int64_t rows = KMAJOR ? outs : left, cols = KMAJOR ? left : outs;
-        end = rows > 0 && cols > 0 ? base + 2 * ((rows - 1) * ld + cols) : base;
-        tile_bytes = KMAJOR ? 2 * DEPTH : 2 * DEPTH * ld;
-        const int row = wave * PIECE_ROWS + lane / OT::row_groups;
-        const int word = Swizzle{OT::unit, OT::shift, OT::mask}.apply(row, lane % OT::row_groups * 4);
+        const int64_t rows = KMAJOR ? outs : length, cols = KMAJOR ? length : outs;
+        size = rows > 0 && cols > 0 ? 2 * ((rows - 1) * ld + cols) : 0;
+        const int row = wave * PIECE_ROWS + lane / Tile::row_groups;
+        const int word = (lane % Tile::row_groups * 4) ^ Tile::swizzle(row);
         offset = (uint32_t)(2 * row * ld) + 4 * word;
-        depth = KMAJOR ? 2 * word : 0;
-        if (!KMAJOR && 2 * word >= outs) offset = kBeyond;
         step = (uint32_t)(2 * WAVES * PIECE_ROWS * ld);
+        advance = KMAJOR ? 2 * kDepth : (uint32_t)(2 * kDepth * ld);
+        depth = 2 * word;
+        left = KMAJOR ? (int)length : 0;
+        if (!KMAJOR && 2 * word >= outs) offset = kBeyond;
+        // (a lane past the edge stays beyond: its offset may grow to 2^32 - 1, never past it)
+        period = until = KMAJOR ? 0x7fffffff : (int)(0x3fffffff / advance);
         lds_piece = wave * 1024;
+        set_buffer();
     }
-    // Offsets within a tile stay below 2^31.
+    __device__ void set_buffer() {
+        const uint64_t b = (uint64_t)(uintptr_t)base;
+        const int64_t bytes = size < 0 ? 0 : size > 0x7fffffff ? 0x7fffffff : size;
+        buffer = u32x4{first_lane((uint32_t)b), first_lane((uint32_t)(b >> 32) & 0xffffu), first_lane((uint32_t)bytes),
+                       0x00020000u};
+    }
+    // Offsets within a tile stay below 2^30, k-major within the whole contraction.
     __host__ __device__ static constexpr bool fits(int64_t ld) {
-        return ld <= (((int64_t)1 << 31) - 1) / (2 * Tile::rows) - 2 * Tile::cols;
+        return ld <= 0x3fffffff / (2 * Tile::rows) - 2 * Tile::cols;
     }
-    // The copies of contraction tile t into `stage`, one instruction at a time; `left`: contraction elements from
-    // that tile's first on (a tile past the end fills the stage with zeros).
+    // Copy i of the tile into `stage` (a tile past the end fills it with zeros).
     struct Issue {
         u32x4 buffer;
         uint32_t from, step, to;
         __device__ void operator()(int i) const { copy16_checked(buffer, from + i * step, to + i * (WAVES * 1024)); }
     };
-    __device__ Issue tile(int64_t t, int64_t left, uint32_t* lds, int stage) const {
+    __device__ Issue tile(uint32_t* lds, int stage) const {
         typedef __attribute__((address_space(3))) uint32_t lds_word;
-        const char* tile = base + t * tile_bytes;
-        int64_t bytes = end - tile;
-        bytes = left <= 0 || bytes < 0 ? 0 : bytes > 0x7fffffff ? 0x7fffffff : bytes;
-        const uint64_t b = (uint64_t)(uintptr_t)tile;
-        const u32x4 buffer{first_lane((uint32_t)b), first_lane((uint32_t)(b >> 32) & 0xffffu),
-                           first_lane((uint32_t)bytes), 0x00020000u};
-        const uint32_t to = first_lane((uint32_t)(uintptr_t)(lds_word*)lds + stage * (Tile::stage_elems * 4) + lds_piece);
-        const int inside = left > DEPTH ? DEPTH : (int)left;
-        return Issue{buffer, KMAJOR && (int)depth >= inside ? kBeyond : offset, step, to};
+        const uint32_t to = first_lane((uint32_t)(uintptr_t)(lds_word*)lds + stage * (Tile::stage_words * 4) + lds_piece);
+        return Issue{buffer, KMAJOR && depth >= left ? kBeyond : offset, step, to};
     }
-    __device__ void issue(int64_t t, int64_t left, uint32_t* lds, int stage) const {
-        const Issue copy = tile(t, left, lds, stage);
+    __device__ void next() {
+        offset += advance;
+        if constexpr (KMAJOR) {
+            left -= kDepth;
+        } else if (--until == 0) {
+            until = period;
+            base += (int64_t)period * advance;
+            size -= (int64_t)period * advance;
+            offset -= (uint32_t)period * advance;
+            set_buffer();
+        }
+    }
+    __device__ void issue(uint32_t* lds, int stage) const {
+        const Issue copy = tile(lds, stage);
 #pragma unroll
         for (int i = 0; i < PER_WAVE; ++i) copy(i);
     }
@@ -439,11 +466,10 @@ struct OperandCopy {
 // The same tiles through registers, for operands whose rows or widths are
 // not multiples of 16 bytes: 16-byte loads at any 2-byte alignment where a
 // whole group is in range, masked elements at the edges.
-template <bool KMAJOR, int OUT, int DEPTH, int STAGES, int THREADS>
+template <bool KMAJOR, int OUT, int STAGES, int THREADS>
 struct OperandLoad {
-    using OT = OperandTile<KMAJOR, OUT, DEPTH, STAGES>;
-    using Tile = typename OT::Tile;
-    static constexpr int GROUPS = Tile::rows * OT::row_groups;
+    using Tile = OperandTile<KMAJOR, OUT, STAGES>;
+    static constexpr int GROUPS = Tile::rows * Tile::row_groups;
     static constexpr int PER_THREAD = GROUPS / THREADS;
     static_assert(GROUPS % THREADS == 0, "whole groups per thread");
 
@@ -453,50 +479,49 @@ struct OperandLoad {
 
     __device__ OperandLoad(const uint16_t* origin_, int64_t ld_, int64_t outs_) : origin(origin_), ld(ld_), outs(outs_) {}
     __device__ void load(int64_t t, int64_t left, int tid) {
-        const uint16_t* tile = origin + t * (KMAJOR ? (int64_t)DEPTH : DEPTH * ld);
+        const uint16_t* tile = origin + t * (KMAJOR ? (int64_t)kDepth : kDepth * ld);
         const int64_t rows = KMAJOR ? outs : left, cols = KMAJOR ? left : outs;
 #pragma unroll
         for (int i = 0; i < PER_THREAD; ++i) {
-            const int at = tid + i * THREADS, row = at / OT::row_groups, col = at % OT::row_groups * 8;
+            const int at = tid + i * THREADS, row = at / Tile::row_groups, col = at % Tile::row_groups * 8;
             held[i] = load8(tile + row * ld + col, row < rows ? cols - col : 0);
         }
     }
     __device__ void store(uint32_t* lds, int stage, int tid) const {
 #pragma unroll
         for (int i = 0; i < PER_THREAD; ++i) {
-            const int at = tid + i * THREADS, row = at / OT::row_groups, col = at % OT::row_groups * 8;
-            *reinterpret_cast<u32x4*>(lds + Tile::offset(stage, row, col / 2)) = held[i].w;
+            const int at = tid + i * THREADS, row = at / Tile::row_groups, col = at % Tile::row_groups * 8;
+            *reinterpret_cast<u32x4*>(lds + stage * Tile::stage_words + Tile::at(row, col / 2)) = held[i].w;
         }
     }
 };
 
-// A wave's fragments of one operand: block i (32 output rows or columns) of
-// MFMA step st, 8 contraction elements per lane.
-template <class OT, bool KMAJOR, int BLOCKS, int STEPS>
+// A wave's fragments of one operand: block i (16 output rows or columns) of
+// MFMA step st (32 contraction elements), 8 of them per lane.
+template <class Tile, bool KMAJOR, int BLOCKS>
 struct OperandRead {
-    using Tile = typename OT::Tile;
-    int at[KMAJOR ? STEPS : BLOCKS];  // k-major: by step; else by block
+    int from[KMAJOR ? kDepth / 32 : BLOCKS];  // k-major: by step; else by block
 
     __device__ OperandRead(int out0, int lane) {
         if constexpr (KMAJOR) {
 #pragma unroll
-            for (int st = 0; st < STEPS; ++st) at[st] = Tile::offset(0, out0 + lane % 32, st * 8 + 4 * (lane / 32));
+            for (int st = 0; st < kDepth / 32; ++st) from[st] = Tile::at(out0 + lane % 16, st * 16 + 4 * (lane / 16));
         } else {
-            const int row = 8 * (lane / 32) + (lane % 16) / 4, col = 16 * ((lane / 16) % 2) + 4 * (lane % 4);
+            const int row = 8 * (lane / 16) + (lane % 16) / 4;
 #pragma unroll
-            for (int i = 0; i < BLOCKS; ++i) at[i] = Tile::offset(0, row, (out0 + i * 32 + col) / 2);
+            for (int i = 0; i < BLOCKS; ++i) from[i] = Tile::at(row, (out0 + i * 16 + 4 * (lane % 4)) / 2);
         }
     }
     __device__ u32x4 read(const uint32_t* lds, int stage, int st, int i) const {
         if constexpr (KMAJOR) {
-            return *reinterpret_cast<const u32x4*>(lds + stage * Tile::stage_elems + at[st] + i * 32 * Tile::row_stride);
+            return *reinterpret_cast<const u32x4*>(lds + stage * Tile::stage_words + from[st] + i * 16 * Tile::cols);
         } else {
             typedef __attribute__((address_space(3))) const uint32_t lds_word;
             typedef __attribute__((address_space(3))) shortx4 lds_short4;
             u32x2 half[2];
 #pragma unroll
             for (int rr = 0; rr < 2; ++rr) {
-                const int word = stage * Tile::stage_elems + at[i] + (st * 16 + 4 * rr) * Tile::row_stride;
+                const int word = stage * Tile::stage_words + from[i] + (st * 32 + 4 * rr) * Tile::cols;
                 half[rr] = __builtin_bit_cast(u32x2,
                                               __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)((lds_word*)lds + word)));
             }
@@ -509,14 +534,12 @@ struct OperandRead {
 // PERSISTENT: one workgroup per place on the chip works through many tiles;
 // the first copies of the next tile are issued before the epilogue of this
 // one, whose rows pass through LDS of their own.
-template <int BM_, int BN_, int BK_, int WM_, int WN_, int STAGES_, int MIN_WAVES_, bool PERSISTENT_ = false>
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int MIN_WAVES_, bool PERSISTENT_ = false>
 struct LinearShape {
     static constexpr bool PERSISTENT = PERSISTENT_;
-    static constexpr int COPY_SHARE = 4;  // eighths of a tile's copies issued in the last step of the tile before
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_, MIN_WAVES = MIN_WAVES_;
-    static constexpr int BK = BK_;
     static constexpr int WAVES_N = BN / WN, THREADS = BM / WM * WAVES_N * kWave;
-    static constexpr int MI = WM / 32, NI = WN / 32;
+    static constexpr int MI = WM / 16, NI = WN / 16;
 };
 
 // Consecutive tiles on one XCD (workgroups go to the eight XCDs in turn), in
@@ -599,13 +622,19 @@ __device__ inline LinearWork linear_work(const LinearProblem& p, uint32_t tile, 
 }
 
 // One BM x BN output tile (of a slice of the contraction, or of a group) at a
-// time.  S LDS stages with one barrier per contraction tile: every wave has
-// read all of tile t by the barrier inside iteration t, so the copies of tile
-// t+S go into its stage from there on, spread over the MFMAs of that
-// iteration's last step and of the next iteration's first ones (COPY_SHARE).
-// The fragments of an MFMA step are read between the MFMAs of the step
-// before, the first of a tile between those of the last step of the tile
-// before it, after the barrier.
+// time, with one barrier per contraction tile: every wave has read all of tile
+// t by the barrier inside iteration t, before that iteration's last MFMA step,
+// and what is copied into the places it frees is issued between the MFMAs of
+// that step.  S LDS stages of both operands: there go the copies of tile t+S.
+// Persistent (the operands' tiles are of one size): a ring of five places for
+// A 0, B 0, A 1, B 1, A 2, ...; there go B of tile t+2 and A of tile t+3, so
+// that A's copies have two tiles' time to land and B's, issued first, one; the
+// fifth place serves the epilogue's rows while the next share's first two
+// tiles are on their way to the others.
+// The fragments of an MFMA step (16x16x32: the same products with 32x32x16
+// draw more power and ran at 1.80 against 2.03 PFLOP/s from registers) are
+// read between the MFMAs of the step before, the first of a tile between those
+// of the last step of the tile before it, after the barrier.
 // The MFMAs take B as their row operand, so a lane's four consecutive results
 // are four consecutive columns of one output row; each wave passes its
 // results through LDS, 16 or 32 rows at a time, to give every lane eight
@@ -613,25 +642,23 @@ __device__ inline LinearWork linear_work(const LinearProblem& p, uint32_t tile, 
 template <int TYPE, bool AK, bool BK_, class Shape, bool DIRECT>
 __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_kernel(LinearProblem, uint32_t tiles_m,
                                                                                    uint32_t tiles_n, uint32_t grid_y) {
-    using Op = Mfma16Op<TYPE, 32>;
-    static_assert(Shape::BK % 32 == 0, "steps alternate between two fragment buffers");
-    constexpr int BM = Shape::BM, BN = Shape::BN, BK = Shape::BK, S = DIRECT ? Shape::STAGES : 2;
-    constexpr int MI = Shape::MI, NI = Shape::NI, THREADS = Shape::THREADS, STEPS = BK / 16;
+    using Op = Mfma16Op<TYPE, 16>;
+    constexpr int BM = Shape::BM, BN = Shape::BN, BK = kDepth, S = DIRECT ? Shape::STAGES : 2;
+    constexpr int MI = Shape::MI, NI = Shape::NI, THREADS = Shape::THREADS, STEPS = BK / 32;
     constexpr bool PERSISTENT = Shape::PERSISTENT && DIRECT;
-    using OA = OperandTile<AK, BM, BK, S>;
-    using OB = OperandTile<BK_, BN, BK, S>;
-    using TileA = typename OA::Tile;
-    using TileB = typename OB::Tile;
-    constexpr int OPERANDS = TileA::total_elems + TileB::total_elems;
-    constexpr int BR = PERSISTENT ? 16 : 32;  // rows that a wave stages at a time
+    using TileA = OperandTile<AK, BM, S>;
+    using TileB = OperandTile<BK_, BN, S>;
+    constexpr int RING = 5;
+    static_assert(!PERSISTENT || TileA::stage_words == TileB::stage_words, "the ring's places take either operand");
+    constexpr int OPERANDS = PERSISTENT ? RING * TileA::stage_words : TileA::total_words + TileB::total_words;
+    constexpr int BR = 16;  // rows that a wave stages at a time: one block of results
     constexpr int BLOCK_WORDS = BR * Shape::WN, STAGED = THREADS / kWave * BLOCK_WORDS;
-    static_assert(PERSISTENT || STAGED <= OPERANDS, "the staged blocks fit the operand stages");
-    constexpr int WORDS = OPERANDS + (PERSISTENT ? STAGED : 0);
+    static_assert(STAGED <= (PERSISTENT ? TileA::stage_words : OPERANDS), "the staged blocks fit");
 
-    __shared__ __attribute__((aligned(16))) uint32_t lds[WORDS];
-    poison_lds(lds, WORDS);
+    __shared__ __attribute__((aligned(16))) uint32_t lds[OPERANDS];
+    poison_lds(lds, OPERANDS);
     uint32_t* const lds_a = lds;
-    uint32_t* const lds_b = lds + TileA::total_elems;
+    uint32_t* const lds_b = lds + (PERSISTENT ? 0 : TileA::total_words);
 
     const int tid = threadIdx.x, every_lane = tid % kWave;
     const int every_wave = __builtin_amdgcn_readfirstlane(tid / kWave);
@@ -653,47 +680,32 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
     if (!find_work(id, w)) return;
 
     using acc_t = typename Op::acc_t;
-    using CA = OperandCopy<AK, BM, BK, S, THREADS>;
-    using CB = OperandCopy<BK_, BN, BK, S, THREADS>;
+    using CA = OperandCopy<AK, BM, S, THREADS>;
+    using CB = OperandCopy<BK_, BN, S, THREADS>;
     constexpr int COPIES = CA::PER_WAVE + CB::PER_WAVE;
-    constexpr int EARLY = (COPIES * Shape::COPY_SHARE + 7) / 8;  // copies issued in the last step
-    // The first copies of a share: its first S-1 contraction tiles and the early ones of the next.
+    // The first copies of a share.
     auto start_copies = [&](const LinearWork& w) {
         if constexpr (DIRECT) {
             const LinearProblem p = problem_again();
             const int lane = afresh(every_lane), wave = afresh_uniform(every_wave);
-            const CA copy_a(w.A, p.lda, w.m_end - w.m0, w.L, wave, lane);
-            const CB copy_b(w.B, p.ldb, p.C - w.n0, w.L, wave, lane);
+            CA copy_a(w.A, p.lda, w.m_end - w.m0, w.L, wave, lane);
+            CB copy_b(w.B, p.ldb, p.C - w.n0, w.L, wave, lane);
 #pragma unroll
-            for (int s = 0; s < S - 1; ++s) {
-                copy_a.issue(s, w.L - s * BK, lds_a, s);
-                copy_b.issue(s, w.L - s * BK, lds_b, s);
+            for (int s = 0; s < S; ++s) {
+                copy_a.issue(lds_a, PERSISTENT ? 2 * s : s);
+                copy_b.issue(lds_b, PERSISTENT ? 2 * s + 1 : s);
+                copy_a.next();
+                copy_b.next();
             }
-            const auto a = copy_a.tile(S - 1, w.L - (S - 1) * BK, lds_a, S - 1);
-            const auto b = copy_b.tile(S - 1, w.L - (S - 1) * BK, lds_b, S - 1);
-            static_for<EARLY>([&](auto X_) {
-                constexpr int X = decltype(X_)::value;
-                if constexpr (X < CA::PER_WAVE)
-                    a(X);
-                else
-                    b(X - CA::PER_WAVE);
-            });
         }
     };
     start_copies(w);
-    bool landed = false;  // the first copies of this share are known to have landed
 
     for (;;) {
         const int lane = afresh(every_lane), wave = afresh_uniform(every_wave);
         const int wm0 = wave / Shape::WAVES_N * Shape::WM, wn0 = wave % Shape::WAVES_N * Shape::WN;
-        const OperandRead<OA, AK, MI, STEPS> read_a(wm0, lane);
-        const OperandRead<OB, BK_, NI, STEPS> read_b(wn0, lane);
-        auto read_fragments = [&](int stage, int st, u32x4 (&af)[MI], u32x4 (&bf)[NI]) {
-#pragma unroll
-            for (int i = 0; i < MI; ++i) af[i] = read_a.read(lds_a, stage, st, i);
-#pragma unroll
-            for (int j = 0; j < NI; ++j) bf[j] = read_b.read(lds_b, stage, st, j);
-        };
+        const OperandRead<TileA, AK, MI> read_a(wm0, lane);
+        const OperandRead<TileB, BK_, NI> read_b(wn0, lane);
         const int64_t T = w.L > 0 ? (w.L + BK - 1) / BK : 0;
         acc_t acc[MI][NI];
 #pragma unroll
@@ -702,64 +714,87 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
             for (int j = 0; j < NI; ++j)
 #pragma unroll
                 for (int v = 0; v < Op::ACC; ++v) acc[i][j][v] = 0.0f;
-        u32x4 af[2][MI], bf[2][NI];
+        // Fragments: A's of the step after replace this step's as each has been multiplied, B's alternate.
+        u32x4 af[MI], bf[2][NI];
+        auto read_first = [&](int place_a, int place_b) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i) af[i] = read_a.read(lds_a, place_a, 0, i);
+#pragma unroll
+            for (int j = 0; j < NI; ++j) bf[0][j] = read_b.read(lds_b, place_b, 0, j);
+        };
 
         if constexpr (DIRECT) {
             const LinearProblem p = problem_again();
-            const CA copy_a(w.A, p.lda, w.m_end - w.m0, w.L, wave, lane);
-            const CB copy_b(w.B, p.ldb, p.C - w.n0, w.L, wave, lane);
-            if (!landed) wait_vector_memory_at_most<(S - 2) * COPIES + EARLY>();
+            CA copy_a(w.A, p.lda, w.m_end - w.m0, w.L, wave, lane);
+            CB copy_b(w.B, p.ldb, p.C - w.n0, w.L, wave, lane);
+#pragma unroll
+            for (int s = 0; s < S; ++s) {  // (issued by start_copies)
+                copy_a.next();
+                copy_b.next();
+            }
+            // A persistent workgroup waits for its last epilogue's stores as well: left pending, they would make the
+            // compiler wait for all copies inside the K loop.
+            if (PERSISTENT)
+                wait_vector_memory();
+            else
+                wait_vector_memory_at_most<(S - 1) * COPIES>();
             __syncthreads();
-            int s = 0;  // stage of tile t
-            // the copies being issued: those of tile t+S-1, then of t+S
-            auto issue_a = copy_a.tile(S - 1, w.L - (S - 1) * BK, lds_a, S - 1);
-            auto issue_b = copy_b.tile(S - 1, w.L - (S - 1) * BK, lds_b, S - 1);
-            if (T > 0) read_fragments(0, 0, af[0], bf[0]);
+            int at_a = 0, at_b = PERSISTENT ? 1 : 0;  // places of tile t
+            if constexpr (PERSISTENT) {
+                copy_a.issue(lds_a, 4);
+                copy_a.next();
+            }
+            if (T > 0) read_first(at_a, at_b);
             for (int64_t t = 0; t < T; ++t) {
-                const int next = s + 1 == S ? 0 : s + 1;
+                // places of tile t+1
+                const int next_a = PERSISTENT ? (at_a >= RING - 2 ? at_a + 2 - RING : at_a + 2) : at_a + 1 == S ? 0 : at_a + 1;
+                const int next_b = PERSISTENT ? (at_b >= RING - 2 ? at_b + 2 - RING : at_b + 2) : next_a;
                 static_for<STEPS>([&](auto ST_) {
                     constexpr int ST = decltype(ST_)::value, NOW = ST & 1, THEN = NOW ^ 1;
                     constexpr bool LAST = ST + 1 == STEPS;
-                    // this step's copies: [FROM, TO) of the list A's then B's
-                    constexpr int REST = COPIES - EARLY, OVER = STEPS > 2 ? 2 : 1;
-                    constexpr int FROM = LAST ? 0 : ST < OVER ? EARLY + REST * ST / OVER : COPIES;
-                    constexpr int TO = LAST ? EARLY : ST < OVER ? EARLY + REST * (ST + 1) / OVER : COPIES;
-                    constexpr int ITEMS = MI + NI + TO - FROM;
+                    const int from_a = LAST ? next_a : at_a, from_b = LAST ? next_b : at_b;
                     if constexpr (LAST) {
-                        wait_vector_memory_at_most<(S - 2) * COPIES>();
+                        wait_vector_memory_at_most<PERSISTENT ? CA::PER_WAVE : (S - 2) * COPIES>();
                         __syncthreads();
-                        issue_a = copy_a.tile(t + S, w.L - (t + S) * BK, lds_a, s);
-                        issue_b = copy_b.tile(t + S, w.L - (t + S) * BK, lds_b, s);
                     }
+                    const auto issue_b = copy_b.tile(lds_b, PERSISTENT ? at_a : at_b);
+                    const auto issue_a = copy_a.tile(lds_a, PERSISTENT ? at_b : at_a);
                     __builtin_amdgcn_sched_barrier(0);
-                    static_for<MI * NI>([&](auto Q_) {
-                        constexpr int Q = decltype(Q_)::value, I = Q / NI, J = Q % NI;
-                        acc[I][J] = Op::mma(bf[NOW][J], af[NOW][I], acc[I][J]);
-                        static_for<ITEMS>([&](auto X_) {
-                            constexpr int X = decltype(X_)::value;
-                            if constexpr (X * MI * NI / ITEMS == Q) {
-                                if constexpr (X < NI)
-                                    bf[THEN][X] = read_b.read(lds_b, LAST ? next : s, LAST ? 0 : ST + 1, X);
-                                else if constexpr (X < NI + MI)
-                                    af[THEN][X - NI] = read_a.read(lds_a, LAST ? next : s, LAST ? 0 : ST + 1, X - NI);
-                                else if constexpr (FROM + X - NI - MI < CA::PER_WAVE)
-                                    issue_a(FROM + X - NI - MI);
-                                else
-                                    issue_b(FROM + X - NI - MI - CA::PER_WAVE);
-                            }
+                    static_for<MI>([&](auto I_) {
+                        constexpr int I = decltype(I_)::value;
+                        static_for<NI>([&](auto J_) {
+                            constexpr int J = decltype(J_)::value, Q = I * NI + J;
+                            acc[I][J] = Op::mma(bf[NOW][J], af[I], acc[I][J]);
+                            if constexpr (Q % 2 == 0 && Q / 2 < NI)
+                                bf[THEN][Q / 2] = read_b.read(lds_b, from_b, LAST ? 0 : ST + 1, Q / 2);
+                            if constexpr (LAST)
+                                static_for<COPIES>([&](auto X_) {
+                                    constexpr int X = decltype(X_)::value;
+                                    if constexpr (X * MI * NI / COPIES == Q) {
+                                        if constexpr (X < CB::PER_WAVE)
+                                            issue_b(X);
+                                        else
+                                            issue_a(X - CB::PER_WAVE);
+                                    }
+                                });
+                            __builtin_amdgcn_sched_barrier(0);
                         });
+                        af[I] = read_a.read(lds_a, from_a, LAST ? 0 : ST + 1, I);
                         __builtin_amdgcn_sched_barrier(0);
                     });
                 });
-                s = next;
+                copy_a.next();
+                copy_b.next();
+                at_a = next_a;
+                at_b = next_b;
             }
             wait_vector_memory();  // (copies past the last tile, which write zeros)
         } else {
             // Two stages; the loads of tile t+1 are issued before the
             // multiply of tile t and stored to LDS after it.
             const LinearProblem p = problem_again();
-            OperandLoad<AK, BM, BK, S, THREADS> load_a(w.A, p.lda, w.m_end - w.m0);
-            OperandLoad<BK_, BN, BK, S, THREADS> load_b(w.B, p.ldb, p.C - w.n0);
+            OperandLoad<AK, BM, S, THREADS> load_a(w.A, p.lda, w.m_end - w.m0);
+            OperandLoad<BK_, BN, S, THREADS> load_b(w.B, p.ldb, p.C - w.n0);
             if (T > 0) {
                 load_a.load(0, w.L, tid);
                 load_b.load(0, w.L, tid);
@@ -773,15 +808,20 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
                     load_a.load(t + 1, w.L - (t + 1) * BK, tid);
                     load_b.load(t + 1, w.L - (t + 1) * BK, tid);
                 }
-                read_fragments(s, 0, af[0], bf[0]);
+                read_first(s, s);
+                static_for<STEPS>([&](auto ST_) {
+                    constexpr int ST = decltype(ST_)::value, NOW = ST & 1, THEN = NOW ^ 1;
+                    if constexpr (ST + 1 < STEPS) {
 #pragma unroll
-                for (int st = 0; st < STEPS; ++st) {
-                    if (st + 1 < STEPS) read_fragments(s, st + 1, af[(st + 1) & 1], bf[(st + 1) & 1]);
+                        for (int j = 0; j < NI; ++j) bf[THEN][j] = read_b.read(lds_b, s, ST + 1, j);
+                    }
 #pragma unroll
-                    for (int i = 0; i < MI; ++i)
+                    for (int i = 0; i < MI; ++i) {
 #pragma unroll
-                        for (int j = 0; j < NI; ++j) acc[i][j] = Op::mma(bf[st & 1][j], af[st & 1][i], acc[i][j]);
-                }
+                        for (int j = 0; j < NI; ++j) acc[i][j] = Op::mma(bf[NOW][j], af[i], acc[i][j]);
+                        if constexpr (ST + 1 < STEPS) af[i] = read_a.read(lds_a, s, ST + 1, i);
+                    }
+                });
                 if (t + 1 < T) {
                     load_a.store(lds_a, s ^ 1, tid);
                     load_b.store(lds_b, s ^ 1, tid);
@@ -806,7 +846,7 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
         const LinearProblem p = problem_again();
         constexpr int LANES = Shape::WN / 8, ROWS = kWave / LANES, PARTS = BR / ROWS;
         const int out_lane = afresh(every_lane), r = out_lane / LANES, c = out_lane % LANES * 8;
-        float* const staged = reinterpret_cast<float*>(lds) + (PERSISTENT ? OPERANDS : 0) + wave * BLOCK_WORDS;
+        float* const staged = reinterpret_cast<float*>(lds) + (PERSISTENT ? 4 * TileA::stage_words : 0) + wave * BLOCK_WORDS;
         auto staged_at = [&](int row, int group16) {
             return staged + row * Shape::WN + 4 * (group16 ^ (((row & 1) << 2) | ((row >> 1) & 3)));
         };
@@ -833,23 +873,16 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
                 Row8 next_residual{};
                 if (m + 1 < Shape::WM / ROWS) next_residual = read_residual(m + 1);
                 if (m % PARTS == 0) {
-                    const int k = m / PARTS;  // the staged block
+                    const int k = m / PARTS;  // the block of results to stage
                     wave_fence();
                     // Only this choice of registers is unrolled; the comments keep the compiler from merging the
                     // choices into one sequence behind copies of all of a block's registers.
                     static_for<MI>([&](auto I_) {
                         constexpr int I = decltype(I_)::value;
-                        if (k * BR / 32 != I) return;
-                        if (BR == 32 || out_lane % 32 / BR == k % (32 / BR)) {
+                        if (k != I) return;
 #pragma unroll
-                            for (int j = 0; j < NI; ++j)
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const acc_t& x = acc[I][j];
-                                    *reinterpret_cast<floatx4*>(staged_at(out_lane % BR, 8 * j + 2 * q + out_lane / 32)) =
-                                        floatx4{x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]};
-                                }
-                        }
+                        for (int j = 0; j < NI; ++j)
+                            *reinterpret_cast<acc_t*>(staged_at(out_lane % 16, 4 * j + out_lane / 16)) = acc[I][j];
                         asm volatile("; rows %0" ::"i"(I) : "memory");
                     });
                     wave_fence();
@@ -861,9 +894,6 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
 #pragma unroll
                     for (int e = 0; e < 4; ++e) z[4 * g + e] = x[e];
                 }
-                // Before the last stores, so that the next share's copies are known to have landed without waiting
-                // for those stores.
-                if (PERSISTENT && m + 1 == Shape::WM / ROWS) wait_vector_memory();
                 if (inside(m)) {
                     if (w.partial)
                         store8(w.partial + (tile_row + m * ROWS + r) * p.C + tile_col + c, z, left);
@@ -879,7 +909,6 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
             finish(std::false_type{});
         if (!more) return;
         w = then;
-        landed = true;
     }
 }
 

@@ -16,18 +16,18 @@ struct TileSize {
     int bm, bn;
 };
 constexpr TileSize kTileSizes[kTileCount] = {{256, 256}, {128, 128}, {64, 64}, {32, 128}};
-constexpr int kTileDepth = 64;  // contraction elements per tile
+constexpr int kTileDepth = kDepth;  // contraction elements per tile
 
 template <int TILE>
 struct ShapeOf;
 template <>
-struct ShapeOf<kTile256> { using type = LinearShape<256, 256, 64, 128, 64, 2, 2, true>; };
+struct ShapeOf<kTile256> { using type = LinearShape<256, 256, 128, 64, 2, 2, true>; };
 template <>
-struct ShapeOf<kTile128> { using type = LinearShape<128, 128, 64, 64, 64, 2, 2>; };
+struct ShapeOf<kTile128> { using type = LinearShape<128, 128, 64, 64, 2, 2>; };
 template <>
-struct ShapeOf<kTile64> { using type = LinearShape<64, 64, 64, 32, 32, 4, 2>; };
+struct ShapeOf<kTile64> { using type = LinearShape<64, 64, 32, 32, 4, 2>; };
 template <>
-struct ShapeOf<kTile32x128> { using type = LinearShape<32, 128, 64, 32, 32, 4, 2>; };
+struct ShapeOf<kTile32x128> { using type = LinearShape<32, 128, 32, 32, 4, 2>; };
 
 // Which operands run along the contraction.
 enum LinearLayout { kForward = 0, kGradA = 1, kGradB = 2 };
