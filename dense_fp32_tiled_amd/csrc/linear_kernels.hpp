@@ -241,44 +241,57 @@ __device__ inline void store8(float* p, const float (&v)[8], int64_t in_range) {
 }
 
 // The epilogue of eight consecutive columns of one output row.  `bias` and
-// `residual` (of 16 bits) have been read ahead, so that they are on their way
-// while earlier columns are finished; an fp32 residual is read here.  Element
-// offsets: those of the eight in the output, the residual and the
-// pre-activation; `left` of them lie inside the matrix.
+// `residual` (of 16 bits) have been read before; an fp32 residual is read
+// here.  Addresses are a uniform base and a lane's byte offset, which the
+// loads and stores take as they are; `left` of the columns lie inside the
+// matrix.
+struct EpilogueBase {
+    char *out, *preact;
+    const char* residual;
+};
+struct EpilogueLane {
+    uint32_t out, preact, residual;
+};
+__device__ inline EpilogueBase epilogue_base(const LinearEpilogue& ep, int64_t group, int64_t row, int64_t col) {
+    const int64_t bytes = ep.out_f32 ? 4 : 2;
+    return EpilogueBase{static_cast<char*>(ep.out) + bytes * (group * ep.out_group + row * ep.ldo + col),
+                        reinterpret_cast<char*>(ep.preact) + 2 * (row * ep.ldp + col),
+                        static_cast<const char*>(ep.residual) + bytes * (row * ep.ldr + col)};
+}
+__device__ inline EpilogueLane epilogue_lane(const LinearEpilogue& ep, int row, int col) {
+    const uint32_t bytes = ep.out_f32 ? 4 : 2;
+    return EpilogueLane{bytes * (row * (uint32_t)ep.ldo + col), 2 * (row * (uint32_t)ep.ldp + col),
+                        bytes * (row * (uint32_t)ep.ldr + col)};
+}
 __device__ inline Row8 bias_reads(const LinearEpilogue& ep, int64_t at, int64_t left) {
     return ep.bias ? load8(ep.bias + at, left) : Row8{};
 }
-__device__ inline Row8 residual_reads(const LinearEpilogue& ep, int64_t at, int64_t left) {
+__device__ inline Row8 residual_reads(const LinearEpilogue& ep, const EpilogueBase& base, const EpilogueLane& lane,
+                                      int64_t left) {
     if (!ep.residual || ep.out_f32) return Row8{};
-    return load8(static_cast<const uint16_t*>(ep.residual) + at, left);
+    return load8(reinterpret_cast<const uint16_t*>(base.residual + lane.residual), left);
 }
-struct EpilogueAt {
-    int64_t out, residual, preact;
-};
 template <int TYPE>
-__device__ inline void epilogue8(const LinearEpilogue& ep, const Row8& bias, const Row8& residual, const EpilogueAt& at,
-                                 int64_t left, float (&z)[8]) {
-    if (ep.bias) {
-        float b[8];
-        bias.widen<TYPE>(b);
+__device__ inline void epilogue8(const LinearEpilogue& ep, const Row8& bias, const Row8& residual,
+                                 const EpilogueBase& base, const EpilogueLane& lane, int64_t left, float (&z)[8]) {
+    float add[8];
+    bias.widen<TYPE>(add);  // (zeros without a bias, and so for the residual: an addition is less than a branch)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] += b[e];
-    }
-    if (ep.preact) store8(ep.preact + at.preact, Row8::narrow<TYPE>(z), left);
+    for (int e = 0; e < 8; ++e) z[e] += add[e];
+    if (ep.preact) store8(reinterpret_cast<uint16_t*>(base.preact + lane.preact), Row8::narrow<TYPE>(z), left);
     act_values(z, ep.act);
-    if (ep.residual) {
-        float r[8];
-        if (ep.out_f32)
-            load8(r, static_cast<const float*>(ep.residual) + at.residual, left);
-        else
-            residual.widen<TYPE>(r);
+    residual.widen<TYPE>(add);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] += r[e];
+    for (int e = 0; e < 8; ++e) z[e] += add[e];
+    if (ep.residual && ep.out_f32) {
+        load8(add, reinterpret_cast<const float*>(base.residual + lane.residual), left);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] += add[e];
     }
     if (ep.out_f32)
-        store8(static_cast<float*>(ep.out) + at.out, z, left);
+        store8(reinterpret_cast<float*>(base.out + lane.out), z, left);
     else
-        store8(static_cast<uint16_t*>(ep.out) + at.out, Row8::narrow<TYPE>(z), left);
+        store8(reinterpret_cast<uint16_t*>(base.out + lane.out), Row8::narrow<TYPE>(z), left);
 }
 
 // ---- groups of rows -----------------------------------------------------------------
@@ -580,6 +593,12 @@ __device__ inline int afresh_uniform(int wave) {
     return wave;
 }
 
+// A uniform value, in scalar registers.
+__device__ inline int64_t scalar(int64_t v) {
+    const uint64_t lo = first_lane((uint32_t)v), hi = first_lane((uint32_t)((uint64_t)v >> 32));
+    return (int64_t)(lo | hi << 32);
+}
+
 // A workgroup's share of the work: one output tile of one matrix, group or slice.
 struct LinearWork {
     int64_t m0, m_end, n0, group, L;
@@ -841,8 +860,8 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
 
         // The epilogue, BR rows of a wave's WN columns at a time: a lane has 8 columns of every ROWS-th row, and a
         // row's lanes cover whole 128-byte lines of a 16-bit output (64-byte pieces cost the stores up to a fifth more
-        // time).  The residual of the next rows is fetched while these are finished.  A tile wholly inside the matrix
-        // takes a copy of the code without masks.
+        // time).  A tile wholly inside the matrix takes a copy of the
+        // code without masks.
         const LinearProblem p = problem_again();
         constexpr int LANES = Shape::WN / 8, ROWS = kWave / LANES, PARTS = BR / ROWS;
         const int out_lane = afresh(every_lane), r = out_lane / LANES, c = out_lane % LANES * 8;
@@ -850,57 +869,63 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
         auto staged_at = [&](int row, int group16) {
             return staged + row * Shape::WN + 4 * (group16 ^ (((row & 1) << 2) | ((row >> 1) & 3)));
         };
-        const int64_t tile_row = w.m0 + wm0, tile_col = w.n0 + wn0;  // (uniform)
-        const EpilogueAt lane_at{r * p.ep.ldo + c, r * p.ep.ldr + c, r * p.ep.ldp + c};
+        const int64_t tile_row = scalar(w.m0 + wm0), tile_col = scalar(w.n0 + wn0), group = scalar(w.group);
         auto finish = [&](auto WHOLE_) {
             constexpr bool WHOLE = decltype(WHOLE_)::value;
             const int64_t left = WHOLE ? (int64_t)8 : p.C - (tile_col + c);
             // part m: rows r, r + 1, ... of the wave's tile from m * ROWS on
             auto inside = [&](int m) { return WHOLE || (left > 0 && tile_row + m * ROWS + r < w.m_end); };
-            auto at = [&](int m) {
-                const int64_t row = tile_row + m * ROWS;
-                return EpilogueAt{row * p.ep.ldo + tile_col + w.group * p.ep.out_group + lane_at.out,
-                                  row * p.ep.ldr + tile_col + lane_at.residual,
-                                  row * p.ep.ldp + tile_col + lane_at.preact};
+            auto base = [&](int m) { return epilogue_base(p.ep, group, tile_row + m * ROWS, tile_col); };
+            auto read_residual = [&](int m, const EpilogueLane& lane_at) {
+                return !w.partial && inside(m) ? residual_reads(p.ep, base(m), lane_at, left) : Row8{};
             };
-            auto read_residual = [&](int m) {
-                return !w.partial && inside(m) ? residual_reads(p.ep, at(m).residual, left) : Row8{};
-            };
-            Row8 bias{}, residual = read_residual(0);
-            if (!w.partial && left > 0) bias = bias_reads(p.ep, w.group * p.ep.bias_group + tile_col + c, left);
+            Row8 bias{};
+            if (!w.partial && left > 0) bias = bias_reads(p.ep, group * p.ep.bias_group + tile_col + c, left);
+            // The residual is read for a group of parts at a time: loads and stores complete in order, so a load
+            // waits for every store before it.
+            constexpr int ALL = Shape::WM / ROWS, GROUP = WHOLE ? (ALL < 4 ? ALL : 4) : 1;
 #pragma unroll 1
-            for (int m = 0; m < Shape::WM / ROWS; ++m) {
-                Row8 next_residual{};
-                if (m + 1 < Shape::WM / ROWS) next_residual = read_residual(m + 1);
-                if (m % PARTS == 0) {
-                    const int k = m / PARTS;  // the block of results to stage
-                    wave_fence();
-                    // Only this choice of registers is unrolled; the comments keep the compiler from merging the
-                    // choices into one sequence behind copies of all of a block's registers.
-                    static_for<MI>([&](auto I_) {
-                        constexpr int I = decltype(I_)::value;
-                        if (k != I) return;
+            for (int m0 = 0; m0 < ALL; m0 += GROUP) {
+                // (the lane's places and the bias afresh for each group: kept across the loop in all the forms they
+                // are used in, they would not fit beside the sums)
+                const int out_lane = afresh(every_lane), r = out_lane / LANES, c = out_lane % LANES * 8;
+                const EpilogueLane lane_at = epilogue_lane(p.ep, r, c);
+                asm volatile("" : "+v"(bias.w));
+                Row8 residual[GROUP];
 #pragma unroll
-                        for (int j = 0; j < NI; ++j)
-                            *reinterpret_cast<acc_t*>(staged_at(out_lane % 16, 4 * j + out_lane / 16)) = acc[I][j];
-                        asm volatile("; rows %0" ::"i"(I) : "memory");
-                    });
-                    wave_fence();
-                }
-                float z[8];
+                for (int u = 0; u < GROUP; ++u) residual[u] = read_residual(m0 + u, lane_at);
+                static_for<GROUP>([&](auto U_) {
+                    constexpr int U = decltype(U_)::value;
+                    const int m = m0 + U;
+                    if (U % PARTS == 0 && (GROUP % PARTS == 0 || m % PARTS == 0)) {
+                        const int k = m / PARTS;  // the block of results to stage
+                        wave_fence();
+                        // Only this choice of registers is unrolled; the comments keep the compiler from merging the
+                        // choices into one sequence behind copies of all of a block's registers.
+                        static_for<MI>([&](auto I_) {
+                            constexpr int I = decltype(I_)::value;
+                            if (k != I) return;
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const floatx4 x = *reinterpret_cast<const floatx4*>(staged_at(r + ROWS * (m % PARTS), c / 4 + g));
+                            for (int j = 0; j < NI; ++j)
+                                *reinterpret_cast<acc_t*>(staged_at(out_lane % 16, 4 * j + out_lane / 16)) = acc[I][j];
+                            asm volatile("; rows %0" ::"i"(I) : "memory");
+                        });
+                        wave_fence();
+                    }
+                    float z[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) z[4 * g + e] = x[e];
-                }
-                if (inside(m)) {
-                    if (w.partial)
-                        store8(w.partial + (tile_row + m * ROWS + r) * p.C + tile_col + c, z, left);
-                    else
-                        epilogue8<TYPE>(p.ep, bias, residual, at(m), left, z);
-                }
-                residual = next_residual;
+                    for (int g = 0; g < 2; ++g) {
+                        const floatx4 x = *reinterpret_cast<const floatx4*>(staged_at(r + ROWS * (m % PARTS), c / 4 + g));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) z[4 * g + e] = x[e];
+                    }
+                    if (inside(m)) {
+                        if (w.partial)
+                            store8(w.partial + (tile_row + m * ROWS + r) * p.C + tile_col + c, z, left);
+                        else
+                            epilogue8<TYPE>(p.ep, bias, residual[U], base(m), lane_at, left, z);
+                    }
+                });
             }
         };
         if (w.m0 + BM <= w.m_end && w.n0 + BN <= p.C)
@@ -920,8 +945,9 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearProblem p) {
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
         const int64_t row = i / row_groups, col = i % row_groups * 8, left = p.C - col;
         const float* src = p.partial + row * p.C + col;
-        const EpilogueAt at{row * p.ep.ldo + col, row * p.ep.ldr + col, row * p.ep.ldp + col};
-        const Row8 bias = bias_reads(p.ep, col, left), residual = residual_reads(p.ep, at.residual, left);
+        const EpilogueBase base = epilogue_base(p.ep, 0, row, col);
+        const EpilogueLane none{0, 0, 0};
+        const Row8 bias = bias_reads(p.ep, col, left), residual = residual_reads(p.ep, base, none, left);
         float z[8];
         load8(z, src, left);
         for (int s = 1; s < p.splits; ++s) {
@@ -930,7 +956,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearProblem p) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[e] += more[e];
         }
-        epilogue8<TYPE>(p.ep, bias, residual, at, left, z);
+        epilogue8<TYPE>(p.ep, bias, residual, base, none, left, z);
     }
 }
 
