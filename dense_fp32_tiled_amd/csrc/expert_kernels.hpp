@@ -223,14 +223,28 @@ __global__ __launch_bounds__(kRowWaves* kWave) void expert_combine_kernel(RowsPr
     const int64_t col = (int64_t)blockIdx.y * kRowCols + threadIdx.x % kWave * 8, left = p.cols - col;
     if (token >= p.tokens || left <= 0) return;
     float sum[8] = {};
-    for (int j = 0; j < p.top_k; ++j) {
-        const int64_t s = slot_of(p, token, j);
-        if (s < 0) continue;
-        const float w = p.weights ? p.weights[token * p.top_k + j] : 1.0f;
-        float v[8];
-        load8(p.y + s * p.ldy + col, left).widen<TYPE>(v);
+    // four choices at a time: their positions, then their rows, are on their way together
+    for (int j0 = 0; j0 < p.top_k; j0 += 4) {
+        int64_t slot[4];
+        float w[4];
+        Row8 row[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += w * v[e];
+        for (int j = 0; j < 4; ++j) {
+            const bool there = j0 + j < p.top_k;
+            slot[j] = there ? slot_of(p, token, j0 + j) : -1;
+            w[j] = there && p.weights ? p.weights[token * p.top_k + j0 + j] : 1.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (slot[j] >= 0) row[j] = load8(p.y + slot[j] * p.ldy + col, left);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (slot[j] < 0) continue;
+            float v[8];
+            row[j].widen<TYPE>(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += w[j] * v[e];
+        }
     }
     store8(p.out + token * p.ldo + col, Row8::narrow<TYPE>(sum), left);
 }

@@ -99,6 +99,7 @@ struct Plan {
     bool direct;
     int splits;
     int64_t slice;
+    double us;  // as estimated
 };
 
 // Full-chip rates of the tiles (TFLOP/s, one type) and workgroups per CU.
@@ -137,8 +138,7 @@ double estimate(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, Linea
 }
 
 Plan choose(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, bool direct, int variant, int splits, int cus) {
-    Plan best{kTile128, direct, 1, L};
-    double least = 1e300;
+    Plan best{kTile128, direct, 1, L, 1e300};
     for (int t = 0; t < kTileCount; ++t) {
         if (variant != GEMM_LINEAR_AUTO && t != variant - 1) continue;
         LinearTile tile = (LinearTile)t;
@@ -156,10 +156,7 @@ Plan choose(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, bool dire
                 use = (int)ceil_div(L, slice);
             }
             const double us = estimate(R, C, L, groups, axis, tile, direct, use, cus);
-            if (us < least) {
-                least = us;
-                best = Plan{tile, direct, std::max(use, 1), slice};
-            }
+            if (us < best.us) best = Plan{tile, direct, std::max(use, 1), slice, us};
             if (splits > 0 || axis != kGroupNone || L == 0) break;
         }
     }
@@ -193,11 +190,11 @@ hipError_t launch(int type, const LinearProblem& p, LinearLayout layout, const P
                              : launch_linear_f16(p, layout, plan.tile, plan.direct, tiles_m, tiles_n, grid_y, cus, stream);
     if (e != hipSuccess || plan.splits <= 1) return e;
     LinearProblem problem = p;
-    const int64_t blocks = std::min<int64_t>(ceil_div(p.R * ceil_div(p.C, 8), 256), 16384);
+    const int64_t blocks = std::min<int64_t>(ceil_div(p.R * ceil_div(p.C, 8), kJoinGroups), 16384);
     void* args[] = {&problem};
     const void* join = type == GEMM_INPUT_BF16 ? reinterpret_cast<const void*>(linear_join_kernel<kInputBf16>)
                                                : reinterpret_cast<const void*>(linear_join_kernel<kInputF16>);
-    return hipLaunchKernel(join, dim3((unsigned)blocks), dim3(256), args, 0, stream);
+    return hipLaunchKernel(join, dim3((unsigned)blocks), dim3(kJoinThreads), args, 0, stream);
 }
 
 // ---- gemm_linear ----------------------------------------------------------------------
@@ -214,6 +211,49 @@ bool copies_fit(LinearTile tile, const Matrix& a, bool a_kmajor, const Matrix& b
 bool direct_ok(const Matrix& a, bool a_kmajor, const Matrix& b, bool b_kmajor) {
     return a.aligned16() && b.aligned16() && a.cols % 8 == 0 && b.cols % 8 == 0 &&
            copies_fit(kTile256, a, a_kmajor, b, b_kmajor);
+}
+
+// An operand as the products read it: itself, or packed to rows of whole 16
+// bytes in the workspace.
+bool whole_rows(const Matrix& m) { return m.aligned16() && m.cols % 8 == 0; }
+Matrix packed(const Matrix& m) {
+    Matrix r = m;
+    r.ld = ceil_div(std::max<int64_t>(m.cols, 1), 8) * 8;
+    r.copy_stride = m.rows * r.ld;
+    r.data = nullptr;  // (placed when the workspace is known)
+    return r;
+}
+int64_t packed_bytes(const Matrix& m) { return ceil_div(2 * m.copies * m.rows * packed(m).ld, 256) * 256; }
+// Reading and writing every element once at 4 TB/s, beside the launch.
+double pack_us(const Matrix& m) { return 2.0 * (double)packed_bytes(m) / 4e6; }
+
+// Workspace cut into 256-byte pieces from its start.
+struct Space {
+    char* at;
+    void* take(int64_t bytes) {
+        void* p = at;
+        at += ceil_div(bytes, 256) * 256;
+        return p;
+    }
+};
+
+int launch_pack(const Matrix* from, Matrix* to, int n, Space* space, hipStream_t stream) {
+    PackJobs jobs{};
+    int64_t most = 1;
+    for (int i = 0; i < n; ++i) {
+        to[i] = packed(from[i]);
+        to[i].data = space->take(packed_bytes(from[i]));
+        jobs.job[i] = PackJob{static_cast<const uint16_t*>(from[i].data), from[i].rows, from[i].cols, from[i].ld,
+                              from[i].copies, from[i].copy_stride,
+                              static_cast<uint16_t*>(const_cast<void*>(to[i].data)), to[i].ld};
+        most = std::max(most, from[i].copies * from[i].rows * (to[i].ld / 8));
+    }
+    void* args[] = {&jobs};
+    const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(most, 256), 65536);
+    return hipLaunchKernel(reinterpret_cast<const void*>(linear_pack_kernel<0>), dim3(blocks, (unsigned)n), dim3(256),
+                           args, 0, stream) == hipSuccess
+               ? GEMM_OK
+               : GEMM_ERR_HIP;
 }
 
 struct LinearCall {
@@ -249,8 +289,32 @@ int describe(const gemm_linear_args& a, LinearCall* c) {
     return check_matrices(uses, 8);
 }
 
-Plan plan_linear(const gemm_linear_args& a, const LinearCall& c, int cus) {
-    return choose(a.M, a.N, a.K, c.groups, c.axis, direct_ok(c.A, true, c.B, false), a.variant, a.splits, cus);
+// The operands as they are, or, where their rows are not whole 16 bytes and
+// the product is large enough to win the copies' time back, packed.
+struct LinearPlan {
+    Plan plan;
+    bool pack_a, pack_b;
+    int64_t workspace;  // bytes
+};
+LinearPlan plan_linear(const gemm_linear_args& a, const LinearCall& c, int cus) {
+    LinearPlan best{choose(a.M, a.N, a.K, c.groups, c.axis, direct_ok(c.A, true, c.B, false), a.variant, a.splits, cus),
+                    false, false, 0};
+    if (!best.plan.direct && a.K > 0) {
+        const bool pack_a = !whole_rows(c.A), pack_b = !whole_rows(c.B);
+        const Matrix A = pack_a ? packed(c.A) : c.A, B = pack_b ? packed(c.B) : c.B;
+        if (copies_fit(kTile256, A, true, B, false)) {
+            const Plan p = choose(a.M, a.N, a.K, c.groups, c.axis, true, a.variant, a.splits, cus);
+            const double us = p.us + 2.5 + (pack_a ? pack_us(c.A) : 0) + (pack_b ? pack_us(c.B) : 0);
+            if (us < best.plan.us) best = LinearPlan{p, pack_a, pack_b, 0};
+        }
+    }
+    best.workspace = (best.pack_a ? packed_bytes(c.A) : 0) + (best.pack_b ? packed_bytes(c.B) : 0) +
+                     partial_bytes(best.plan, a.M, a.N);
+    return best;
+}
+
+bool workspace_ok(int64_t need, const void* workspace, int64_t bytes) {
+    return need == 0 || (workspace && bytes >= need && ((uintptr_t)workspace & 15) == 0);
 }
 
 int run_linear(const gemm_linear_args& a, hipStream_t stream) {
@@ -261,17 +325,28 @@ int run_linear(const gemm_linear_args& a, hipStream_t stream) {
     int cus = 0;
     st = current_cus(&cus);
     if (st != GEMM_OK) return st;
-    const Plan plan = plan_linear(a, c, cus);
+    const LinearPlan chosen = plan_linear(a, c, cus);
+    const Plan& plan = chosen.plan;
     st = check_grid(plan, a.M, a.N, c.groups, c.axis);
     if (st != GEMM_OK) return st;
-    const int64_t need = partial_bytes(plan, a.M, a.N);
-    if (need > 0 && (!a.workspace || a.workspace_bytes < need || ((uintptr_t)a.workspace & 3))) return GEMM_ERR_WORKSPACE;
+    if (!workspace_ok(chosen.workspace, a.workspace, a.workspace_bytes)) return GEMM_ERR_WORKSPACE;
+    Space space{static_cast<char*>(a.workspace)};
+    Matrix A = c.A, B = c.B, from[2], to[2];
+    int n = 0;
+    if (chosen.pack_a) from[n++] = c.A;
+    if (chosen.pack_b) from[n++] = c.B;
+    if (n > 0) {
+        st = launch_pack(from, to, n, &space, stream);
+        if (st != GEMM_OK) return st;
+        if (chosen.pack_a) A = to[0];
+        if (chosen.pack_b) B = to[n - 1];
+    }
     LinearProblem p{};
     p.R = a.M; p.C = a.N; p.L = a.K;
-    p.A = static_cast<const uint16_t*>(a.A); p.lda = a.lda;
-    p.B = static_cast<const uint16_t*>(a.B); p.ldb = a.ldb; p.b_group = a.b_stride;
+    p.A = static_cast<const uint16_t*>(A.data); p.lda = A.ld;
+    p.B = static_cast<const uint16_t*>(B.data); p.ldb = B.ld; p.b_group = B.copy_stride;
     p.offsets = a.offsets; p.groups = (int32_t)c.groups; p.axis = c.axis;
-    p.splits = plan.splits; p.slice = plan.slice; p.partial = static_cast<float*>(a.workspace);
+    p.splits = plan.splits; p.slice = plan.slice; p.partial = reinterpret_cast<float*>(space.at);
     p.ep.bias = static_cast<const uint16_t*>(a.bias); p.ep.bias_group = a.bias_stride;
     p.ep.residual = a.residual; p.ep.ldr = a.ldr;
     p.ep.preact = static_cast<uint16_t*>(a.preact); p.ep.ldp = a.ldp;
@@ -316,33 +391,58 @@ int describe(const gemm_linear_grad_args& a, GradCall* c) {
     return check_matrices(uses, 10);
 }
 
-Plan plan_a(const gemm_linear_grad_args& a, const GradCall& c, int cus) {
-    return choose(a.M, a.K, a.N, c.groups, c.axis, direct_ok(c.slope(), true, c.B, true), GEMM_LINEAR_AUTO, 0, cus);
+Plan plan_a(const gemm_linear_grad_args& a, const GradCall& c, bool direct, int cus) {
+    return choose(a.M, a.K, a.N, c.groups, c.axis, direct, GEMM_LINEAR_AUTO, 0, cus);
 }
-Plan plan_b(const gemm_linear_grad_args& a, const GradCall& c, int cus) {
-    return choose(a.K, a.N, a.M, c.groups, c.axis == kGroupRows ? kGroupContraction : kGroupNone,
-                  direct_ok(c.A, false, c.slope(), false), GEMM_LINEAR_AUTO, 0, cus);
+Plan plan_b(const gemm_linear_grad_args& a, const GradCall& c, bool direct, int cus) {
+    return choose(a.K, a.N, a.M, c.groups, c.axis == kGroupRows ? kGroupContraction : kGroupNone, direct,
+                  GEMM_LINEAR_AUTO, 0, cus);
 }
 int64_t slope_chunks(const gemm_linear_grad_args& a, const GradCall& c) {
     return row_tiles(a.M, c.groups, c.axis, kSlopeRows);
 }
 
-// The workspace holds the column sums' chunks first and each product's
-// slices after them, one use at a time (the launches run in stream order).
-int64_t grad_workspace(const gemm_linear_grad_args& a, const GradCall& c, int cus) {
-    int64_t need = a.dbias ? slope_chunks(a, c) * a.N * 4 : 0;
-    if (a.dA) need = std::max(need, partial_bytes(plan_a(a, c, cus), a.M, a.K));
-    if (a.dB) need = std::max(need, partial_bytes(plan_b(a, c, cus), a.K, a.N));
-    return need;
+// Both products' plans, with dZ, A and B as they are or packed (one choice
+// for all that have rows of other than whole 16 bytes, dZ being read by both).
+// The workspace holds what is packed, then the column sums' chunks and each
+// product's slices, one after the other (the launches run in stream order).
+struct GradPlan {
+    Plan a, b;
+    bool pack_z, pack_a, pack_b;
+    int64_t workspace;
+};
+GradPlan plan_grad(const gemm_linear_grad_args& a, const GradCall& c, int cus) {
+    const Matrix dz = c.slope();
+    const bool want_a = a.dA && a.M > 0 && a.K > 0, want_b = a.dB && a.K > 0 && a.N > 0;
+    GradPlan best{plan_a(a, c, direct_ok(dz, true, c.B, true), cus), plan_b(a, c, direct_ok(c.A, false, dz, false), cus),
+                  false, false, false, 0};
+    const bool slow = (want_a && !best.a.direct) || (want_b && !best.b.direct);
+    if (slow && a.M > 0 && a.N > 0) {
+        const bool z = !whole_rows(dz), pa = want_b && !whole_rows(c.A), pb = want_a && !whole_rows(c.B);
+        const Matrix Z = z ? packed(dz) : dz, A = pa ? packed(c.A) : c.A, B = pb ? packed(c.B) : c.B;
+        if ((!want_a || copies_fit(kTile256, Z, true, B, true)) && (!want_b || copies_fit(kTile256, A, false, Z, false))) {
+            const Plan p = plan_a(a, c, true, cus), q = plan_b(a, c, true, cus);
+            const double before = (want_a ? best.a.us : 0) + (want_b ? best.b.us : 0);
+            const double after = (want_a ? p.us : 0) + (want_b ? q.us : 0) + 2.5 + (z ? pack_us(dz) : 0) +
+                                 (pa ? pack_us(c.A) : 0) + (pb ? pack_us(c.B) : 0);
+            if (after < before) best = GradPlan{p, q, z, pa, pb, 0};
+        }
+    }
+    int64_t rest = a.dbias ? slope_chunks(a, c) * a.N * 4 : 0;
+    if (want_a) rest = std::max(rest, partial_bytes(best.a, a.M, a.K));
+    if (want_b) rest = std::max(rest, partial_bytes(best.b, a.K, a.N));
+    best.workspace = (best.pack_z ? packed_bytes(dz) : 0) + (best.pack_a ? packed_bytes(c.A) : 0) +
+                     (best.pack_b ? packed_bytes(c.B) : 0) + rest;
+    return best;
 }
 
-int run_slope(const gemm_linear_grad_args& a, const GradCall& c, hipStream_t stream) {
+int run_slope(const gemm_linear_grad_args& a, const GradCall& c, float* partial, hipStream_t stream) {
     SlopeProblem p{};
     p.M = a.M; p.N = a.N;
     p.dY = static_cast<const uint16_t*>(a.dY); p.ldy = a.ldy;
     p.Z = static_cast<const uint16_t*>(c.Z.data); p.ldz = a.ldz;
     p.dZ = static_cast<uint16_t*>(const_cast<void*>(c.dZ.data)); p.lddz = a.lddz;
-    p.partial = a.dbias ? static_cast<float*>(a.workspace) : nullptr;
+    p.partial = a.dbias ? partial : nullptr;
     p.offsets = a.groups > 0 ? a.offsets : nullptr; p.groups = (int32_t)c.groups;
     p.act = a.activation; p.dbias = a.dbias;
     void* args[] = {&p};
@@ -369,22 +469,39 @@ int run_grad(const gemm_linear_grad_args& a, hipStream_t stream) {
     int cus = 0;
     st = current_cus(&cus);
     if (st != GEMM_OK) return st;
-    const int64_t need = grad_workspace(a, c, cus);
-    if (need > 0 && (!a.workspace || a.workspace_bytes < need || ((uintptr_t)a.workspace & 3))) return GEMM_ERR_WORKSPACE;
-    const Plan pa = plan_a(a, c, cus), pb = plan_b(a, c, cus);
+    const GradPlan plan = plan_grad(a, c, cus);
+    if (!workspace_ok(plan.workspace, a.workspace, a.workspace_bytes)) return GEMM_ERR_WORKSPACE;
+    const Plan &pa = plan.a, &pb = plan.b;
     const int axis_b = c.axis == kGroupRows ? kGroupContraction : kGroupNone;
     if (a.dA && (st = check_grid(pa, a.M, a.K, c.groups, c.axis)) != GEMM_OK) return st;
     if (a.dB && (st = check_grid(pb, a.K, a.N, c.groups, axis_b)) != GEMM_OK) return st;
     if (slope_chunks(a, c) > kMaxGrid / 256 || a.N > (int64_t)0xffff * 64) return GEMM_ERR_TOO_LARGE;
-    if (a.N > 0 && (c.dZ.data || a.dbias) && (st = run_slope(a, c, stream)) != GEMM_OK) return st;
-    const Matrix dz = c.slope();
+    Space space{static_cast<char*>(a.workspace)};
+    // places of what is packed, in front of the rest (its kernel runs after dZ's)
+    Matrix from[3], to[3], dz = c.slope(), A = c.A, B = c.B;
+    int n = 0;
+    if (plan.pack_z) from[n++] = dz;
+    if (plan.pack_a) from[n++] = c.A;
+    if (plan.pack_b) from[n++] = c.B;
+    Space rest = space;
+    for (int i = 0; i < n; ++i) rest.take(packed_bytes(from[i]));
+    if (a.N > 0 && (c.dZ.data || a.dbias) && (st = run_slope(a, c, reinterpret_cast<float*>(rest.at), stream)) != GEMM_OK)
+        return st;
+    if (n > 0) {
+        st = launch_pack(from, to, n, &space, stream);
+        if (st != GEMM_OK) return st;
+        int i = 0;
+        if (plan.pack_z) dz = to[i++];
+        if (plan.pack_a) A = to[i++];
+        if (plan.pack_b) B = to[i++];
+    }
     LinearProblem p{};
     p.offsets = a.offsets; p.groups = (int32_t)c.groups;
-    p.partial = static_cast<float*>(a.workspace);
+    p.partial = reinterpret_cast<float*>(rest.at);
     if (a.dA && a.M > 0 && a.K > 0) {
         p.R = a.M; p.C = a.K; p.L = a.N; p.axis = c.axis;
         p.A = static_cast<const uint16_t*>(dz.data); p.lda = dz.ld;
-        p.B = static_cast<const uint16_t*>(a.B); p.ldb = a.ldb; p.b_group = a.b_stride;
+        p.B = static_cast<const uint16_t*>(B.data); p.ldb = B.ld; p.b_group = B.copy_stride;
         p.splits = pa.splits; p.slice = pa.slice;
         p.ep = LinearEpilogue{};
         p.ep.out = a.dA; p.ep.ldo = a.ldda; p.ep.out_f32 = a.a_grad_type == GEMM_OUTPUT_F32;
@@ -392,7 +509,7 @@ int run_grad(const gemm_linear_grad_args& a, hipStream_t stream) {
     }
     if (a.dB && a.K > 0 && a.N > 0) {
         p.R = a.K; p.C = a.N; p.L = a.M; p.axis = axis_b;
-        p.A = static_cast<const uint16_t*>(a.A); p.lda = a.lda;
+        p.A = static_cast<const uint16_t*>(A.data); p.lda = A.ld;
         p.B = static_cast<const uint16_t*>(dz.data); p.ldb = dz.ld; p.b_group = 0;
         p.splits = pb.splits; p.slice = pb.slice;
         p.ep = LinearEpilogue{};
@@ -462,7 +579,7 @@ int64_t gemm_linear_workspace_bytes(const gemm_linear_args* args, int32_t num_cu
     LinearCall c;
     const int st = describe(a, &c);
     if (st != GEMM_OK) return st;
-    return a.M == 0 || a.N == 0 ? 0 : partial_bytes(plan_linear(a, c, num_cus), a.M, a.N);
+    return a.M == 0 || a.N == 0 ? 0 : plan_linear(a, c, num_cus).workspace;
 }
 
 int gemm_linear_choice(const gemm_linear_args* args, int32_t num_cus, int32_t* variant, int32_t* splits) {
@@ -471,7 +588,7 @@ int gemm_linear_choice(const gemm_linear_args* args, int32_t num_cus, int32_t* v
     LinearCall c;
     const int st = describe(*args, &c);
     if (st != GEMM_OK) return st;
-    const Plan plan = plan_linear(*args, c, num_cus);
+    const Plan plan = plan_linear(*args, c, num_cus).plan;
     *variant = plan.tile + 1;
     *splits = plan.splits;
     return GEMM_OK;
@@ -489,7 +606,7 @@ int64_t gemm_linear_grad_workspace_bytes(const gemm_linear_grad_args* args, int3
     a.workspace_bytes = 0;
     GradCall c;
     const int st = describe(a, &c);
-    return st != GEMM_OK ? st : grad_workspace(a, c, num_cus);
+    return st != GEMM_OK ? st : plan_grad(a, c, num_cus).workspace;
 }
 
 int64_t gemm_expert_sort_workspace_bytes(int64_t tokens, int32_t top_k, int32_t num_experts) {

@@ -422,7 +422,8 @@ struct OperandCopy {
     __device__ OperandCopy(const uint16_t* origin, int64_t ld, int64_t outs, int64_t length, int wave, int lane) {
         base = reinterpret_cast<const char*>(origin);
         const int64_t rows = KMAJOR ? outs : length, cols = KMAJOR ? length : outs;
-        size = rows > 0 && cols > 0 ? 2 * ((rows - 1) * ld + cols) : 0;
+        // (widths are multiples of 8, or packed rows padded to them)
+        size = rows > 0 && cols > 0 ? 2 * ((rows - 1) * ld + (cols + 7) / 8 * 8) : 0;
         const int row = wave * PIECE_ROWS + lane / Tile::row_groups;
         const int word = (lane % Tile::row_groups * 4) ^ Tile::swizzle(row);
         offset = (uint32_t)(2 * row * ld) + 4 * word;
@@ -937,26 +938,65 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
     }
 }
 
-// Sums the slices' partial products in ascending order and applies the
-// epilogue; eight columns per thread.
+// Sums the slices' partial products and applies the epilogue.  Four lanes per
+// eight columns: lane l adds slices l, l + 4, ... in ascending order, then the
+// four sums are added as (0 + 1) + (2 + 3), so that a few rows of many slices
+// are not one long chain of loads.
+constexpr int kJoinThreads = 256, kJoinGroups = kJoinThreads / 4;  // column groups per workgroup
+
 template <int TYPE>
-__global__ __launch_bounds__(256) void linear_join_kernel(LinearProblem p) {
-    const int64_t row_groups = (p.C + 7) / 8, total = p.R * row_groups;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t row = i / row_groups, col = i % row_groups * 8, left = p.C - col;
+__global__ __launch_bounds__(kJoinThreads) void linear_join_kernel(LinearProblem p) {
+    const int lane = threadIdx.x % kWave, slice0 = lane / 16;
+    const int64_t row_groups = (p.C + 7) / 8, total = p.R * row_groups, stride = p.R * p.C;
+    for (int64_t first = (int64_t)blockIdx.x * kJoinGroups + threadIdx.x / kWave * 16; first < total;
+         first += (int64_t)gridDim.x * kJoinGroups) {
+        const int64_t i = first + lane % 16;
+        const bool own = i < total;
+        const int64_t row = own ? i / row_groups : 0, col = own ? i % row_groups * 8 : 0, left = own ? p.C - col : 0;
         const float* src = p.partial + row * p.C + col;
         const EpilogueBase base = epilogue_base(p.ep, 0, row, col);
         const EpilogueLane none{0, 0, 0};
-        const Row8 bias = bias_reads(p.ep, col, left), residual = residual_reads(p.ep, base, none, left);
-        float z[8];
-        load8(z, src, left);
-        for (int s = 1; s < p.splits; ++s) {
+        Row8 bias{}, residual{};
+        if (slice0 == 0) {
+            bias = bias_reads(p.ep, col, left);
+            residual = residual_reads(p.ep, base, none, left);
+        }
+        float z[8] = {};
+#pragma unroll 4
+        for (int s = slice0; s < p.splits; s += 4) {
             float more[8];
-            load8(more, src + s * p.R * p.C, left);
+            load8(more, src + s * stride, left);
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[e] += more[e];
         }
-        epilogue8<TYPE>(p.ep, bias, residual, base, none, left, z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            z[e] += __shfl_xor(z[e], 16);
+            z[e] += __shfl_xor(z[e], 32);
+        }
+        if (slice0 == 0 && left > 0) epilogue8<TYPE>(p.ep, bias, residual, base, none, left, z);
+    }
+}
+
+// Copies matrices to rows of whole 16 bytes (zeros past their width): what
+// lets a product of unaligned operands run on direct copies.
+struct PackJob {
+    const uint16_t* src;
+    int64_t rows, cols, ld, copies, copy_stride;
+    uint16_t* dst;
+    int64_t ldd;  // a multiple of 8; copies lie rows * ldd apart
+};
+struct PackJobs {
+    PackJob job[3];
+};
+template <int TYPE>  // (one instance, as every kernel of this header is a template)
+__global__ __launch_bounds__(256) void linear_pack_kernel(PackJobs jobs) {
+    const PackJob& j = jobs.job[blockIdx.y];
+    const int64_t groups = j.ldd / 8, total = j.copies * j.rows * groups;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t at = i / groups, col = i % groups * 8, copy = at / j.rows, row = at % j.rows;
+        const Row8 v = load8(j.src + copy * j.copy_stride + row * j.ld + col, j.cols - col);
+        *reinterpret_cast<u32x4*>(j.dst + at * j.ldd + col) = v.w;
     }
 }
 

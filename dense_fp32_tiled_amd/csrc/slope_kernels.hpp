@@ -43,6 +43,7 @@ __global__ __launch_bounds__(256) void linear_slope_kernel(SlopeProblem p) {
     if (hi > lo + kSlopeRows) hi = lo + kSlopeRows;
     float sum[8] = {};
     if (left > 0) {
+#pragma unroll 4
         for (int64_t row = lo + r; row < hi; row += 8) {
             const Row8 dy = load8(p.dY + row * p.ldy + col, left);
             float d[8];
@@ -95,8 +96,10 @@ __global__ __launch_bounds__(256) void linear_bias_join_kernel(SlopeProblem p) {
     }
     const int64_t chunks = (rows + kSlopeRows - 1) / kSlopeRows;
     float sum = 0.0f;
-    if (col < p.N)
+    if (col < p.N) {
+#pragma unroll 8
         for (int64_t k = r; k < chunks; k += 4) sum += p.partial[(first + k) * p.N + col];
+    }
     sums[r][c] = sum;
     __syncthreads();
     if (r == 0 && col < p.N) p.dbias[group * p.N + col] = sums[0][c] + sums[1][c] + sums[2][c] + sums[3][c];

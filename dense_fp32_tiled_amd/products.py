@@ -123,13 +123,24 @@ def gemm_expert_combine_grad(input_type, tokens, rows, top_k, cols, dout, ldd, Y
 
 
 # ---- torch convenience --------------------------------------------------------------------
+# A single token's layer takes a few microseconds on the GPU, so what a call costs here counts: torch is bound on
+# first use (the package works without it), and every tensor is looked at once.
 _ACT_CODES = {name: code for code, name in ACT_NAMES.items()}
 _cus: dict[int, int] = {}
+torch = None
+_Tensor: type = type(None)
+_bf16 = _f16 = _f32 = _int32 = None
+
+
+def _bind():
+    global torch, _Tensor, _bf16, _f16, _f32, _int32
+    import torch as torch_
+
+    _Tensor, _bf16, _f16, _f32, _int32 = torch_.Tensor, torch_.bfloat16, torch_.float16, torch_.float32, torch_.int32
+    torch = torch_
 
 
 def _num_cus(device) -> int:
-    import torch
-
     n = _cus.get(device.index)
     if n is None:
         n = _cus[device.index] = torch.cuda.get_device_properties(device).multi_processor_count
@@ -137,15 +148,16 @@ def _num_cus(device) -> int:
 
 
 def _input_type(t, name):
-    import torch
-
-    if not isinstance(t, torch.Tensor):
+    if torch is None:
+        _bind()
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is torch.bfloat16:
+    dtype = t.dtype
+    if dtype is _bf16:
         return dft.INPUT_BF16
-    if t.dtype is torch.float16:
+    if dtype is _f16:
         return dft.INPUT_F16
-    raise TypeError(f"{name} must be bfloat16 or float16, not {t.dtype}")
+    raise TypeError(f"{name} must be bfloat16 or float16, not {dtype}")
 
 
 def _act_code(activation):
@@ -155,51 +167,44 @@ def _act_code(activation):
     return code
 
 
-def _matrix(t, name, shape, dtype, device):
-    """(device pointer, row pitch) of a 2-D tensor of that shape, type and device, rows laid out one after another."""
-    import torch
+def _bad(t, name, dims, dtype, device):
+    """What is wrong with a tensor that is not of these dimensions, type and device."""
+    if not isinstance(t, _Tensor):
+        return TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype or (dims is not None and t.dim() != dims):
+        return TypeError(f"{name} must be a {f'{dims}-D ' if dims else ''}{dtype} tensor")
+    return ValueError(f"{name} is on {t.device}, expected {device}")
 
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype or t.dim() != 2:
-        raise TypeError(f"{name} must be a 2-D {dtype} tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    rows, cols = t.shape
-    if (rows, cols) != shape:
-        raise ValueError(f"{name} has shape {(rows, cols)}, expected {tuple(shape)}")
+
+def _matrix(t, name, rows, cols, dtype, device):
+    """(device pointer, row pitch) of a rows x cols tensor of that type and device, rows laid out one after another."""
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.dim() != 2 or t.device != device:
+        raise _bad(t, name, 2, dtype, device)
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(rows, cols)}")
     ld, inner = t.stride()
-    if cols > 1 and inner != 1:
+    if inner != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    if rows > 1 and cols > 0:
-        if ld < cols:
+    if ld < cols or cols == 0 or rows <= 1:
+        if rows > 1 and cols > 0:
             raise ValueError(f"{name} has overlapping rows (row stride {ld} < {cols} columns)")
-    else:
-        ld = max(cols, 1)
+        ld = cols if cols > 1 else 1
     return t.data_ptr(), ld
 
 
-def _stack(t, name, shape, dtype, device):
-    """(device pointer, row pitch, elements between matrices) of a 3-D tensor."""
-    import torch
-
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype or t.dim() != 3:
-        raise TypeError(f"{name} must be a 3-D {dtype} tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    count, rows, cols = t.shape
+def _stack(t, name, count, rows, cols, dtype, device):
+    """(device pointer, row pitch, elements between matrices) of a count x rows x cols tensor."""
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.dim() != 3 or t.device != device:
+        raise _bad(t, name, 3, dtype, device)
+    if t.shape != (count, rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(count, rows, cols)}")
     outer, ld, inner = t.stride()
-    if cols > 1 and inner != 1:
+    if inner != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
-    if rows > 1 and cols > 0:
-        if ld < cols:
+    if ld < cols or cols == 0 or rows <= 1:
+        if rows > 1 and cols > 0:
             raise ValueError(f"{name} has overlapping rows (row stride {ld} < {cols} columns)")
-    else:
-        ld = max(cols, 1)
+        ld = cols if cols > 1 else 1
     span = (rows - 1) * ld + cols if rows > 0 else 0
     if count > 1 and outer < span:
         raise ValueError(f"{name} has overlapping matrices (stride {outer} < {span} elements)")
@@ -208,15 +213,9 @@ def _stack(t, name, shape, dtype, device):
 
 def _list(t, name, shape, dtype, device):
     """Device pointer of a packed tensor."""
-    import torch
-
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be a {dtype} tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if tuple(t.shape) != tuple(shape):
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.device != device:
+        raise _bad(t, name, None, dtype, device)
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -231,10 +230,12 @@ def _gpu(t, name):
 
 def _run(entry, what, device, stream, *args):
     """One entry point on the tensors' device and stream."""
-    import torch
-
-    handle = dft._stream_handle(stream, device)
-    if torch.cuda.current_device() == device.index:
+    index = device.index
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
         st = entry(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -244,8 +245,6 @@ def _run(entry, what, device, stream, *args):
 
 
 def _workspace(args, need, what, given, device):
-    import torch
-
     if need < 0:
         raise dft.GemmError(int(need), what)
     if given is None and need > 0:
@@ -260,28 +259,26 @@ def _workspace(args, need, what, given, device):
 
 
 def _linear(a, b, offsets, bias, residual, activation, out, out_dtype, preact, workspace, stream, variant, splits):
-    import torch
-
     dtype, kind = getattr(a, "dtype", None), _input_type(a, "a")
     device = _gpu(a, "a")
     grouped = offsets is not None
-    if a.dim() != 2 or not isinstance(b, torch.Tensor) or b.dim() != 2 + grouped:
+    if a.dim() != 2 or not isinstance(b, _Tensor) or b.dim() != 2 + grouped:
         raise TypeError(f"a must be a 2-D tensor and b a {2 + grouped}-D one")
     M, K = a.shape
     N = b.shape[-1]
     g = LinearArgs(input_type=kind, activation=_act_code(activation), variant=variant, splits=splits, M=M, N=N, K=K)
-    g.A, g.lda = _matrix(a, "a", (M, K), dtype, device)
+    g.A, g.lda = _matrix(a, "a", M, K, dtype, device)
     if grouped:
         groups = b.shape[0]
         if groups < 1:
             raise ValueError("b must have at least one matrix")
         g.groups = groups
-        g.B, g.ldb, g.b_stride = _stack(b, "b", (groups, K, N), dtype, device)
-        g.offsets = _list(offsets, "offsets", (groups + 1,), torch.int32, device)
+        g.B, g.ldb, g.b_stride = _stack(b, "b", groups, K, N, dtype, device)
+        g.offsets = _list(offsets, "offsets", (groups + 1,), _int32, device)
         if bias is not None:
-            g.bias, g.bias_stride = _matrix(bias, "bias", (groups, N), dtype, device)
+            g.bias, g.bias_stride = _matrix(bias, "bias", groups, N, dtype, device)
     else:
-        g.B, g.ldb = _matrix(b, "b", (K, N), dtype, device)
+        g.B, g.ldb = _matrix(b, "b", K, N, dtype, device)
         if bias is not None:
             g.bias = _list(bias, "bias", (N,), dtype, device)
     if out is None:
@@ -289,15 +286,15 @@ def _linear(a, b, offsets, bias, residual, activation, out, out_dtype, preact, w
     elif out_dtype is not None and getattr(out, "dtype", None) is not out_dtype:
         raise TypeError(f"out must be a 2-D {out_dtype} tensor")
     out_type = getattr(out, "dtype", None)
-    if out_type is torch.float32:
+    if out_type is _f32:
         g.output_type = OUTPUT_F32
     elif out_type is not dtype:
         raise TypeError(f"out must be {dtype} or torch.float32")
-    g.D, g.ldd = _matrix(out, "out", (M, N), out_type, device)
+    g.D, g.ldd = _matrix(out, "out", M, N, out_type, device)
     if residual is not None:
-        g.residual, g.ldr = _matrix(residual, "residual", (M, N), out_type, device)
+        g.residual, g.ldr = _matrix(residual, "residual", M, N, out_type, device)
     if preact is not None:
-        g.preact, g.ldp = _matrix(preact, "preact", (M, N), dtype, device)
+        g.preact, g.ldp = _matrix(preact, "preact", M, N, dtype, device)
     lib = dft.library()
     keep = _workspace(g, lib.gemm_linear_workspace_bytes(g, _num_cus(device)), "gemm_linear_workspace_bytes",
                       workspace, device)
@@ -326,21 +323,11 @@ def grouped_linear(a, b, offsets, bias=None, residual=None, activation="none", o
     return _linear(a, b, offsets, bias, residual, activation, out, out_dtype, preact, workspace, stream, variant, 1)
 
 
-def _grad_out(given, wanted, shape, dtype, device):
-    import torch
-
-    if not wanted:
-        return None
-    return torch.empty(shape, dtype=dtype, device=device) if given is None else given
-
-
 def _linear_grad(dy, a, b, offsets, preact, activation, want, a_dtype, b_dtype, workspace, stream):
-    import torch
-
     dtype, kind = getattr(a, "dtype", None), _input_type(a, "a")
     device = _gpu(a, "a")
     grouped = offsets is not None
-    if a.dim() != 2 or not isinstance(b, torch.Tensor) or b.dim() != 2 + grouped:
+    if a.dim() != 2 or not isinstance(b, _Tensor) or b.dim() != 2 + grouped:
         raise TypeError(f"a must be a 2-D tensor and b a {2 + grouped}-D one")
     want = frozenset(want)
     if not want <= {"a", "b", "bias"}:
@@ -349,18 +336,18 @@ def _linear_grad(dy, a, b, offsets, preact, activation, want, a_dtype, b_dtype, 
     N = b.shape[-1]
     act = _act_code(activation)
     g = LinearGradArgs(input_type=kind, activation=act, M=M, N=N, K=K)
-    g.A, g.lda = _matrix(a, "a", (M, K), dtype, device)
-    g.dY, g.ldy = _matrix(dy, "dy", (M, N), dtype, device)
+    g.A, g.lda = _matrix(a, "a", M, K, dtype, device)
+    g.dY, g.ldy = _matrix(dy, "dy", M, N, dtype, device)
     groups = 1
     if grouped:
         groups = b.shape[0]
         if groups < 1:
             raise ValueError("b must have at least one matrix")
         g.groups = groups
-        g.B, g.ldb, g.b_stride = _stack(b, "b", (groups, K, N), dtype, device)
-        g.offsets = _list(offsets, "offsets", (groups + 1,), torch.int32, device)
+        g.B, g.ldb, g.b_stride = _stack(b, "b", groups, K, N, dtype, device)
+        g.offsets = _list(offsets, "offsets", (groups + 1,), _int32, device)
     else:
-        g.B, g.ldb = _matrix(b, "b", (K, N), dtype, device)
+        g.B, g.ldb = _matrix(b, "b", K, N, dtype, device)
     types = {None: (dtype, OUTPUT_SAME), dtype: (dtype, OUTPUT_SAME), torch.float32: (torch.float32, OUTPUT_F32)}
     if a_dtype not in types or b_dtype not in types:
         raise TypeError(f"gradients are {dtype} or torch.float32")
@@ -369,7 +356,7 @@ def _linear_grad(dy, a, b, offsets, preact, activation, want, a_dtype, b_dtype, 
     if act != ACT_NONE:
         if preact is None:
             raise ValueError(f"the gradient of {activation} needs preact")
-        g.Z, g.ldz = _matrix(preact, "preact", (M, N), dtype, device)
+        g.Z, g.ldz = _matrix(preact, "preact", M, N, dtype, device)
         dz = torch.empty((M, N), dtype=dtype, device=device)
         g.dZ, g.lddz = dz.data_ptr(), max(N, 1)
     if "a" in want:
@@ -411,13 +398,13 @@ def expert_sort(experts, num_experts: int, stream=None):
     """Sorts (token, choice) pairs by expert, by gemm_expert_sort.  experts: tokens x top_k int32; a value outside
     [0, num_experts) drops its pair.  Returns int32 tensors: offsets (num_experts + 1), order (tokens * top_k) and
     position (tokens x top_k)."""
-    import torch
-
-    if not isinstance(experts, torch.Tensor) or experts.dim() != 2:
+    if torch is None:
+        _bind()
+    if not isinstance(experts, _Tensor) or experts.dim() != 2:
         raise TypeError("experts must be a 2-D torch.int32 tensor")
     device = _gpu(experts, "experts")
     tokens, top_k = experts.shape
-    src = _list(experts, "experts", (tokens, top_k), torch.int32, device)
+    src = _list(experts, "experts", (tokens, top_k), _int32, device)
     need = gemm_expert_sort_workspace_bytes(tokens, top_k, num_experts)
     if need < 0:
         raise dft.GemmError(need, "gemm_expert_sort")
@@ -434,27 +421,23 @@ def expert_sort(experts, num_experts: int, stream=None):
 
 
 def _positions(position, device):
-    import torch
-
-    if not isinstance(position, torch.Tensor) or position.dim() != 2:
+    if not isinstance(position, _Tensor) or position.dim() != 2:
         raise TypeError("position must be a 2-D torch.int32 tensor")
     tokens, top_k = position.shape
-    return tokens, top_k, _list(position, "position", (tokens, top_k), torch.int32, device)
+    return tokens, top_k, _list(position, "position", (tokens, top_k), _int32, device)
 
 
 def expert_gather(x, position, out=None, stream=None):
     """The tokens' rows in expert order, by gemm_expert_gather: row position[t, j] of the result is x[t].  The
     result has tokens * top_k rows (or ``out``'s); rows that no pair has are left as they were."""
-    import torch
-
     kind, device = _input_type(x, "x"), _gpu(x, "x")
     tokens, top_k, pos = _positions(position, device)
     cols = x.shape[-1] if x.dim() == 2 else -1
-    px, ldx = _matrix(x, "x", (tokens, cols), x.dtype, device)
+    px, ldx = _matrix(x, "x", tokens, cols, x.dtype, device)
     if out is None:
         out = torch.empty((tokens * top_k, cols), dtype=x.dtype, device=device)
-    rows = out.shape[0] if isinstance(out, torch.Tensor) and out.dim() == 2 else -1
-    po, ldo = _matrix(out, "out", (rows, cols), x.dtype, device)
+    rows = out.shape[0] if isinstance(out, _Tensor) and out.dim() == 2 else -1
+    po, ldo = _matrix(out, "out", rows, cols, x.dtype, device)
     _run(dft.library().gemm_expert_gather, "gemm_expert_gather", device, stream, kind, tokens, rows, top_k, cols, px,
          ldx, pos, po, ldo)
     return out
@@ -463,16 +446,14 @@ def expert_gather(x, position, out=None, stream=None):
 def expert_combine(y, position, weights=None, out=None, stream=None):
     """The experts' rows back in token order, by gemm_expert_combine: result[t] = sum over j of weights[t, j] *
     y[position[t, j]] (weights: tokens x top_k float32, or None for ones: the gradient of expert_gather)."""
-    import torch
-
     kind, device = _input_type(y, "y"), _gpu(y, "y")
     tokens, top_k, pos = _positions(position, device)
     rows, cols = y.shape if y.dim() == 2 else (-1, -1)
-    py, ldy = _matrix(y, "y", (rows, cols), y.dtype, device)
-    pw = None if weights is None else _list(weights, "weights", (tokens, top_k), torch.float32, device)
+    py, ldy = _matrix(y, "y", rows, cols, y.dtype, device)
+    pw = None if weights is None else _list(weights, "weights", (tokens, top_k), _f32, device)
     if out is None:
         out = torch.empty((tokens, cols), dtype=y.dtype, device=device)
-    po, ldo = _matrix(out, "out", (tokens, cols), y.dtype, device)
+    po, ldo = _matrix(out, "out", tokens, cols, y.dtype, device)
     _run(dft.library().gemm_expert_combine, "gemm_expert_combine", device, stream, kind, tokens, rows, top_k, cols,
          py, ldy, pos, pw, po, ldo)
     return out
@@ -482,21 +463,19 @@ def expert_combine_grad(dout, y, position, weights=None, dy=None, stream=None):
     """Gradients of expert_combine, by gemm_expert_combine_grad: (dy, dweights) with dy[position[t, j]] = weights[t,
     j] * dout[t] and dweights[t, j] = y[position[t, j]] . dout[t] (float32; None without weights).  Rows of dy that
     no pair has are left as they were."""
-    import torch
-
     kind, device = _input_type(y, "y"), _gpu(y, "y")
     tokens, top_k, pos = _positions(position, device)
     rows, cols = y.shape if y.dim() == 2 else (-1, -1)
-    py, ldy = _matrix(y, "y", (rows, cols), y.dtype, device)
-    pd, ldd = _matrix(dout, "dout", (tokens, cols), y.dtype, device)
+    py, ldy = _matrix(y, "y", rows, cols, y.dtype, device)
+    pd, ldd = _matrix(dout, "dout", tokens, cols, y.dtype, device)
     pw = pdw = dweights = None
     if weights is not None:
-        pw = _list(weights, "weights", (tokens, top_k), torch.float32, device)
+        pw = _list(weights, "weights", (tokens, top_k), _f32, device)
         dweights = torch.empty((tokens, top_k), dtype=torch.float32, device=device)
         pdw = dweights.data_ptr()
     if dy is None:
         dy = torch.empty((rows, cols), dtype=y.dtype, device=device)
-    pdy, lddy = _matrix(dy, "dy", (rows, cols), y.dtype, device)
+    pdy, lddy = _matrix(dy, "dy", rows, cols, y.dtype, device)
     _run(dft.library().gemm_expert_combine_grad, "gemm_expert_combine_grad", device, stream, kind, tokens, rows,
          top_k, cols, pd, ldd, py, ldy, pos, pw, pdy, lddy, pdw)
     return dy, dweights
@@ -520,9 +499,9 @@ def expert_mlp(x, experts, weights, w1, w2, b1=None, b2=None, activation="silu",
 
     x: tokens x D; experts: tokens x top_k int32; weights: tokens x top_k float32; w1: E x D x H; w2: E x H x D;
     b1: E x H; b2: E x D.  Returns (out, state); state is what expert_mlp_grad needs."""
-    import torch
-
-    if not isinstance(w1, torch.Tensor) or w1.dim() != 3:
+    if torch is None:
+        _bind()
+    if not isinstance(w1, _Tensor) or w1.dim() != 3:
         raise TypeError("w1 must be a 3-D tensor")
     offsets, _, position = expert_sort(experts, w1.shape[0], stream=stream)
     rows = expert_gather(x, position, stream=stream)

@@ -515,7 +515,7 @@ typedef struct {
     int64_t ldp;
     void *D;                  /* M x N */
     int64_t ldd;
-    void *workspace;          /* DEVICE, 4-byte aligned; may be NULL when gemm_linear_workspace_bytes is 0 */
+    void *workspace;          /* DEVICE, 16-byte aligned; may be NULL when gemm_linear_workspace_bytes is 0 */
     int64_t workspace_bytes;
 } gemm_linear_args;
 
