@@ -102,38 +102,53 @@ struct Plan {
     double us;  // as estimated
 };
 
-// Full-chip rates of the tiles (TFLOP/s, one type) and workgroups per CU.
-struct TileRate {
-    double rate;
+// Times of the tiles in microseconds, fitted to bf16 products of 1 to 4096
+// rows by 1024 to 16384 columns and 1024 to 8192 deep (forward): a round of
+// workgroups takes `fixed` and, per contraction tile, `alone` with one
+// workgroup per CU and `full` with every place taken.
+struct TileTime {
     int per_cu;
+    double fixed, alone, full;
 };
-constexpr TileRate kDirectRates[kTileCount] = {{1200, 1}, {950, 2}, {600, 2}, {350, 2}};
-constexpr TileRate kRegisterRates[kTileCount] = {{0, 1}, {400, 2}, {250, 2}, {150, 2}};
+constexpr TileTime kDirectTimes[kTileCount] = {{1, 12, 1.0, 1.42}, {2, 1.8, 0.62, 0.94}, {2, 3, 0.2, 0.40}, {2, 3, 0.2, 0.44}};
+constexpr TileTime kRegisterTimes[kTileCount] = {{1, 0, 0, 0}, {2, 3, 2.5, 3.2}, {2, 3, 1.5, 2.0}, {2, 3, 1.5, 2.0}};
 constexpr int kMaxSlices = 32;
 
-// Estimated microseconds of a plan: whole rounds of workgroups, each as long
-// as its multiply at the tile's rate or as its own operand stream, with a
-// fixed cost to fill and drain it; slices add the join's launch and traffic.
+// Estimated microseconds of a plan: its launch, its rounds (the last one by
+// how much of the chip it takes), no less than its operands' bytes at 5 TB/s,
+// and the slices' join.
 double estimate(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, LinearTile t, bool direct, int splits,
                 int cus) {
-    const TileRate rate = (direct ? kDirectRates : kRegisterRates)[t];
-    if (rate.rate <= 0) return 1e30;
+    const TileTime time = (direct ? kDirectTimes : kRegisterTimes)[t];
+    if (time.alone <= 0) return 1e30;
     const TileSize size = kTileSizes[t];
-    double row_tiles = (double)ceil_div(R, size.bm), length = (double)L;
-    if (axis == kGroupRows)  // on average half a tile more for every group that has rows
-        row_tiles = (double)R / size.bm + 0.5 * (double)std::min<int64_t>(groups, R);
+    double row_tiles = (double)ceil_div(R, size.bm), length = (double)L, copies = 1;
+    if (axis == kGroupRows) {  // on average half a tile more for every group that has rows
+        copies = (double)std::min<int64_t>(groups, R);
+        row_tiles = (double)R / size.bm + 0.5 * copies;
+    }
     double tiles = row_tiles * (double)ceil_div(C, size.bn) * splits;
     if (axis == kGroupContraction) {
         tiles *= (double)groups;
         length = (double)L / (double)groups;
     }
-    const double slots = (double)cus * rate.per_cu;
-    const double rounds = std::max(1.0, tiles > 4 * slots ? tiles / slots : (double)(int64_t)(tiles / slots + 0.999));
-    const double deep = ceil_div((int64_t)(length / splits + 0.999), kTileDepth) * (double)kTileDepth;
-    const double multiply = 2.0 * size.bm * size.bn * deep / (rate.rate / slots) * 1e-6;
-    const double stream = 2.0 * (size.bm + size.bn) * deep / 60e3;  // 60 GB/s per workgroup
-    double us = rounds * (std::max(multiply, stream) + 1.5) + 2.0;
-    if (splits > 1) us += 3.0 + (splits + 1.0) * (double)R * (double)C * 4.0 / 4e6;
+    const double slots = (double)cus * time.per_cu;
+    const double depth = (double)ceil_div((int64_t)(length / splits + 0.999), kTileDepth);
+    const double whole = (double)(int64_t)(tiles / slots), left = tiles / slots - whole;  // rounds
+    // (128x128 tiles: the epilogues of a round that another follows)
+    double us = whole * (time.fixed + (t == kTile128 ? 4 : 0) + depth * time.full);
+    if (left > 0) {
+        // from `alone` while there is at most one workgroup per CU (one-per-CU tiles: by the share of CUs) to `full`
+        const double busy = time.per_cu == 1 ? left : std::max(0.0, left * time.per_cu - 1) / (time.per_cu - 1);
+        const double last = time.fixed + depth * (time.alone + busy * (time.full - time.alone));
+        const bool tail = t == kTile256 && direct && axis != kGroupContraction && splits == 1 && whole > 0 &&
+                          depth >= kTailDepth && left <= 0.5;
+        us += tail ? std::min(last, time.fixed + depth * time.full * left + 30) : last;
+    }
+    const double bytes = 2.0 * ((double)R * (double)L + copies * (double)L * (double)C) +
+                         2.0 * (double)R * (double)C * (axis == kGroupContraction ? (double)groups : 1.0);
+    us = std::max(us, bytes / 5e6) + 0.1 * us + 2.5;  // (of two plans that wait for memory, the one that computes less)
+    if (splits > 1) us += 3.5 + (splits + 1.0) * (double)R * (double)C * 4.0 / 4e6;
     return us;
 }
 
@@ -155,8 +170,10 @@ Plan choose(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, bool dire
                 if (splits == 0 && slice < 4 * kTileDepth) break;
                 use = (int)ceil_div(L, slice);
             }
-            const double us = estimate(R, C, L, groups, axis, tile, direct, use, cus);
-            if (us < best.us) best = Plan{tile, direct, std::max(use, 1), slice, us};
+            double us = estimate(R, C, L, groups, axis, tile, direct, use, cus);
+            // at equal times the tile whose rows are used, and fewer slices
+            if (tile == kTile32x128 && R > 32 * groups) us += 0.3;
+            if (us < best.us - 0.2) best = Plan{tile, direct, std::max(use, 1), slice, us};
             if (splits > 0 || axis != kGroupNone || L == 0) break;
         }
     }
@@ -164,6 +181,17 @@ Plan choose(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, bool dire
 }
 
 int64_t partial_bytes(const Plan& plan, int64_t R, int64_t C) { return plan.splits > 1 ? plan.splits * R * C * 4 : 0; }
+
+// The blocks for the slices of a last round (tail_split): one per workgroup
+// of a persistent grid, where it has whole rounds before it.
+int64_t tail_bytes(const Plan& plan, int64_t R, int64_t C, int64_t L, int64_t groups, int axis, int cus) {
+    if (plan.tile != kTile256 || !plan.direct || plan.splits > 1 || axis == kGroupContraction) return 0;
+    if (ceil_div(L, kTileDepth) < kTailDepth) return 0;
+    const int64_t across = ceil_div(C, 256), most = (axis == kGroupRows ? (R + groups * 255) / 256 : ceil_div(R, 256)) * across;
+    if (most <= cus) return 0;
+    if (axis == kGroupNone && (most % cus == 0 || cus / (most % cus) < 2)) return 0;
+    return (int64_t)cus * 256 * 256 * 4;
+}
 
 // Row tiles enough for any division of R rows into groups.
 int64_t row_tiles(int64_t R, int64_t groups, int axis, int64_t bm) {
@@ -188,8 +216,17 @@ hipError_t launch(int type, const LinearProblem& p, LinearLayout layout, const P
     const hipError_t e = type == GEMM_INPUT_BF16
                              ? launch_linear_bf16(p, layout, plan.tile, plan.direct, tiles_m, tiles_n, grid_y, cus, stream)
                              : launch_linear_f16(p, layout, plan.tile, plan.direct, tiles_m, tiles_n, grid_y, cus, stream);
-    if (e != hipSuccess || plan.splits <= 1) return e;
+    if (e != hipSuccess) return e;
     LinearProblem problem = p;
+    if (p.tail) {
+        uint32_t m = tiles_m, n = tiles_n, grid = std::min<uint32_t>((uint32_t)cus, tiles_m * tiles_n);
+        void* args[] = {&problem, &m, &n, &grid};
+        const void* join = type == GEMM_INPUT_BF16
+                               ? reinterpret_cast<const void*>(linear_tail_kernel<kInputBf16, 256, 256>)
+                               : reinterpret_cast<const void*>(linear_tail_kernel<kInputF16, 256, 256>);
+        return hipLaunchKernel(join, dim3(grid / 2, 256 / 32), dim3(256), args, 0, stream);
+    }
+    if (plan.splits <= 1) return e;
     const int64_t blocks = std::min<int64_t>(ceil_div(p.R * ceil_div(p.C, 8), kJoinGroups), 16384);
     void* args[] = {&problem};
     const void* join = type == GEMM_INPUT_BF16 ? reinterpret_cast<const void*>(linear_join_kernel<kInputBf16>)
@@ -295,21 +332,23 @@ struct LinearPlan {
     Plan plan;
     bool pack_a, pack_b;
     int64_t workspace;  // bytes
+    bool tail;          // slices of the last round
 };
 LinearPlan plan_linear(const gemm_linear_args& a, const LinearCall& c, int cus) {
     LinearPlan best{choose(a.M, a.N, a.K, c.groups, c.axis, direct_ok(c.A, true, c.B, false), a.variant, a.splits, cus),
-                    false, false, 0};
+                    false, false, 0, false};
     if (!best.plan.direct && a.K > 0) {
         const bool pack_a = !whole_rows(c.A), pack_b = !whole_rows(c.B);
         const Matrix A = pack_a ? packed(c.A) : c.A, B = pack_b ? packed(c.B) : c.B;
         if (copies_fit(kTile256, A, true, B, false)) {
             const Plan p = choose(a.M, a.N, a.K, c.groups, c.axis, true, a.variant, a.splits, cus);
             const double us = p.us + 2.5 + (pack_a ? pack_us(c.A) : 0) + (pack_b ? pack_us(c.B) : 0);
-            if (us < best.plan.us) best = LinearPlan{p, pack_a, pack_b, 0};
+            if (us < best.plan.us) best = LinearPlan{p, pack_a, pack_b, 0, false};
         }
     }
+    best.tail = tail_bytes(best.plan, a.M, a.N, a.K, c.groups, c.axis, cus) > 0;
     best.workspace = (best.pack_a ? packed_bytes(c.A) : 0) + (best.pack_b ? packed_bytes(c.B) : 0) +
-                     partial_bytes(best.plan, a.M, a.N);
+                     partial_bytes(best.plan, a.M, a.N) + tail_bytes(best.plan, a.M, a.N, a.K, c.groups, c.axis, cus);
     return best;
 }
 
@@ -347,6 +386,7 @@ int run_linear(const gemm_linear_args& a, hipStream_t stream) {
     p.B = static_cast<const uint16_t*>(B.data); p.ldb = B.ld; p.b_group = B.copy_stride;
     p.offsets = a.offsets; p.groups = (int32_t)c.groups; p.axis = c.axis;
     p.splits = plan.splits; p.slice = plan.slice; p.partial = reinterpret_cast<float*>(space.at);
+    p.tail = chosen.tail ? reinterpret_cast<float*>(space.at) : nullptr;
     p.ep.bias = static_cast<const uint16_t*>(a.bias); p.ep.bias_group = a.bias_stride;
     p.ep.residual = a.residual; p.ep.ldr = a.ldr;
     p.ep.preact = static_cast<uint16_t*>(a.preact); p.ep.ldp = a.ldp;
@@ -398,8 +438,11 @@ Plan plan_b(const gemm_linear_grad_args& a, const GradCall& c, bool direct, int 
     return choose(a.K, a.N, a.M, c.groups, c.axis == kGroupRows ? kGroupContraction : kGroupNone, direct,
                   GEMM_LINEAR_AUTO, 0, cus);
 }
+int slope_rows(const gemm_linear_grad_args& a) {
+    return ceil_div(a.M, kSlopeRows) * ceil_div(a.N, 256) < 1024 ? kFewSlopeRows : kSlopeRows;
+}
 int64_t slope_chunks(const gemm_linear_grad_args& a, const GradCall& c) {
-    return row_tiles(a.M, c.groups, c.axis, kSlopeRows);
+    return row_tiles(a.M, c.groups, c.axis, slope_rows(a));
 }
 
 // Both products' plans, with dZ, A and B as they are or packed (one choice
@@ -410,12 +453,13 @@ struct GradPlan {
     Plan a, b;
     bool pack_z, pack_a, pack_b;
     int64_t workspace;
+    bool tail_a, tail_b;  // slices of the last rounds
 };
 GradPlan plan_grad(const gemm_linear_grad_args& a, const GradCall& c, int cus) {
     const Matrix dz = c.slope();
     const bool want_a = a.dA && a.M > 0 && a.K > 0, want_b = a.dB && a.K > 0 && a.N > 0;
     GradPlan best{plan_a(a, c, direct_ok(dz, true, c.B, true), cus), plan_b(a, c, direct_ok(c.A, false, dz, false), cus),
-                  false, false, false, 0};
+                  false, false, false, 0, false, false};
     const bool slow = (want_a && !best.a.direct) || (want_b && !best.b.direct);
     if (slow && a.M > 0 && a.N > 0) {
         const bool z = !whole_rows(dz), pa = want_b && !whole_rows(c.A), pb = want_a && !whole_rows(c.B);
@@ -425,12 +469,17 @@ GradPlan plan_grad(const gemm_linear_grad_args& a, const GradCall& c, int cus) {
             const double before = (want_a ? best.a.us : 0) + (want_b ? best.b.us : 0);
             const double after = (want_a ? p.us : 0) + (want_b ? q.us : 0) + 2.5 + (z ? pack_us(dz) : 0) +
                                  (pa ? pack_us(c.A) : 0) + (pb ? pack_us(c.B) : 0);
-            if (after < before) best = GradPlan{p, q, z, pa, pb, 0};
+            if (after < before) best = GradPlan{p, q, z, pa, pb, 0, false, false};
         }
     }
     int64_t rest = a.dbias ? slope_chunks(a, c) * a.N * 4 : 0;
-    if (want_a) rest = std::max(rest, partial_bytes(best.a, a.M, a.K));
-    if (want_b) rest = std::max(rest, partial_bytes(best.b, a.K, a.N));
+    const int axis_b = c.axis == kGroupRows ? kGroupContraction : kGroupNone;
+    const int64_t tail_a = want_a ? tail_bytes(best.a, a.M, a.K, a.N, c.groups, c.axis, cus) : 0;
+    const int64_t tail_b = want_b ? tail_bytes(best.b, a.K, a.N, a.M, c.groups, axis_b, cus) : 0;
+    best.tail_a = tail_a > 0;
+    best.tail_b = tail_b > 0;
+    if (want_a) rest = std::max({rest, partial_bytes(best.a, a.M, a.K), tail_a});
+    if (want_b) rest = std::max({rest, partial_bytes(best.b, a.K, a.N), tail_b});
     best.workspace = (best.pack_z ? packed_bytes(dz) : 0) + (best.pack_a ? packed_bytes(c.A) : 0) +
                      (best.pack_b ? packed_bytes(c.B) : 0) + rest;
     return best;
@@ -444,7 +493,7 @@ int run_slope(const gemm_linear_grad_args& a, const GradCall& c, float* partial,
     p.dZ = static_cast<uint16_t*>(const_cast<void*>(c.dZ.data)); p.lddz = a.lddz;
     p.partial = a.dbias ? partial : nullptr;
     p.offsets = a.groups > 0 ? a.offsets : nullptr; p.groups = (int32_t)c.groups;
-    p.act = a.activation; p.dbias = a.dbias;
+    p.act = a.activation; p.dbias = a.dbias; p.chunk_rows = slope_rows(a);
     void* args[] = {&p};
     const int64_t chunks = slope_chunks(a, c);
     if ((p.dZ || p.partial) && chunks > 0) {
@@ -502,7 +551,7 @@ int run_grad(const gemm_linear_grad_args& a, hipStream_t stream) {
         p.R = a.M; p.C = a.K; p.L = a.N; p.axis = c.axis;
         p.A = static_cast<const uint16_t*>(dz.data); p.lda = dz.ld;
         p.B = static_cast<const uint16_t*>(B.data); p.ldb = B.ld; p.b_group = B.copy_stride;
-        p.splits = pa.splits; p.slice = pa.slice;
+        p.splits = pa.splits; p.slice = pa.slice; p.tail = plan.tail_a ? p.partial : nullptr;
         p.ep = LinearEpilogue{};
         p.ep.out = a.dA; p.ep.ldo = a.ldda; p.ep.out_f32 = a.a_grad_type == GEMM_OUTPUT_F32;
         if (launch(a.input_type, p, kGradA, pa, cus, stream) != hipSuccess) return GEMM_ERR_HIP;
@@ -511,7 +560,7 @@ int run_grad(const gemm_linear_grad_args& a, hipStream_t stream) {
         p.R = a.K; p.C = a.N; p.L = a.M; p.axis = axis_b;
         p.A = static_cast<const uint16_t*>(A.data); p.lda = A.ld;
         p.B = static_cast<const uint16_t*>(dz.data); p.ldb = dz.ld; p.b_group = 0;
-        p.splits = pb.splits; p.slice = pb.slice;
+        p.splits = pb.splits; p.slice = pb.slice; p.tail = plan.tail_b ? p.partial : nullptr;
         p.ep = LinearEpilogue{};
         p.ep.out = a.dB; p.ep.ldo = a.lddb; p.ep.out_group = a.db_stride; p.ep.out_f32 = a.b_grad_type == GEMM_OUTPUT_F32;
         if (launch(a.input_type, p, kGradB, pb, cus, stream) != hipSuccess) return GEMM_ERR_HIP;

@@ -50,6 +50,7 @@ struct LinearProblem {
     int32_t splits;              // slices of the contraction along gridDim.y (one matrix only)
     int64_t slice;               // contraction elements per slice, a multiple of the tile's
     float* partial;              // splits > 1: packed R x C partial products
+    float* tail;                 // not nullptr: the tiles past the last whole round are sliced (TailSplit)
     LinearEpilogue ep;
 };
 
@@ -189,17 +190,21 @@ struct Row8 {
         return r;
     }
 };
-// The first `in_range` of the eight, zeros for the others; one access when all are in range, else one each.
+// The first `in_range` of the eight, zeros for the others: one access when all
+// are in range, else eight, at the last one in range for those beyond it, so
+// that all are on their way together.
 __device__ inline Row8 load8(const uint16_t* p, int64_t in_range) {
-    Row8 r;
+    Row8 r{};
     if (in_range >= 8) {
         __builtin_memcpy(&r.w, p, sizeof(r.w));
-    } else {
+    } else if (in_range > 0) {
+        const int last = (int)in_range - 1;
+        uint32_t v[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = 2 * e < in_range ? p[2 * e] : 0u, hi = 2 * e + 1 < in_range ? p[2 * e + 1] : 0u;
-            r.w[e] = lo | (hi << 16);
-        }
+        for (int e = 0; e < 8; ++e) v[e] = p[e < last ? e : last];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            r.w[e] = (2 * e <= last ? v[2 * e] : 0u) | (2 * e + 1 <= last ? v[2 * e + 1] << 16 : 0u);
     }
     return r;
 }
@@ -221,9 +226,15 @@ __device__ inline void load8(float (&v)[8], const float* p, int64_t in_range) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[4 * h + e] = x[e];
         }
+    } else if (in_range > 0) {
+        const int last = (int)in_range - 1;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = p[e < last ? e : last];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e <= last ? v[e] : 0.0f;
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = e < in_range ? p[e] : 0.0f;
+        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
     }
 }
 __device__ inline void store8(float* p, const float (&v)[8], int64_t in_range) {
@@ -271,22 +282,25 @@ __device__ inline Row8 residual_reads(const LinearEpilogue& ep, const EpilogueBa
     if (!ep.residual || ep.out_f32) return Row8{};
     return load8(reinterpret_cast<const uint16_t*>(base.residual + lane.residual), left);
 }
-template <int TYPE>
+// PLAIN (the gradients' products): the sums alone, rounded.
+template <int TYPE, bool PLAIN = false>
 __device__ inline void epilogue8(const LinearEpilogue& ep, const Row8& bias, const Row8& residual,
                                  const EpilogueBase& base, const EpilogueLane& lane, int64_t left, float (&z)[8]) {
-    float add[8];
-    bias.widen<TYPE>(add);  // (zeros without a bias, and so for the residual: an addition is less than a branch)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] += add[e];
-    if (ep.preact) store8(reinterpret_cast<uint16_t*>(base.preact + lane.preact), Row8::narrow<TYPE>(z), left);
-    act_values(z, ep.act);
-    residual.widen<TYPE>(add);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] += add[e];
-    if (ep.residual && ep.out_f32) {
-        load8(add, reinterpret_cast<const float*>(base.residual + lane.residual), left);
+    if constexpr (!PLAIN) {
+        float add[8];
+        bias.widen<TYPE>(add);  // (zeros without a bias, and so for the residual: an addition is less than a branch)
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[e] += add[e];
+        if (ep.preact) store8(reinterpret_cast<uint16_t*>(base.preact + lane.preact), Row8::narrow<TYPE>(z), left);
+        act_values(z, ep.act);
+        residual.widen<TYPE>(add);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] += add[e];
+        if (ep.residual && ep.out_f32) {
+            load8(add, reinterpret_cast<const float*>(base.residual + lane.residual), left);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] += add[e];
+        }
     }
     if (ep.out_f32)
         store8(reinterpret_cast<float*>(base.out + lane.out), z, left);
@@ -511,31 +525,32 @@ struct OperandLoad {
 };
 
 // A wave's fragments of one operand: block i (16 output rows or columns) of
-// MFMA step st (32 contraction elements), 8 of them per lane.
+// MFMA step st (32 contraction elements), 8 of them per lane.  One place per
+// lane: a block along the rows (k-major: a step) is 8 (16) words further on,
+// in bits that the swizzle may have flipped but that the wave's first column
+// and whole rows leave alone, so it flips the same bits of the place.
 template <class Tile, bool KMAJOR, int BLOCKS>
 struct OperandRead {
-    int from[KMAJOR ? kDepth / 32 : BLOCKS];  // k-major: by step; else by block
+    static_assert(KMAJOR || (BLOCKS & (BLOCKS - 1)) == 0, "a wave's blocks fill an aligned range of columns");
+    int from;
 
     __device__ OperandRead(int out0, int lane) {
-        if constexpr (KMAJOR) {
-#pragma unroll
-            for (int st = 0; st < kDepth / 32; ++st) from[st] = Tile::at(out0 + lane % 16, st * 16 + 4 * (lane / 16));
-        } else {
-            const int row = 8 * (lane / 16) + (lane % 16) / 4;
-#pragma unroll
-            for (int i = 0; i < BLOCKS; ++i) from[i] = Tile::at(row, (out0 + i * 16 + 4 * (lane % 4)) / 2);
-        }
+        if constexpr (KMAJOR)
+            from = Tile::at(out0 + lane % 16, 4 * (lane / 16));
+        else
+            from = Tile::at(8 * (lane / 16) + (lane % 16) / 4, (out0 + 4 * (lane % 4)) / 2);
     }
-    __device__ u32x4 read(const uint32_t* lds, int stage, int st, int i) const {
+    __device__ u32x4 read(const uint32_t* lds, int place, int st, int i) const {
+        const int base = place * Tile::stage_words + from;
         if constexpr (KMAJOR) {
-            return *reinterpret_cast<const u32x4*>(lds + stage * Tile::stage_words + from[st] + i * 16 * Tile::cols);
+            return *reinterpret_cast<const u32x4*>(lds + (base ^ (16 * st)) + i * 16 * Tile::cols);
         } else {
             typedef __attribute__((address_space(3))) const uint32_t lds_word;
             typedef __attribute__((address_space(3))) shortx4 lds_short4;
             u32x2 half[2];
 #pragma unroll
             for (int rr = 0; rr < 2; ++rr) {
-                const int word = stage * Tile::stage_words + from[i] + (st * 32 + 4 * rr) * Tile::cols;
+                const int word = (base ^ (8 * i)) + (st * 32 + 4 * rr) * Tile::cols;
                 half[rr] = __builtin_bit_cast(u32x2,
                                               __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)((lds_word*)lds + word)));
             }
@@ -568,6 +583,46 @@ __device__ inline TilePlace place_of_block(uint32_t block, uint32_t blocks, uint
     const uint32_t panel = 8 * tiles_n, p = id / panel, in = id % panel;
     const uint32_t high = tiles_m - 8 * p < 8 ? tiles_m - 8 * p : 8;
     return TilePlace{8 * p + in % high, in / high};
+}
+
+// Tiles of all groups' rows.
+__device__ inline int64_t count_group_tiles(const int32_t* offsets, int groups, int64_t rows, int tile_rows) {
+    int64_t all = 0;
+    for (int g0 = 0; g0 < groups; g0 += kWave) {
+        const int g = g0 + (int)(threadIdx.x % kWave);
+        int own = 0;
+        if (g < groups) {
+            const RowRange r = group_rows(offsets, g, rows);
+            own = (int)((r.hi - r.lo + tile_rows - 1) / tile_rows);
+        }
+#pragma unroll
+        for (int d = kWave / 2; d > 0; d /= 2) own += __shfl_xor(own, d);
+        all += __builtin_amdgcn_readfirstlane(own);
+    }
+    return all;
+}
+
+// The last round of a persistent grid: `left` tiles for `grid` workgroups.
+// Cut along the contraction into `parts` slices each, their partial products
+// go to p.tail, one BM x BN block of fp32 per workgroup, and are joined by
+// linear_tail_kernel.  A round of whole tiles of 64 contraction tiles takes
+// about 100 us; slicing costs the join's launch and twice 64 MiB of traffic,
+// about 30 us, so it is asked for from 32 contraction tiles on (by the host)
+// and done where each tile gets at least two slices.
+constexpr int kTailDepth = 32;
+struct TailSplit {
+    uint32_t whole, left, parts;  // tiles before the last round (all, if it is not sliced), tiles in it, slices of each
+    int64_t slice;                // contraction elements per slice
+};
+__device__ inline TailSplit tail_split(const LinearProblem& p, uint32_t tiles, uint32_t grid) {
+    TailSplit t{tiles, 0, 1, p.L};
+    const uint32_t left = tiles % grid, depth = (uint32_t)((p.L + 63) / 64);
+    if (!p.tail || left == 0 || grid / left < 2) return t;
+    t.left = left;
+    t.whole = tiles - left;
+    t.parts = grid / left < depth / 8 ? grid / left : depth / 8;
+    t.slice = (int64_t)((depth + t.parts - 1) / t.parts) * 64;
+    return t;
 }
 
 // The kernel's own LinearProblem argument, read again from the argument
@@ -605,14 +660,15 @@ struct LinearWork {
     int64_t m0, m_end, n0, group, L;
     const uint16_t* A;  // first element of the operands' rows and contraction
     const uint16_t* B;
-    float* partial;
+    float* partial;     // where the sums go instead of the epilogue: element (row, column) of the output at
+    int64_t partial_ld; //   partial + row * partial_ld + column
     bool none;          // past the last group's tiles
 };
 template <bool AK, bool BK_, int BM, int BN>
 __device__ inline LinearWork linear_work(const LinearProblem& p, uint32_t tile, uint32_t tiles_m, uint32_t tiles_n,
                                          uint32_t y) {
     const TilePlace place = place_of_block(tile, tiles_m * tiles_n, tiles_m, tiles_n);
-    LinearWork w{place.row * BM, p.R, place.col * BN, 0, p.L, p.A, p.B, nullptr, false};
+    LinearWork w{place.row * BM, p.R, place.col * BN, 0, p.L, p.A, p.B, nullptr, p.C, false};
     if (p.axis == kGroupRows) {
         const GroupTile gt = find_group_tile(p.offsets, p.groups, p.R, BM, place.row);
         if (gt.group < 0) {
@@ -640,6 +696,16 @@ __device__ inline LinearWork linear_work(const LinearProblem& p, uint32_t tile, 
     w.B += BK_ ? w.n0 * p.ldb : w.n0;
     return w;
 }
+// Slice `part` of a tile of the last round, the at-th block of p.tail.
+template <bool AK, bool BK_, int BM, int BN>
+__device__ inline void slice_work(const LinearProblem& p, const TailSplit& t, LinearWork& w, uint32_t part, uint32_t at) {
+    const int64_t l0 = part * t.slice;
+    w.A += AK ? l0 : l0 * p.lda;
+    w.B += BK_ ? l0 : l0 * p.ldb;
+    w.L = w.L - l0 < t.slice ? w.L - l0 : t.slice;
+    w.partial = p.tail + (int64_t)at * (BM * BN) - (w.m0 * BN + w.n0);
+    w.partial_ld = BN;
+}
 
 // One BM x BN output tile (of a slice of the contraction, or of a group) at a
 // time, with one barrier per contraction tile: every wave has read all of tile
@@ -665,7 +731,7 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
     using Op = Mfma16Op<TYPE, 16>;
     constexpr int BM = Shape::BM, BN = Shape::BN, BK = kDepth, S = DIRECT ? Shape::STAGES : 2;
     constexpr int MI = Shape::MI, NI = Shape::NI, THREADS = Shape::THREADS, STEPS = BK / 32;
-    constexpr bool PERSISTENT = Shape::PERSISTENT && DIRECT;
+    constexpr bool PERSISTENT = Shape::PERSISTENT && DIRECT, PLAIN = !AK || BK_;
     using TileA = OperandTile<AK, BM, S>;
     using TileB = OperandTile<BK_, BN, S>;
     constexpr int RING = 5;
@@ -687,8 +753,32 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
     auto work_of = [&](uint32_t id) {
         return linear_work<AK, BK_, BM, BN>(problem_again(), id % tiles, tiles_m, tiles_n, id / tiles);
     };
-    // The next share that exists from id on (grouped rows may need fewer tiles than were counted for them).
+    // The share of tile number id, or the next that exists (grouped rows may need fewer tiles than were counted for
+    // them); in the last round, a slice of a tile.
+    bool sliced = false;
     auto find_work = [&](uint32_t& id, LinearWork& w) {
+        if constexpr (PERSISTENT) {
+            const LinearProblem p = problem_again();
+            if (p.tail) {
+                const uint32_t real_m = p.axis == kGroupRows
+                                            ? (uint32_t)count_group_tiles(p.offsets, p.groups, p.R, BM)
+                                            : tiles_m;  // (the tiles there are, so that the last ones are the last round)
+                const TailSplit t = tail_split(p, real_m * tiles_n, gridDim.x);
+                auto tile_of = [&](uint32_t tile) {
+                    return linear_work<AK, BK_, BM, BN>(p, tile, real_m, tiles_n, 0);
+                };
+                if (id < t.whole) {
+                    w = tile_of(id);
+                    return true;
+                }
+                const uint32_t at = blockIdx.x;  // (id is in the last round: id - at == whole)
+                if (sliced || at >= t.left * t.parts) return false;
+                sliced = true;
+                w = tile_of(t.whole + at / t.parts);
+                slice_work<AK, BK_, BM, BN>(p, t, w, at % t.parts, at);
+                return true;
+            }
+        }
         for (; id < total; id += gridDim.x) {
             w = work_of(id);
             if (!w.none) return true;
@@ -881,7 +971,7 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
                 return !w.partial && inside(m) ? residual_reads(p.ep, base(m), lane_at, left) : Row8{};
             };
             Row8 bias{};
-            if (!w.partial && left > 0) bias = bias_reads(p.ep, group * p.ep.bias_group + tile_col + c, left);
+            if (!PLAIN && !w.partial && left > 0) bias = bias_reads(p.ep, group * p.ep.bias_group + tile_col + c, left);
             // The residual is read for a group of parts at a time: loads and stores complete in order, so a load
             // waits for every store before it.
             constexpr int ALL = Shape::WM / ROWS, GROUP = WHOLE ? (ALL < 4 ? ALL : 4) : 1;
@@ -894,7 +984,7 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
                 asm volatile("" : "+v"(bias.w));
                 Row8 residual[GROUP];
 #pragma unroll
-                for (int u = 0; u < GROUP; ++u) residual[u] = read_residual(m0 + u, lane_at);
+                for (int u = 0; u < GROUP; ++u) residual[u] = PLAIN ? Row8{} : read_residual(m0 + u, lane_at);
                 static_for<GROUP>([&](auto U_) {
                     constexpr int U = decltype(U_)::value;
                     const int m = m0 + U;
@@ -922,9 +1012,9 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
                     }
                     if (inside(m)) {
                         if (w.partial)
-                            store8(w.partial + (tile_row + m * ROWS + r) * p.C + tile_col + c, z, left);
+                            store8(w.partial + (tile_row + m * ROWS + r) * w.partial_ld + tile_col + c, z, left);
                         else
-                            epilogue8<TYPE>(p.ep, bias, residual[U], base(m), lane_at, left, z);
+                            epilogue8<TYPE, PLAIN>(p.ep, bias, residual[U], base(m), lane_at, left, z);
                     }
                 });
             }
@@ -975,6 +1065,38 @@ __global__ __launch_bounds__(kJoinThreads) void linear_join_kernel(LinearProblem
             z[e] += __shfl_xor(z[e], 32);
         }
         if (slice0 == 0 && left > 0) epilogue8<TYPE>(p.ep, bias, residual, base, none, left, z);
+    }
+}
+
+// Joins the slices of the last round's tiles (tail_split of the same
+// arguments): workgroup (j, part) sums 32 rows of its j-th tile.
+template <int TYPE, int BM, int BN>
+__global__ __launch_bounds__(256) void linear_tail_kernel(LinearProblem p, uint32_t tiles_m, uint32_t tiles_n,
+                                                          uint32_t grid) {
+    const uint32_t real_m =
+        p.axis == kGroupRows ? (uint32_t)count_group_tiles(p.offsets, p.groups, p.R, BM) : tiles_m;
+    const TailSplit t = tail_split(p, real_m * tiles_n, grid);
+    if (blockIdx.x >= t.left) return;
+    const LinearWork w = linear_work<true, false, BM, BN>(p, t.whole + blockIdx.x, real_m, tiles_n, 0);
+    const float* block = p.tail + (int64_t)blockIdx.x * t.parts * (BM * BN);
+#pragma unroll
+    for (int k = 0; k < 32 * BN / 8 / 256; ++k) {
+        const int i = threadIdx.x + k * 256, r = blockIdx.y * 32 + i / (BN / 8), c = i % (BN / 8) * 8;
+        const int64_t row = w.m0 + r, col = w.n0 + c, left = p.C - col;
+        if (row >= w.m_end || left <= 0) continue;
+        const EpilogueBase base = epilogue_base(p.ep, w.group, row, col);
+        const EpilogueLane none{0, 0, 0};
+        const Row8 bias = bias_reads(p.ep, w.group * p.ep.bias_group + col, left),
+                   residual = residual_reads(p.ep, base, none, left);
+        float z[8] = {};
+#pragma unroll 4
+        for (uint32_t s = 0; s < t.parts; ++s) {
+            float more[8];
+            load8(more, block + (int64_t)s * (BM * BN) + r * BN + c, left);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] += more[e];
+        }
+        epilogue8<TYPE>(p.ep, bias, residual, base, none, left, z);
     }
 }
 

@@ -2,7 +2,7 @@
 //
 // dZ = dY act'(Z), rounded to 16 bits for the two products that read it, and
 // the column sums of the unrounded values (dbias): each workgroup sums a
-// chunk of kSlopeRows rows of one group over 256 columns into
+// chunk of 16 or 64 rows of one group over 256 columns into
 // partial[chunk][column]; linear_bias_join_kernel adds a group's chunks in
 // ascending order.  Bound by bytes: dY and Z read once, dZ written once.
 #pragma once
@@ -11,7 +11,9 @@
 
 namespace dft {
 
-constexpr int kSlopeRows = 64;
+// Rows per chunk: 64, or 16 where that leaves fewer workgroups than keep the
+// chip's loads in flight (slope_rows).
+constexpr int kSlopeRows = 64, kFewSlopeRows = 16;
 
 struct SlopeProblem {
     int64_t M, N;
@@ -25,6 +27,7 @@ struct SlopeProblem {
     const int32_t* offsets;
     int32_t groups;
     int32_t act;
+    int32_t chunk_rows;
     float* dbias;                // groups x N, rows N apart
 };
 
@@ -33,33 +36,37 @@ __global__ __launch_bounds__(256) void linear_slope_kernel(SlopeProblem p) {
     __shared__ float sums[8][256 + 8];
     const int c = threadIdx.x % 32, r = threadIdx.x / 32;
     const int64_t chunk = blockIdx.x, col = (int64_t)blockIdx.y * 256 + c * 8, left = p.N - col;
-    int64_t lo = chunk * kSlopeRows, hi = p.M;
+    int64_t lo = chunk * p.chunk_rows, hi = p.M;
     if (p.offsets) {
-        const GroupTile gt = find_group_tile(p.offsets, p.groups, p.M, kSlopeRows, chunk);
+        const GroupTile gt = find_group_tile(p.offsets, p.groups, p.M, p.chunk_rows, chunk);
         if (gt.group < 0) return;
         lo = gt.row0;
         hi = gt.row_end;
     }
-    if (hi > lo + kSlopeRows) hi = lo + kSlopeRows;
+    if (hi > lo + p.chunk_rows) hi = lo + p.chunk_rows;
     float sum[8] = {};
-    if (left > 0) {
+    auto rows = [&](auto WHOLE_) {  // (columns wholly inside the matrix: no masks)
+        const int64_t in = decltype(WHOLE_)::value ? (int64_t)8 : left;
 #pragma unroll 4
         for (int64_t row = lo + r; row < hi; row += 8) {
-            const Row8 dy = load8(p.dY + row * p.ldy + col, left);
             float d[8];
-            dy.widen<TYPE>(d);
+            load8(p.dY + row * p.ldy + col, in).widen<TYPE>(d);
             if (p.dZ) {
                 float z[8];
-                load8(p.Z + row * p.ldz + col, left).widen<TYPE>(z);
+                load8(p.Z + row * p.ldz + col, in).widen<TYPE>(z);
                 act_slopes(z, p.act);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) d[e] *= z[e];
-                store8(p.dZ + row * p.lddz + col, Row8::narrow<TYPE>(d), left);
+                store8(p.dZ + row * p.lddz + col, Row8::narrow<TYPE>(d), in);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[e] += d[e];
         }
-    }
+    };
+    if ((int64_t)(blockIdx.y + 1) * 256 <= p.N)
+        rows(std::true_type{});
+    else if (left > 0)
+        rows(std::false_type{});
     if (!p.partial) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) sums[r][c * 8 + e] = sum[e];
@@ -86,7 +93,7 @@ __global__ __launch_bounds__(256) void linear_bias_join_kernel(SlopeProblem p) {
         int64_t before = 0;
         for (int g = c; g < group; g += 64) {
             const RowRange range = group_rows(p.offsets, g, p.M);
-            before += (range.hi - range.lo + kSlopeRows - 1) / kSlopeRows;
+            before += (range.hi - range.lo + p.chunk_rows - 1) / p.chunk_rows;
         }
 #pragma unroll
         for (int d = 32; d > 0; d /= 2) before += __shfl_xor((int)before, d);
@@ -94,7 +101,7 @@ __global__ __launch_bounds__(256) void linear_bias_join_kernel(SlopeProblem p) {
         const RowRange own = group_rows(p.offsets, group, p.M);
         rows = own.hi - own.lo;
     }
-    const int64_t chunks = (rows + kSlopeRows - 1) / kSlopeRows;
+    const int64_t chunks = (rows + p.chunk_rows - 1) / p.chunk_rows;
     float sum = 0.0f;
     if (col < p.N) {
 #pragma unroll 8

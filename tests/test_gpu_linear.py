@@ -233,6 +233,48 @@ def test_many_rows_per_group_sum_in_slices(libs):
     assert torch.equal(g["bias"][0].double(), dy.double().sum(0))
 
 
+def test_last_round_in_slices(libs):
+    """More 256x256 tiles than CUs and a deep contraction: the tiles of the last round are cut along it and joined.
+    Integer values, against float64 on the GPU (exact): forward, dA and dB, dense and grouped."""
+    torch.manual_seed(74)
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    N, K = 4096, 2112
+    M = 256 * (cus // 16) + 200  # a row of 16 tiles past whole rounds, its rows ragged
+
+    def ints(*shape):
+        return torch.randint(-3, 4, shape, device="cuda").to(torch.bfloat16)
+
+    a, b, bias, r = ints(M, K), ints(K, N), ints(N), ints(M, N).float()
+    z = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    d = dft.linear(a, b, bias=bias, residual=r, activation="relu", out_dtype=torch.float32, preact=z,
+                   variant=dft.LINEAR_256x256, splits=1)
+    want = a.double() @ b.double() + bias.double()
+    assert torch.equal(d.double(), want.clamp(min=0) + r.double())
+    assert torch.equal(z, want.to(torch.bfloat16))
+    # groups: rows in none first and last, an empty one, one of a single row
+    counts = [700, 0, 1, 1500, 257, 300]
+    counts.append(M - 13 - sum(counts))
+    offsets = torch.tensor([5, *[5 + sum(counts[: i + 1]) for i in range(len(counts))]], dtype=torch.int32, device="cuda")
+    bg, biasg = ints(len(counts), K, N), ints(len(counts), N)
+    out = torch.full((M, N), 7.0, device="cuda")
+    dft.grouped_linear(a, bg, offsets, bias=biasg, activation="relu", out=out, variant=dft.LINEAR_256x256)
+    lo = 5
+    for g, c in enumerate(counts):
+        want = (a[lo:lo + c].double() @ bg[g].double() + biasg[g].double()).clamp(min=0)
+        assert torch.equal(out[lo:lo + c].double(), want), g
+        lo += c
+    assert bool((out[:5] == 7).all()) and bool((out[lo:] == 7).all())
+    # the gradients' products: dA is M x K from N columns, dB (of transposed sizes) from M rows
+    dy = ints(M, N)
+    b2 = ints(4096, N)
+    g = dft.linear_grad(dy, ints(M, 4096), b2, want=("a",), a_dtype=torch.float32)
+    assert torch.equal(g.a.double(), dy.double() @ b2.double().t())
+    x = ints(2112, M)
+    dy2 = ints(2112, 4096)
+    g = dft.linear_grad(dy2, x, ints(M, 4096), want=("b",), b_dtype=torch.float32)
+    assert torch.equal(g.b.double(), x.double().t() @ dy2.double())
+
+
 def test_empty_sizes(libs):
     gen = torch.Generator().manual_seed(71)
     lib = libs["plain"]
