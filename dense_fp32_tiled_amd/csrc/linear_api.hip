@@ -605,8 +605,11 @@ int launch_rows(const void* kernel, const RowsProblem& problem, bool per_token, 
     if (st != GEMM_OK) return st;
     RowsProblem p = problem;
     void* args[] = {&p};
-    const dim3 grid(per_token ? (unsigned)p.tokens : (unsigned)ceil_div(p.tokens, kRowWaves),
-                    per_token ? 1 : (unsigned)ceil_div(p.cols, kRowCols));
+    p.parts = (uint32_t)ceil_div(p.cols, kRowCols);
+    // a launch has fewer than 2^32 threads: longer batches take several steps of one grid
+    const int64_t waves = per_token ? kRowWaves : p.parts;
+    p.step = std::min(p.tokens, std::max<int64_t>((1 << 24) / waves, 1));
+    const dim3 grid((unsigned)ceil_div(p.step * waves, kRowWaves));
     return hipLaunchKernel(kernel, grid, dim3(kRowWaves * kWave), args, 0, stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }
 

@@ -163,6 +163,20 @@ def test_rows_there_and_back(case, kind):
     assert bool((got[1:-1][~live] == 0).all())
 
 
+def test_more_tokens_than_one_launch_holds():
+    """2^24 tokens and a few more: a launch's threads are fewer than 2^32, so the row kernels take several steps."""
+    tokens = (1 << 24) + 5
+    x = torch.randint(-8, 9, (tokens, 1), device="cuda").to(torch.bfloat16)
+    position = torch.arange(tokens - 1, -1, -1, device="cuda", dtype=torch.int32).view(tokens, 1)
+    weights = torch.randint(1, 5, (tokens, 1), device="cuda").float()
+    rows = dft.expert_gather(x, position)
+    assert torch.equal(rows, x.flip(0))
+    assert torch.equal(dft.expert_combine(rows, position, weights), (x.float() * weights).to(torch.bfloat16))
+    dy, dw = dft.expert_combine_grad(x, rows, position, weights)
+    assert torch.equal(dy, (x.float() * weights).to(torch.bfloat16).flip(0))
+    assert torch.equal(dw, x.float() * x.float())
+
+
 def test_positions_outside_the_rows_are_dropped():
     x = torch.ones(4, 16, dtype=torch.bfloat16, device="cuda")
     position = torch.tensor([[-7], [3], [4], [2 ** 31 - 1]], dtype=torch.int32, device="cuda")
