@@ -39,6 +39,9 @@ int current_cus(int* cus) {
 
 // ---- argument checks ----------------------------------------------------------------
 constexpr int64_t kMaxDim = (int64_t)1 << 40;  // products of a size, a pitch and an element's bytes stay inside int64
+constexpr int64_t kMaxElements = (int64_t)1 << 59;
+constexpr int64_t kMaxProduct = (int64_t)1 << 50;   // M N, M K, K N: 32 fp32 slices of one stay inside int64
+constexpr int64_t kMaxOutPitch = (int64_t)1 << 26;  // 16 rows of fp32 stay inside the epilogue's 32-bit lane offsets
 constexpr int64_t kMaxGrid = 0x7fffffff;
 
 struct Matrix {
@@ -47,11 +50,12 @@ struct Matrix {
 
     bool empty() const { return rows == 0 || cols == 0 || copies == 0; }
     bool pitch_ok() const {
-        return ld >= std::max<int64_t>(cols, 1) && (copies <= 1 || rows == 0 || copy_stride >= (rows - 1) * ld + cols);
+        if (ld < std::max<int64_t>(cols, 1)) return false;
+        // (rows too long to count are refused by small_enough)
+        return copies <= 1 || rows == 0 || rows > kMaxElements / ld || copy_stride >= (rows - 1) * ld + cols;
     }
     bool small_enough() const {
-        const int64_t lim = (int64_t)1 << 59;
-        return rows <= lim / ld && (copies <= 1 || copy_stride <= lim / copies);
+        return rows <= kMaxElements / ld && (copies <= 1 || copy_stride <= kMaxElements / copies);
     }
     int64_t bytes() const {
         return empty() ? 0 : ((copies - 1) * copy_stride + (rows - 1) * ld + cols) * elem;
@@ -68,7 +72,13 @@ struct Matrix {
     }
 };
 
-// Pitches, sizes and presence of every matrix; `absent` may be NULL.
+bool products_ok(int64_t m, int64_t n, int64_t k) {
+    const auto ok = [](int64_t a, int64_t b) { return b == 0 || a <= kMaxProduct / b; };
+    return ok(m, n) && ok(m, k) && ok(k, n);
+}
+bool out_pitch_ok(const Matrix& m) { return !m.data || m.rows <= 1 || m.ld <= kMaxOutPitch; }
+
+// Pitches, sizes and presence of every matrix; an optional one may be NULL.
 struct Use {
     Matrix m;
     bool optional, written;
@@ -304,7 +314,7 @@ int describe(const gemm_linear_args& a, LinearCall* c) {
     if (a.variant < 0 || a.variant >= GEMM_LINEAR_COUNT) return GEMM_ERR_UNSUPPORTED;
     if (a.M < 0 || a.N < 0 || a.K < 0 || a.M > kMaxDim || a.N > kMaxDim || a.K > kMaxDim) return GEMM_ERR_INVALID_DIM;
     if (a.groups < 0 || a.groups > GEMM_LINEAR_MAX_GROUPS || a.splits < 0 || a.splits > kMaxSlices) return GEMM_ERR_INVALID_DIM;
-    if (a.groups > 0 && a.M > 0x7fffffff) return GEMM_ERR_TOO_LARGE;
+    if ((a.groups > 0 && a.M > 0x7fffffff) || !products_ok(a.M, a.N, a.K)) return GEMM_ERR_TOO_LARGE;
     c->groups = a.groups > 0 ? a.groups : 1;
     c->axis = a.groups > 0 ? kGroupRows : kGroupNone;
     const int64_t out = elem_bytes(a.output_type);
@@ -323,7 +333,9 @@ int describe(const gemm_linear_args& a, LinearCall* c) {
     const Use uses[] = {{c->A, !work, false}, {c->B, !work, false}, {c->bias, true, false},
                         {in_place ? Matrix{nullptr, 0, 0, 1, 2} : c->residual, true, false}, {c->preact, true, true},
                         {c->out, !work, true}, {offsets, a.groups == 0 || !work, false}, {space, true, true}};
-    return check_matrices(uses, 8);
+    const int st = check_matrices(uses, 8);
+    if (st != GEMM_OK) return st;
+    return out_pitch_ok(c->out) && out_pitch_ok(c->residual) && out_pitch_ok(c->preact) ? GEMM_OK : GEMM_ERR_TOO_LARGE;
 }
 
 // The operands as they are, or, where their rows are not whole 16 bytes and
@@ -408,7 +420,7 @@ int describe(const gemm_linear_grad_args& a, GradCall* c) {
     if (!known_output(a.a_grad_type) || !known_output(a.b_grad_type)) return GEMM_ERR_UNSUPPORTED;
     if (a.M < 0 || a.N < 0 || a.K < 0 || a.M > kMaxDim || a.N > kMaxDim || a.K > kMaxDim) return GEMM_ERR_INVALID_DIM;
     if (a.groups < 0 || a.groups > GEMM_LINEAR_MAX_GROUPS) return GEMM_ERR_INVALID_DIM;
-    if (a.groups > 0 && a.M > 0x7fffffff) return GEMM_ERR_TOO_LARGE;
+    if ((a.groups > 0 && a.M > 0x7fffffff) || !products_ok(a.M, a.N, a.K)) return GEMM_ERR_TOO_LARGE;
     c->groups = a.groups > 0 ? a.groups : 1;
     c->axis = a.groups > 0 ? kGroupRows : kGroupNone;
     const bool act = a.activation != GEMM_ACT_NONE;
@@ -428,7 +440,9 @@ int describe(const gemm_linear_grad_args& a, GradCall* c) {
                         {in_place ? Matrix{nullptr, 0, 0, 1, 2} : c->dZ, !act || in_place, true},
                         {c->A, !a.dB, false}, {c->B, !a.dA, false}, {c->dA, true, true}, {c->dB, true, true},
                         {c->dbias, true, true}, {offsets, a.groups == 0, false}, {space, true, true}};
-    return check_matrices(uses, 10);
+    const int st = check_matrices(uses, 10);
+    if (st != GEMM_OK) return st;
+    return out_pitch_ok(c->dA) && out_pitch_ok(c->dB) ? GEMM_OK : GEMM_ERR_TOO_LARGE;
 }
 
 Plan plan_a(const gemm_linear_grad_args& a, const GradCall& c, bool direct, int cus) {
@@ -494,8 +508,8 @@ int run_slope(const gemm_linear_grad_args& a, const GradCall& c, float* partial,
     p.partial = a.dbias ? partial : nullptr;
     p.offsets = a.groups > 0 ? a.offsets : nullptr; p.groups = (int32_t)c.groups;
     p.act = a.activation; p.dbias = a.dbias; p.chunk_rows = slope_rows(a);
+    const int64_t chunks = p.chunks = slope_chunks(a, c);
     void* args[] = {&p};
-    const int64_t chunks = slope_chunks(a, c);
     if ((p.dZ || p.partial) && chunks > 0) {
         const void* kernel = a.input_type == GEMM_INPUT_BF16
                                  ? reinterpret_cast<const void*>(linear_slope_kernel<kInputBf16>)

@@ -28,6 +28,7 @@ struct SlopeProblem {
     int32_t groups;
     int32_t act;
     int32_t chunk_rows;
+    int64_t chunks;              // places in partial
     float* dbias;                // groups x N, rows N apart
 };
 
@@ -101,7 +102,8 @@ __global__ __launch_bounds__(256) void linear_bias_join_kernel(SlopeProblem p) {
         const RowRange own = group_rows(p.offsets, group, p.M);
         rows = own.hi - own.lo;
     }
-    const int64_t chunks = (rows + p.chunk_rows - 1) / p.chunk_rows;
+    int64_t chunks = (rows + p.chunk_rows - 1) / p.chunk_rows;
+    if (chunks > p.chunks - first) chunks = p.chunks - first;  // (groups that overlap have more chunks than places)
     float sum = 0.0f;
     if (col < p.N) {
 #pragma unroll 8

@@ -4,8 +4,9 @@ The ``gemm_*`` functions forward to the entry points of the same name
 (include/dense_fp32_tiled.h).  ``linear``, ``grouped_linear``, their
 ``*_grad`` and the ``expert_*`` functions take torch tensors; like ``matmul``
 they check types, layouts, shapes and devices before anything is launched,
-enqueue on ``stream`` or torch's current stream of the tensors' device, and
-raise GemmError on a non-zero status.
+enqueue on ``stream`` (a torch.cuda.Stream or raw handle) or torch's current
+stream of the tensors' device, and raise GemmError on a non-zero status.  What
+they allocate (results, workspaces) is allocated on the stream they run on.
 """
 
 from __future__ import annotations
@@ -228,13 +229,20 @@ def _gpu(t, name):
     return t.device
 
 
-def _run(entry, what, device, stream, *args):
-    """One entry point on the tensors' device and stream."""
+def _current(stream, device):
+    """A context with `stream` torch's current one.  The whole call runs inside it, so that a workspace's memory goes
+    back to that stream's pool: from another stream's it could be handed out again while the call's work is queued."""
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, expected {device}")
+    return torch.cuda.stream(stream)
+
+
+def _run(entry, what, device, *args):
+    """One entry point on the tensors' device, on torch's current stream of it."""
     index = device.index
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(index)
-    else:
-        handle = stream if isinstance(stream, int) else stream.cuda_stream
+    handle = torch._C._cuda_getCurrentRawStream(index)
     if torch._C._cuda_getDevice() == index:
         st = entry(*args, handle)
     else:
@@ -261,6 +269,10 @@ def _workspace(args, need, what, given, device):
 def _linear(a, b, offsets, bias, residual, activation, out, out_dtype, preact, workspace, stream, variant, splits):
     dtype, kind = getattr(a, "dtype", None), _input_type(a, "a")
     device = _gpu(a, "a")
+    if stream is not None:
+        with _current(stream, device):
+            return _linear(a, b, offsets, bias, residual, activation, out, out_dtype, preact, workspace, None,
+                           variant, splits)
     grouped = offsets is not None
     if a.dim() != 2 or not isinstance(b, _Tensor) or b.dim() != 2 + grouped:
         raise TypeError(f"a must be a 2-D tensor and b a {2 + grouped}-D one")
@@ -298,7 +310,7 @@ def _linear(a, b, offsets, bias, residual, activation, out, out_dtype, preact, w
     lib = dft.library()
     keep = _workspace(g, lib.gemm_linear_workspace_bytes(g, _num_cus(device)), "gemm_linear_workspace_bytes",
                       workspace, device)
-    _run(lib.gemm_linear, "gemm_linear", device, stream, g)
+    _run(lib.gemm_linear, "gemm_linear", device, g)
     del keep
     return out
 
@@ -326,6 +338,9 @@ def grouped_linear(a, b, offsets, bias=None, residual=None, activation="none", o
 def _linear_grad(dy, a, b, offsets, preact, activation, want, a_dtype, b_dtype, workspace, stream):
     dtype, kind = getattr(a, "dtype", None), _input_type(a, "a")
     device = _gpu(a, "a")
+    if stream is not None:
+        with _current(stream, device):
+            return _linear_grad(dy, a, b, offsets, preact, activation, want, a_dtype, b_dtype, workspace, None)
     grouped = offsets is not None
     if a.dim() != 2 or not isinstance(b, _Tensor) or b.dim() != 2 + grouped:
         raise TypeError(f"a must be a 2-D tensor and b a {2 + grouped}-D one")
@@ -371,7 +386,7 @@ def _linear_grad(dy, a, b, offsets, preact, activation, want, a_dtype, b_dtype, 
     lib = dft.library()
     keep = _workspace(g, lib.gemm_linear_grad_workspace_bytes(g, _num_cus(device)),
                       "gemm_linear_grad_workspace_bytes", workspace, device)
-    _run(lib.gemm_linear_grad, "gemm_linear_grad", device, stream, g)
+    _run(lib.gemm_linear_grad, "gemm_linear_grad", device, g)
     del keep
     return LinearGrads(da, db, dbias, dz)
 
@@ -403,6 +418,9 @@ def expert_sort(experts, num_experts: int, stream=None):
     if not isinstance(experts, _Tensor) or experts.dim() != 2:
         raise TypeError("experts must be a 2-D torch.int32 tensor")
     device = _gpu(experts, "experts")
+    if stream is not None:
+        with _current(stream, device):
+            return expert_sort(experts, num_experts)
     tokens, top_k = experts.shape
     src = _list(experts, "experts", (tokens, top_k), _int32, device)
     need = gemm_expert_sort_workspace_bytes(tokens, top_k, num_experts)
@@ -415,7 +433,7 @@ def expert_sort(experts, num_experts: int, stream=None):
     position = buf[num_experts + 1 + pairs: num_experts + 1 + 2 * pairs].view(tokens, top_k)
     at = buf.data_ptr()
     end = at + 4 * (num_experts + 1 + 2 * pairs)
-    _run(dft.library().gemm_expert_sort, "gemm_expert_sort", device, stream, tokens, top_k, num_experts, src, at,
+    _run(dft.library().gemm_expert_sort, "gemm_expert_sort", device, tokens, top_k, num_experts, src, at,
          at + 4 * (num_experts + 1), at + 4 * (num_experts + 1 + pairs), end if need else None, need)
     return offsets, order, position
 
@@ -431,6 +449,9 @@ def expert_gather(x, position, out=None, stream=None):
     """The tokens' rows in expert order, by gemm_expert_gather: row position[t, j] of the result is x[t].  The
     result has tokens * top_k rows (or ``out``'s); rows that no pair has are left as they were."""
     kind, device = _input_type(x, "x"), _gpu(x, "x")
+    if stream is not None:
+        with _current(stream, device):
+            return expert_gather(x, position, out)
     tokens, top_k, pos = _positions(position, device)
     cols = x.shape[-1] if x.dim() == 2 else -1
     px, ldx = _matrix(x, "x", tokens, cols, x.dtype, device)
@@ -438,7 +459,7 @@ def expert_gather(x, position, out=None, stream=None):
         out = torch.empty((tokens * top_k, cols), dtype=x.dtype, device=device)
     rows = out.shape[0] if isinstance(out, _Tensor) and out.dim() == 2 else -1
     po, ldo = _matrix(out, "out", rows, cols, x.dtype, device)
-    _run(dft.library().gemm_expert_gather, "gemm_expert_gather", device, stream, kind, tokens, rows, top_k, cols, px,
+    _run(dft.library().gemm_expert_gather, "gemm_expert_gather", device, kind, tokens, rows, top_k, cols, px,
          ldx, pos, po, ldo)
     return out
 
@@ -447,6 +468,9 @@ def expert_combine(y, position, weights=None, out=None, stream=None):
     """The experts' rows back in token order, by gemm_expert_combine: result[t] = sum over j of weights[t, j] *
     y[position[t, j]] (weights: tokens x top_k float32, or None for ones: the gradient of expert_gather)."""
     kind, device = _input_type(y, "y"), _gpu(y, "y")
+    if stream is not None:
+        with _current(stream, device):
+            return expert_combine(y, position, weights, out)
     tokens, top_k, pos = _positions(position, device)
     rows, cols = y.shape if y.dim() == 2 else (-1, -1)
     py, ldy = _matrix(y, "y", rows, cols, y.dtype, device)
@@ -454,7 +478,7 @@ def expert_combine(y, position, weights=None, out=None, stream=None):
     if out is None:
         out = torch.empty((tokens, cols), dtype=y.dtype, device=device)
     po, ldo = _matrix(out, "out", tokens, cols, y.dtype, device)
-    _run(dft.library().gemm_expert_combine, "gemm_expert_combine", device, stream, kind, tokens, rows, top_k, cols,
+    _run(dft.library().gemm_expert_combine, "gemm_expert_combine", device, kind, tokens, rows, top_k, cols,
          py, ldy, pos, pw, po, ldo)
     return out
 
@@ -464,6 +488,9 @@ def expert_combine_grad(dout, y, position, weights=None, dy=None, stream=None):
     j] * dout[t] and dweights[t, j] = y[position[t, j]] . dout[t] (float32; None without weights).  Rows of dy that
     no pair has are left as they were."""
     kind, device = _input_type(y, "y"), _gpu(y, "y")
+    if stream is not None:
+        with _current(stream, device):
+            return expert_combine_grad(dout, y, position, weights, dy)
     tokens, top_k, pos = _positions(position, device)
     rows, cols = y.shape if y.dim() == 2 else (-1, -1)
     py, ldy = _matrix(y, "y", rows, cols, y.dtype, device)
@@ -476,7 +503,7 @@ def expert_combine_grad(dout, y, position, weights=None, dy=None, stream=None):
     if dy is None:
         dy = torch.empty((rows, cols), dtype=y.dtype, device=device)
     pdy, lddy = _matrix(dy, "dy", rows, cols, y.dtype, device)
-    _run(dft.library().gemm_expert_combine_grad, "gemm_expert_combine_grad", device, stream, kind, tokens, rows,
+    _run(dft.library().gemm_expert_combine_grad, "gemm_expert_combine_grad", device, kind, tokens, rows,
          top_k, cols, pd, ldd, py, ldy, pos, pw, pdy, lddy, pdw)
     return dy, dweights
 
@@ -499,18 +526,21 @@ def expert_mlp(x, experts, weights, w1, w2, b1=None, b2=None, activation="silu",
 
     x: tokens x D; experts: tokens x top_k int32; weights: tokens x top_k float32; w1: E x D x H; w2: E x H x D;
     b1: E x H; b2: E x D.  Returns (out, state); state is what expert_mlp_grad needs."""
-    if torch is None:
-        _bind()
+    _input_type(x, "x")
     if not isinstance(w1, _Tensor) or w1.dim() != 3:
         raise TypeError("w1 must be a 3-D tensor")
-    offsets, _, position = expert_sort(experts, w1.shape[0], stream=stream)
-    rows = expert_gather(x, position, stream=stream)
+    device = _gpu(x, "x")
+    if stream is not None:
+        with _current(stream, device):
+            return expert_mlp(x, experts, weights, w1, w2, b1, b2, activation)
+    offsets, _, position = expert_sort(experts, w1.shape[0])
+    rows = expert_gather(x, position)
     preact = None
     if activation != "none":
-        preact = torch.empty((rows.shape[0], w1.shape[2]), dtype=x.dtype, device=x.device)
-    hidden = grouped_linear(rows, w1, offsets, bias=b1, activation=activation, preact=preact, stream=stream)
-    back = grouped_linear(hidden, w2, offsets, bias=b2, stream=stream)
-    out = expert_combine(back, position, weights, stream=stream)
+        preact = torch.empty((rows.shape[0], w1.shape[2]), dtype=x.dtype, device=device)
+    hidden = grouped_linear(rows, w1, offsets, bias=b1, activation=activation, preact=preact)
+    back = grouped_linear(hidden, w2, offsets, bias=b2)
+    out = expert_combine(back, position, weights)
     return out, ExpertState(offsets, position, rows, preact, hidden, back)
 
 
@@ -525,9 +555,12 @@ class ExpertGrads(NamedTuple):
 
 def expert_mlp_grad(dout, state: ExpertState, weights, w1, w2, activation="silu", stream=None) -> ExpertGrads:
     """Gradients of expert_mlp for its output's gradient dout (tokens x D); the biases' are float32."""
-    dback, dweights = expert_combine_grad(dout, state.back, state.position, weights, stream=stream)
-    g2 = grouped_linear_grad(dback, state.hidden, w2, state.offsets, stream=stream)
-    g1 = grouped_linear_grad(g2.a, state.rows, w1, state.offsets, preact=state.preact, activation=activation,
-                             stream=stream)
-    dx = expert_combine(g1.a, state.position, stream=stream)
+    _input_type(dout, "dout")
+    if stream is not None:
+        with _current(stream, _gpu(dout, "dout")):
+            return expert_mlp_grad(dout, state, weights, w1, w2, activation)
+    dback, dweights = expert_combine_grad(dout, state.back, state.position, weights)
+    g2 = grouped_linear_grad(dback, state.hidden, w2, state.offsets)
+    g1 = grouped_linear_grad(g2.a, state.rows, w1, state.offsets, preact=state.preact, activation=activation)
+    dx = expert_combine(g1.a, state.position)
     return ExpertGrads(dx, dweights, g1.b, g1.bias, g2.b, g2.bias)

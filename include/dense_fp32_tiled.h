@@ -459,11 +459,14 @@ int gemm_mixed_auto_variant(int64_t M, int64_t N, int64_t K, int32_t num_cus);
  *   - `offsets` is read on the device: groups + 1 ascending row numbers.  Rows
  *     before the first and from the last on belong to no group: their D, Z
  *     and dA are left as they were and they add nothing to dB and dbias.  An
- *     empty group's dB and dbias are zero.  Values outside [0, M], or smaller
- *     than one before them, are taken as the nearest ones that are not.
+ *     empty group's dB and dbias are zero.  Values outside [0, M] are taken as
+ *     the nearest inside; values that descend leave what the groups' outputs
+ *     hold unspecified, but nothing outside the matrices is read or written.
  *   - D may be the residual itself (same address and pitch), and dZ may be dY;
  *     no other output may overlap any operand (GEMM_ERR_ALIAS).
  *   - K == 0 gives Z = bias; M == 0 gives dB = 0 and dbias = 0; N == 0 gives dA = 0.
+ *   - GEMM_ERR_TOO_LARGE: M N, M K or K N above 2^50, grouped M above 2^31 - 1,
+ *     and pitches of D, residual, preact, dA and dB above 2^26 elements.
  *   - The activations' limits hold for large |Z|: no infinite intermediate
  *     makes a NaN of a finite Z. */
 typedef enum {

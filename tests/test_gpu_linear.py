@@ -420,6 +420,61 @@ def test_python_entry_points_match_float64(libs):
     assert g.preact is DY and g.b is None and g.bias is None
 
 
+def test_workspaces_belong_to_the_stream_of_the_call(libs):
+    """With `stream` given, memory that the caller's own stream allocates while the call is queued is none of the
+    call's: the caller overwrites it at once, long before the call's turn."""
+    gen = torch.Generator().manual_seed(83)
+    x, w = ref.draw(gen, (16, 4096), torch.bfloat16).cuda(), ref.draw(gen, (4096, 1024), torch.bfloat16, scale=0.02).cuda()
+    dy, z = ref.draw(gen, (16, 1024), torch.bfloat16).cuda(), ref.draw(gen, (16, 1024), torch.bfloat16).cuda()
+    big = torch.randn(4096, 4096, device="cuda")
+    eager = dft.linear(x, w, splits=8)
+    grads = dft.linear_grad(dy, x, w, preact=z, activation="silu")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                big @ big
+        got = dft.linear(x, w, splits=8, stream=stream)
+        got_grads = dft.linear_grad(dy, x, w, preact=z, activation="silu", stream=stream)
+        spoiled = [torch.full((16 * 1024 * splits,), float("nan"), device="cuda") for splits in (1, 2, 4, 8, 16, 32, 8, 4)]
+        torch.cuda.synchronize()
+        assert torch.equal(got, eager)
+        assert all(torch.equal(p, q) for p, q in zip(got_grads, grads))
+        del spoiled
+
+
+def test_largest_output_pitch(libs):
+    """Rows 2^26 elements apart: the epilogue's offsets within 16 rows reach their largest."""
+    gen = torch.Generator().manual_seed(84)
+    x, w = ref.draw(gen, (17, 72), torch.bfloat16), ref.draw(gen, (72, 40), torch.bfloat16)
+    pitch = 1 << 26
+    wide = torch.empty(16 * pitch + 40, dtype=torch.float32, device="cuda")
+    out = wide.as_strided((17, 40), (pitch, 1))
+    dft.linear(x.cuda(), w.cuda(), out=out)
+    ref.assert_within(out, ref.forward(x, w[None], out_dtype=torch.float32)[0], "pitch 2^26")
+    with pytest.raises(dft.GemmError):
+        dft.linear(x[:2].cuda(), w.cuda(), out=wide.as_strided((2, 40), (pitch + 1, 1)))
+
+
+def test_descending_offsets_stay_inside(libs):
+    """Groups that overlap have more chunks of rows than there are places for their sums: none outside is read."""
+    M, N, K, groups = 64, 8, 16, 5
+    gen = torch.Generator().manual_seed(85)
+    dy = ref.draw(gen, (M, N), torch.bfloat16).cuda()
+    offsets = torch.tensor([0, 64, 0, 64, 0, 64], dtype=torch.int32, device="cuda")
+    dbias = torch.empty(groups, N, device="cuda")
+    g = dft.LinearGradArgs(groups=groups, M=M, N=N, K=K, offsets=offsets.data_ptr(), dY=dy.data_ptr(), ldy=N,
+                           dbias=dbias.data_ptr())
+    need = dft.gemm_linear_grad_workspace_bytes(g, torch.cuda.get_device_properties(0).multi_processor_count)
+    assert 0 < need < 64 * N * 4
+    space = torch.full((64 * N,), float("nan"), device="cuda")
+    g.workspace, g.workspace_bytes = space.data_ptr(), need
+    assert dft.gemm_linear_grad(g, torch.cuda.current_stream().cuda_stream) == dft.GEMM_OK
+    assert bool(torch.isfinite(dbias).all())
+    assert bool(space[need // 4:].isnan().all())
+
+
 def test_streams_and_graphs(libs):
     """Two calls at once on two streams, and a captured call replayed between eager ones."""
     gen = torch.Generator().manual_seed(82)

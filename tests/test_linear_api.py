@@ -49,6 +49,8 @@ def grad_args(M=64, N=32, K=48, **kw):
     (dict(workspace=D, workspace_bytes=4), "ALIAS"), (dict(workspace=W, workspace_bytes=-1), "WORKSPACE"),
     (dict(lda=1 << 60), "TOO_LARGE"), (dict(M=1 << 41), "INVALID_DIM"),
     (dict(M=1 << 31, groups=1, offsets=R), "TOO_LARGE"),
+    (dict(ldd=(1 << 26) + 1), "TOO_LARGE"), (dict(residual=R, ldr=(1 << 26) + 1), "TOO_LARGE"),
+    (dict(preact=P, ldp=(1 << 26) + 1), "TOO_LARGE"),
 ])
 def test_linear_refusals(kw, status, gemm_lib):
     want = getattr(dft, "GEMM_ERR_" + status)
@@ -56,6 +58,18 @@ def test_linear_refusals(kw, status, gemm_lib):
     assert dft.gemm_linear(args) == want
     if status not in ("WORKSPACE",) and "workspace" not in kw:
         assert dft.gemm_linear_workspace_bytes(args, 256) == want
+
+
+def test_sizes_without_a_place_in_64_bits(gemm_lib):
+    """Products of sizes that the byte counts could not hold are refused, by the queries too."""
+    big = 1 << 26
+    g = linear_args(M=big, N=big, K=8, lda=8, ldb=big, ldd=big)
+    assert dft.gemm_linear_workspace_bytes(g, 256) == dft.GEMM_ERR_TOO_LARGE
+    assert dft.gemm_linear(g) == dft.GEMM_ERR_TOO_LARGE
+    d = grad_args(M=big, N=big, K=8, ldy=big, lda=8, ldb=big, ldda=8, lddb=big)
+    assert dft.gemm_linear_grad_workspace_bytes(d, 256) == dft.GEMM_ERR_TOO_LARGE
+    # (matrices so far apart that their rows' elements cannot be counted)
+    assert dft.gemm_linear(linear_args(groups=2, offsets=R, ldb=1 << 60, b_stride=1)) == dft.GEMM_ERR_TOO_LARGE
 
 
 def test_null_arguments(gemm_lib):
