@@ -572,17 +572,28 @@ struct LinearShape {
 };
 
 // Consecutive tiles on one XCD (workgroups go to the eight XCDs in turn), in
-// panels of eight tile rows, so that the tiles an XCD works on at one time
+// panels of `high` tile rows, so that the tiles an XCD works on at one time
 // share their operands' rows and columns in its L2.
 struct TilePlace {
     int64_t row, col;
 };
-__device__ inline TilePlace place_of_block(uint32_t block, uint32_t blocks, uint32_t tiles_m, uint32_t tiles_n) {
+__device__ inline TilePlace place_of_block(uint32_t block, uint32_t blocks, uint32_t tiles_m, uint32_t tiles_n,
+                                           uint32_t high) {
     const uint32_t xcd = block % 8, each = blocks / 8, more = blocks % 8;
     const uint32_t id = xcd * each + (xcd < more ? xcd : more) + block / 8;
-    const uint32_t panel = 8 * tiles_n, p = id / panel, in = id % panel;
-    const uint32_t high = tiles_m - 8 * p < 8 ? tiles_m - 8 * p : 8;
-    return TilePlace{8 * p + in % high, in / high};
+    const uint32_t panel = high * tiles_n, p = id / panel, in = id % panel;
+    const uint32_t rows = tiles_m - high * p < high ? tiles_m - high * p : high;
+    return TilePlace{high * p + in % rows, in / rows};
+}
+// Four tile rows for 256x256 tiles: the XCDs' panels are then more often whole
+// ones, which move over B's columns together (8192^3 with bias, activation,
+// residual and pre-activation 855 us with panels of 8, 838 with 4, 870 with
+// 16).  Eight for grouped rows (each group has a B of its own: 546 against 552
+// us for 8 groups of about 2048 rows by 4096, 4096 deep) and for the smaller
+// tiles, of which an XCD works on 64 at a time.
+template <int BM>
+__device__ inline uint32_t panel_rows(const LinearProblem& p) {
+    return BM == 256 && p.axis != kGroupRows ? 4 : 8;
 }
 
 // Tiles of all groups' rows.
@@ -667,7 +678,7 @@ struct LinearWork {
 template <bool AK, bool BK_, int BM, int BN>
 __device__ inline LinearWork linear_work(const LinearProblem& p, uint32_t tile, uint32_t tiles_m, uint32_t tiles_n,
                                          uint32_t y) {
-    const TilePlace place = place_of_block(tile, tiles_m * tiles_n, tiles_m, tiles_n);
+    const TilePlace place = place_of_block(tile, tiles_m * tiles_n, tiles_m, tiles_n, panel_rows<BM>(p));
     LinearWork w{place.row * BM, p.R, place.col * BN, 0, p.L, p.A, p.B, nullptr, p.C, false};
     if (p.axis == kGroupRows) {
         const GroupTile gt = find_group_tile(p.offsets, p.groups, p.R, BM, place.row);
