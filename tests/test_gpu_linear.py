@@ -275,6 +275,45 @@ def test_last_round_in_slices(libs):
     assert torch.equal(g.b.double(), x.double().t() @ dy2.double())
 
 
+@pytest.mark.parametrize("grouped", [False, True], ids=["one", "grouped"])
+def test_odd_widths_are_packed(grouped, libs):
+    """Products large enough that operands of odd widths are copied to rows of whole 16 bytes first (which takes
+    workspace), forward and gradients, B's matrices apart: integer values, exact."""
+    torch.manual_seed(75)
+    counts = [300, 0, 1, 517] if grouped else [818]
+    M, N, K, E = sum(counts) + 7, 777, 1001, len(counts)
+
+    def ints(*shape):
+        return torch.randint(-2, 3, shape, device="cuda").to(torch.float16)
+
+    a, dy = ints(M, K + 1)[:, 1:], ints(M, N)
+    b, bias = ints(E, K + 2, N)[:, :K], ints(E, N)
+    lo, hi = (3, M - 4) if grouped else (0, M)
+    offsets = torch.tensor([3 + sum(counts[:i]) for i in range(E + 1)], dtype=torch.int32, device="cuda")
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    g = dft.LinearArgs(input_type=dft.INPUT_F16, splits=1, groups=E if grouped else 0, M=M, N=N, K=K, A=a.data_ptr(),
+                       lda=K + 1, B=b.data_ptr(), ldb=N, b_stride=(K + 2) * N, offsets=offsets.data_ptr(), D=1 << 46,
+                       ldd=N)
+    assert dft.gemm_linear_workspace_bytes(g, cus) >= 2 * M * (K + 7)
+    if grouped:
+        out = torch.full((M, N), 9.0, device="cuda")
+        dft.grouped_linear(a, b, offsets, bias=bias, out=out)
+        grads = dft.grouped_linear_grad(dy, a, b, offsets, a_dtype=torch.float32, b_dtype=torch.float32)
+        assert bool((out[:lo] == 9).all()) and bool((out[hi:] == 9).all())
+    else:
+        out = dft.linear(a, b[0], bias=bias[0], out_dtype=torch.float32)
+        grads = dft.linear_grad(dy, a, b[0], a_dtype=torch.float32, b_dtype=torch.float32)
+        grads = grads._replace(b=grads.b[None], bias=grads.bias[None])
+        counts[0] = M
+    for e, c in enumerate(counts):
+        A, D = a[lo:lo + c].double(), dy[lo:lo + c].double()
+        assert torch.equal(out[lo:lo + c].double(), A @ b[e].double() + bias[e].double()), e
+        assert torch.equal(grads.a[lo:lo + c].double(), D @ b[e].double().t()), e
+        assert torch.equal(grads.b[e].double(), A.t() @ D), e
+        assert torch.equal(grads.bias[e].double(), D.sum(0)), e
+        lo += c
+
+
 def test_empty_sizes(libs):
     gen = torch.Generator().manual_seed(71)
     lib = libs["plain"]
