@@ -224,7 +224,7 @@ def _list(t, name, shape, dtype, device):
 
 
 def _gpu(t, name):
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU device")
     return t.device
 
@@ -294,7 +294,7 @@ def _linear(a, b, offsets, bias, residual, activation, out, out_dtype, preact, w
         if bias is not None:
             g.bias = _list(bias, "bias", (N,), dtype, device)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or dtype, device=device)
+        out = torch.empty(M, N, dtype=out_dtype or dtype, device=device)
     elif out_dtype is not None and getattr(out, "dtype", None) is not out_dtype:
         raise TypeError(f"out must be a 2-D {out_dtype} tensor")
     out_type = getattr(out, "dtype", None)
@@ -372,10 +372,10 @@ def _linear_grad(dy, a, b, offsets, preact, activation, want, a_dtype, b_dtype, 
         if preact is None:
             raise ValueError(f"the gradient of {activation} needs preact")
         g.Z, g.ldz = _matrix(preact, "preact", M, N, dtype, device)
-        dz = torch.empty((M, N), dtype=dtype, device=device)
+        dz = torch.empty(M, N, dtype=dtype, device=device)
         g.dZ, g.lddz = dz.data_ptr(), max(N, 1)
     if "a" in want:
-        da = torch.empty((M, K), dtype=types[a_dtype][0], device=device)
+        da = torch.empty(M, K, dtype=types[a_dtype][0], device=device)
         g.dA, g.ldda, g.a_grad_type = da.data_ptr(), max(K, 1), types[a_dtype][1]
     if "b" in want:
         db = torch.empty(b.shape, dtype=types[b_dtype][0], device=device)
@@ -426,15 +426,13 @@ def expert_sort(experts, num_experts: int, stream=None):
     need = gemm_expert_sort_workspace_bytes(tokens, top_k, num_experts)
     if need < 0:
         raise dft.GemmError(need, "gemm_expert_sort")
-    # one allocation for the three results and the workspace
     pairs = tokens * top_k
-    buf = torch.empty(num_experts + 1 + 2 * pairs + need // 4, dtype=torch.int32, device=device)
-    offsets, order = buf[: num_experts + 1], buf[num_experts + 1: num_experts + 1 + pairs]
-    position = buf[num_experts + 1 + pairs: num_experts + 1 + 2 * pairs].view(tokens, top_k)
-    at = buf.data_ptr()
-    end = at + 4 * (num_experts + 1 + 2 * pairs)
-    _run(dft.library().gemm_expert_sort, "gemm_expert_sort", device, tokens, top_k, num_experts, src, at,
-         at + 4 * (num_experts + 1), at + 4 * (num_experts + 1 + pairs), end if need else None, need)
+    offsets = torch.empty(num_experts + 1, dtype=_int32, device=device)
+    order = torch.empty(pairs, dtype=_int32, device=device)
+    position = torch.empty(tokens, top_k, dtype=_int32, device=device)
+    space = torch.empty(need // 4, dtype=_int32, device=device) if need else None
+    _run(dft.library().gemm_expert_sort, "gemm_expert_sort", device, tokens, top_k, num_experts, src,
+         offsets.data_ptr(), order.data_ptr(), position.data_ptr(), space.data_ptr() if need else None, need)
     return offsets, order, position
 
 
@@ -456,7 +454,7 @@ def expert_gather(x, position, out=None, stream=None):
     cols = x.shape[-1] if x.dim() == 2 else -1
     px, ldx = _matrix(x, "x", tokens, cols, x.dtype, device)
     if out is None:
-        out = torch.empty((tokens * top_k, cols), dtype=x.dtype, device=device)
+        out = torch.empty(tokens * top_k, cols, dtype=x.dtype, device=device)
     rows = out.shape[0] if isinstance(out, _Tensor) and out.dim() == 2 else -1
     po, ldo = _matrix(out, "out", rows, cols, x.dtype, device)
     _run(dft.library().gemm_expert_gather, "gemm_expert_gather", device, kind, tokens, rows, top_k, cols, px,
@@ -476,7 +474,7 @@ def expert_combine(y, position, weights=None, out=None, stream=None):
     py, ldy = _matrix(y, "y", rows, cols, y.dtype, device)
     pw = None if weights is None else _list(weights, "weights", (tokens, top_k), _f32, device)
     if out is None:
-        out = torch.empty((tokens, cols), dtype=y.dtype, device=device)
+        out = torch.empty(tokens, cols, dtype=y.dtype, device=device)
     po, ldo = _matrix(out, "out", tokens, cols, y.dtype, device)
     _run(dft.library().gemm_expert_combine, "gemm_expert_combine", device, kind, tokens, rows, top_k, cols,
          py, ldy, pos, pw, po, ldo)
@@ -498,10 +496,10 @@ def expert_combine_grad(dout, y, position, weights=None, dy=None, stream=None):
     pw = pdw = dweights = None
     if weights is not None:
         pw = _list(weights, "weights", (tokens, top_k), _f32, device)
-        dweights = torch.empty((tokens, top_k), dtype=torch.float32, device=device)
+        dweights = torch.empty(tokens, top_k, dtype=torch.float32, device=device)
         pdw = dweights.data_ptr()
     if dy is None:
-        dy = torch.empty((rows, cols), dtype=y.dtype, device=device)
+        dy = torch.empty(rows, cols, dtype=y.dtype, device=device)
     pdy, lddy = _matrix(dy, "dy", rows, cols, y.dtype, device)
     _run(dft.library().gemm_expert_combine_grad, "gemm_expert_combine_grad", device, kind, tokens, rows,
          top_k, cols, pd, ldd, py, ldy, pos, pw, pdy, lddy, pdw)
@@ -537,7 +535,7 @@ def expert_mlp(x, experts, weights, w1, w2, b1=None, b2=None, activation="silu",
     rows = expert_gather(x, position)
     preact = None
     if activation != "none":
-        preact = torch.empty((rows.shape[0], w1.shape[2]), dtype=x.dtype, device=device)
+        preact = torch.empty(rows.shape[0], w1.shape[2], dtype=x.dtype, device=device)
     hidden = grouped_linear(rows, w1, offsets, bias=b1, activation=activation, preact=preact)
     back = grouped_linear(hidden, w2, offsets, bias=b2)
     out = expert_combine(back, position, weights)
