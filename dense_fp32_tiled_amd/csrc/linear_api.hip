@@ -623,7 +623,8 @@ int launch_rows(const void* kernel, const RowsProblem& problem, bool per_token, 
     // a launch has fewer than 2^32 threads: longer batches take several steps of one grid
     const int64_t waves = per_token ? kRowWaves : p.parts;
     p.step = std::min(p.tokens, std::max<int64_t>((1 << 24) / waves, 1));
-    const dim3 grid((unsigned)ceil_div(p.step * waves, kRowWaves));
+    // (per token: a workgroup for each choice where there are fewer than four tokens per CU)
+    const dim3 grid((unsigned)ceil_div(p.step * waves, kRowWaves), per_token && p.tokens < 4 * cus ? p.top_k : 1);
     return hipLaunchKernel(kernel, grid, dim3(kRowWaves * kWave), args, 0, stream) == hipSuccess ? GEMM_OK : GEMM_ERR_HIP;
 }
 
