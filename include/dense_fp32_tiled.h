@@ -484,8 +484,9 @@ typedef enum {
 
 /* Workgroup tiles (AUTO picks one and a number of slices of K from the sizes;
  * gemm_linear_choice).  Operands whose address, pitch or width is not a
- * multiple of 16 bytes go through registers, with 128x128 in place of
- * 256x256. */
+ * multiple of 16 bytes are copied to rows that are (in the workspace) where
+ * the product wins that time back; else they go through registers, with
+ * 128x128 in place of 256x256. */
 typedef enum {
     GEMM_LINEAR_AUTO = 0,
     GEMM_LINEAR_256x256 = 1,
@@ -502,7 +503,7 @@ typedef struct {
     int32_t output_type;  /* gemm_output_type of D and residual */
     int32_t activation;   /* gemm_activation */
     int32_t variant;      /* gemm_linear_variant */
-    int32_t splits;       /* slices of K joined in ascending order: 0 automatic, 1..32 (1 with groups) */
+    int32_t splits;       /* slices of K, joined in a fixed order: 0 automatic, 1..32 (ignored with groups) */
     int32_t groups;       /* 0: one B */
     int64_t M, N, K;
     const void *A;
@@ -522,12 +523,17 @@ typedef struct {
     int64_t workspace_bytes;
 } gemm_linear_args;
 
-/* Z, D as above, enqueued on `stream`.  Returns a gemm_status. */
+/* Z, D as above, enqueued on `stream`.  The workspace is the call's until its
+ * work on `stream` has ended: calls that may run at the same time, captured
+ * ones too, each need their own.  Sums run in a fixed order: the same
+ * arguments and inputs give the same bits.  Returns a gemm_status. */
 int gemm_linear(const gemm_linear_args *args, void *stream);
 
 /* Bytes gemm_linear needs for these arguments (workspace fields ignored) on a
- * device with num_cus compute units: the slices' partial products, splits * M
- * * N * 4, or 0.  Pure host call; a negative gemm_status on bad arguments. */
+ * device with num_cus compute units, or 0: packed operands, and the slices'
+ * partial products in fp32 (splits * M * N, or one 256x256 block per compute
+ * unit where the last round of tiles is cut along K).  Pure host call; a
+ * negative gemm_status on bad arguments. */
 int64_t gemm_linear_workspace_bytes(const gemm_linear_args *args, int32_t num_cus);
 
 /* The tile and the number of slices gemm_linear runs these arguments with.
@@ -557,12 +563,12 @@ typedef struct {
     void *dB;             /* K x N per group, or NULL */
     int64_t lddb, db_stride;
     float *dbias;         /* groups x N packed, or NULL */
-    void *workspace;
+    void *workspace;      /* DEVICE, 16-byte aligned; may be NULL when gemm_linear_grad_workspace_bytes is 0 */
     int64_t workspace_bytes;
 } gemm_linear_grad_args;
 
-/* The gradients above, enqueued on `stream`.  Sums run in a fixed order: the
- * same inputs give the same bits.  Returns a gemm_status. */
+/* The gradients above, enqueued on `stream`; workspace and order of sums as
+ * gemm_linear's.  Returns a gemm_status. */
 int gemm_linear_grad(const gemm_linear_grad_args *args, void *stream);
 
 /* Bytes gemm_linear_grad needs, as gemm_linear_workspace_bytes. */
@@ -575,15 +581,17 @@ int64_t gemm_linear_grad_workspace_bytes(const gemm_linear_grad_args *args, int3
  *     offsets[e]                    first sorted row of expert e; offsets[num_experts]: rows in all
  *     order[s]                      pair (token * top_k + choice) of sorted row s; -1 from offsets[num_experts] on
  *     position[token * top_k + j]   sorted row of that pair; -1 when its expert is outside [0, num_experts) (dropped)
- * num_experts is 1..1024.  All arrays are on the device; workspace as
- * gemm_expert_sort_workspace_bytes says (0 up to 4096 pairs). */
+ * num_experts is 1..1024; more than 2^31 - 1 pairs (rows, below) are
+ * GEMM_ERR_TOO_LARGE.  All arrays are on the device; workspace (4-byte
+ * aligned) as gemm_expert_sort_workspace_bytes says, 0 up to 4096 pairs. */
 int gemm_expert_sort(int64_t tokens, int32_t top_k, int32_t num_experts, const int32_t *experts, int32_t *offsets,
                      int32_t *order, int32_t *position, void *workspace, int64_t workspace_bytes, void *stream);
 int64_t gemm_expert_sort_workspace_bytes(int64_t tokens, int32_t top_k, int32_t num_experts);
 
 /* sorted[position[t][j]] = X[t], `rows` sorted rows of `cols` 16-bit values.
  * Rows that no pair has are left as they were.  A position outside [0, rows)
- * counts as dropped, here and below. */
+ * counts as dropped, here and below.  Positions that a sort gave differ from
+ * each other; a row that two pairs have gets one's values or the other's. */
 int gemm_expert_gather(int input_type, int64_t tokens, int64_t rows, int32_t top_k, int64_t cols, const void *X,
                        int64_t ldx, const int32_t *position, void *sorted, int64_t lds, void *stream);
 
