@@ -242,6 +242,46 @@ def test_routed_block(size, activation):
         assert rel(value, grads[name]) <= 6 * 2.0 ** -8, name
 
 
+@pytest.mark.parametrize("tokens,top_k,D", [(0, 2, 16), (3, 1, 0)], ids=["no tokens", "no columns"])
+def test_empty_rows(tokens, top_k, D):
+    experts = torch.zeros(tokens, top_k, dtype=torch.int32, device="cuda")
+    x = torch.zeros(tokens, D, dtype=torch.bfloat16, device="cuda")
+    weights = torch.ones(tokens, top_k, device="cuda")
+    offsets, order, position = dft.expert_sort(experts, 2)
+    assert offsets.tolist() == [0, tokens * top_k, tokens * top_k] and order.numel() == tokens * top_k
+    rows = dft.expert_gather(x, position)
+    assert rows.shape == (tokens * top_k, D)
+    assert torch.equal(dft.expert_combine(rows, position, weights), x)
+    dy, dw = dft.expert_combine_grad(x, rows, position, weights)
+    assert dy.shape == rows.shape and bool((dw == 0).all())
+
+
+def test_routed_block_without_tokens():
+    w1, w2 = (torch.ones(3, *s, dtype=torch.bfloat16, device="cuda") for s in ((16, 24), (24, 16)))
+    b1 = torch.ones(3, 24, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros(0, 16, dtype=torch.bfloat16, device="cuda")
+    weights = torch.zeros(0, 2, device="cuda")
+    out, state = dft.expert_mlp(x, torch.zeros(0, 2, dtype=torch.int32, device="cuda"), weights, w1, w2, b1)
+    grads = dft.expert_mlp_grad(out, state, weights, w1, w2)
+    assert out.shape == x.shape == grads.x.shape
+    for g, shape in ((grads.w1, w1.shape), (grads.b1, b1.shape), (grads.w2, w2.shape), (grads.b2, (3, 16))):
+        assert g.shape == shape and bool((g == 0).all())
+
+
+def test_one_expert_chosen_by_every_choice():
+    """The same expert in each of a token's choices: as many rows of its own."""
+    gen = torch.Generator().manual_seed(97)
+    x = ref.draw(gen, (5, 40), torch.float16)
+    y = ref.draw(gen, (15, 40), torch.float16, True)
+    experts = torch.full((5, 3), 2, dtype=torch.int32, device="cuda")
+    _, order, position = dft.expert_sort(experts, 4)
+    assert torch.equal(position.cpu(), torch.arange(15, dtype=torch.int32).view(5, 3))
+    assert torch.equal(dft.expert_gather(x.cuda(), position).cpu(), x.repeat_interleave(3, 0))
+    weights = torch.tensor([1.0, 2.0, 4.0], device="cuda").repeat(5, 1)
+    want = (y.double().view(5, 3, 40) * weights.cpu().double()[..., None]).sum(1)  # small whole numbers: exact
+    assert torch.equal(dft.expert_combine(y.cuda(), position, weights).cpu().double(), want)
+
+
 def test_routed_block_captured():
     """Forward and backward of the routed block in a graph, replayed with new routes between eager calls."""
     gen = torch.Generator().manual_seed(99)
