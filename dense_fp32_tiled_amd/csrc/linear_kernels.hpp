@@ -1120,28 +1120,4 @@ __global__ __launch_bounds__(256) void linear_tail_kernel(LinearProblem p, uint3
     }
 }
 
-// Copies matrices to rows of whole 16 bytes (zeros past their width): what
-// lets a product of unaligned operands run on direct copies.  Bound by bytes,
-// at small sizes by latency: 6.8 us for 1000x999, 1000x513 and 513x999 at once,
-// which the two products that read them win back: 35 against 64 us.
-struct PackJob {
-    const uint16_t* src;
-    int64_t rows, cols, ld, copies, copy_stride;
-    uint16_t* dst;
-    int64_t ldd;  // a multiple of 8; copies lie rows * ldd apart
-};
-struct PackJobs {
-    PackJob job[3];
-};
-template <int TYPE>  // (one instance, as every kernel of this header is a template)
-__global__ __launch_bounds__(256) void linear_pack_kernel(PackJobs jobs) {
-    const PackJob& j = jobs.job[blockIdx.y];
-    const int64_t groups = j.ldd / 8, total = j.copies * j.rows * groups;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t at = i / groups, col = i % groups * 8, copy = at / j.rows, row = at % j.rows;
-        const Row8 v = load8(j.src + copy * j.copy_stride + row * j.ld + col, j.cols - col);
-        *reinterpret_cast<u32x4*>(j.dst + at * j.ldd + col) = v.w;
-    }
-}
-
 }  // namespace dft

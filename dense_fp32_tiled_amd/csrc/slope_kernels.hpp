@@ -1,10 +1,11 @@
-// slope_kernels.hpp -- gfx950 kernels of the epilogue's gradient.
+// slope_kernels.hpp -- gfx950 kernels of the epilogue's gradient, and the copies
+// of operands of odd widths.
 //
 // dZ = dY act'(Z), rounded to 16 bits for the two products that read it, and
 // the column sums of the unrounded values (dbias): each workgroup sums a
 // chunk of 16 or 64 rows of one group over 256 columns into
-// partial[chunk][column]; linear_bias_join_kernel adds a group's chunks in
-// ascending order.  Bound by bytes: dY and Z read once, dZ written once:
+// partial[chunk][column]; bias_join adds a group's chunks in a fixed order.  A
+// single chunk's sums are dbias itself.  Bound by bytes: dY and Z read once, dZ written once:
 // 8192x8192 with silu 98 us (4.1 TB/s of 403 MB), the join 5 us.
 #pragma once
 
@@ -24,7 +25,7 @@ struct SlopeProblem {
     int64_t ldz;
     uint16_t* dZ;                // nullptr: the sums alone (no activation)
     int64_t lddz;
-    float* partial;              // nullptr: no sums wanted
+    float* partial;              // the sums of chunk c at partial + c * N; nullptr: no sums wanted
     const int32_t* offsets;
     int32_t groups;
     int32_t act;
@@ -83,12 +84,11 @@ __global__ __launch_bounds__(256) void linear_slope_kernel(SlopeProblem p) {
 }
 
 // dbias[group][column] over that group's chunks: 64 columns by 4 strides of
-// chunks per workgroup.
-__global__ __launch_bounds__(256) void linear_bias_join_kernel(SlopeProblem p) {
+// chunks per workgroup, workgroup (across, group) of ceil(N / 64) x groups.
+__device__ inline void bias_join(const SlopeProblem& p, uint32_t across, int group) {
     __shared__ float sums[4][64];
     const int c = threadIdx.x % 64, r = threadIdx.x / 64;
-    const int64_t col = (int64_t)blockIdx.x * 64 + c;
-    const int group = blockIdx.y;
+    const int64_t col = (int64_t)across * 64 + c;
     int64_t first = 0, rows = p.M;
     if (p.offsets) {
         // chunks of the groups before this one, by the same rule as find_group_tile
@@ -110,9 +110,44 @@ __global__ __launch_bounds__(256) void linear_bias_join_kernel(SlopeProblem p) {
 #pragma unroll 8
         for (int64_t k = r; k < chunks; k += 4) sum += p.partial[(first + k) * p.N + col];
     }
+    __syncthreads();  // the sums of the call before have been read
     sums[r][c] = sum;
     __syncthreads();
     if (r == 0 && col < p.N) p.dbias[group * p.N + col] = sums[0][c] + sums[1][c] + sums[2][c] + sums[3][c];
+}
+__global__ __launch_bounds__(256) void linear_bias_join_kernel(SlopeProblem p) {
+    bias_join(p, blockIdx.x, blockIdx.y);
+}
+
+// Copies matrices to rows of whole 16 bytes (zeros past their width): what
+// lets a product of unaligned operands run on direct copies.  Bound by bytes,
+// at small sizes by latency: 6.8 us for 1000x999, 1000x513 and 513x999 at once,
+// which the two products that read them win back (64 us without).
+struct PackJob {
+    const uint16_t* src;
+    int64_t rows, cols, ld, copies, copy_stride;
+    uint16_t* dst;
+    int64_t ldd;  // a multiple of 8; copies lie rows * ldd apart
+};
+struct PackJobs {
+    PackJob job[3];
+};
+// The row of workgroups after the jobs' joins dbias: a launch less (all
+// gradients of 1000x999x513: 33.0 against 35.4 us).
+__global__ __launch_bounds__(256) void linear_pack_kernel(PackJobs jobs, int count, SlopeProblem bias) {
+    if ((int)blockIdx.y >= count) {
+        const uint32_t across = (uint32_t)((bias.N + 63) / 64);
+        for (uint64_t block = blockIdx.x; block < (uint64_t)across * bias.groups; block += gridDim.x)
+            bias_join(bias, (uint32_t)(block % across), (int)(block / across));
+        return;
+    }
+    const PackJob& j = jobs.job[blockIdx.y];
+    const int64_t groups = j.ldd / 8, total = j.copies * j.rows * groups;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t at = i / groups, col = i % groups * 8, copy = at / j.rows, row = at % j.rows;
+        const Row8 v = load8(j.src + copy * j.copy_stride + row * j.ld + col, j.cols - col);
+        *reinterpret_cast<u32x4*>(j.dst + at * j.ldd + col) = v.w;
+    }
 }
 
 }  // namespace dft

@@ -233,6 +233,19 @@ def test_many_rows_per_group_sum_in_slices(libs):
     assert torch.equal(g["bias"][0].double(), dy.double().sum(0))
 
 
+@pytest.mark.parametrize("M", [2, 16, 17, 32, 33, 64, 65])
+@pytest.mark.parametrize("N", [8, 300])
+def test_bias_of_few_rows(M, N, libs):
+    """dbias of one chunk of rows and of a few, with and without an activation: whole numbers, exact."""
+    gen = torch.Generator().manual_seed(77 + M)
+    a, b, dy = (ref.draw(gen, s, torch.bfloat16, True) for s in ((M, 16), (1, 16, N), (M, N)))
+    z = ref.draw(gen, (M, N), torch.bfloat16, True)
+    for which in ("plain", "poison"):
+        for act in ("none", "relu"):
+            g = ref.run_grad(libs[which], dy, a, b, preact=z, kind=act, want=("bias",))
+            assert torch.equal(g["bias"][0].double(), (dy.double() * ref.slope(z.double(), act)).sum(0)), (which, act)
+
+
 def test_last_round_in_slices(libs):
     """More 256x256 tiles than CUs and a deep contraction: the tiles of the last round are cut along it and joined.
     Integer values, against float64 on the GPU (exact): forward, dA and dB, dense and grouped."""
@@ -273,6 +286,24 @@ def test_last_round_in_slices(libs):
     dy2 = ints(2112, 4096)
     g = dft.linear_grad(dy2, x, ints(M, 4096), want=("b",), b_dtype=torch.float32)
     assert torch.equal(g.b.double(), x.double().t() @ dy2.double())
+
+
+def test_slices_when_groups_fill_less_than_a_round(libs):
+    """Rows counted for more 256x256 tiles than CUs, but in few groups (or none): every tile there is gets cut."""
+    torch.manual_seed(76)
+    M, N, K, groups = 600, 1024, 2112, 80
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    assert (M + groups * 255) // 256 * (N // 256) > cus
+    a = torch.randint(-3, 4, (M, K), device="cuda").to(torch.bfloat16)
+    b = torch.randint(-3, 4, (groups, K, N), device="cuda").to(torch.bfloat16)
+    for first, second in ((300, 290), (1, 0), (0, 0), (0, 600)):
+        offsets = torch.full((groups + 1,), first, dtype=torch.int32, device="cuda")
+        offsets[0], offsets[groups] = 0, first + second
+        out = torch.full((M, N), 5.0, device="cuda")
+        dft.grouped_linear(a, b, offsets, out=out, variant=dft.LINEAR_256x256)
+        for g, lo, hi in ((0, 0, first), (groups - 1, first, first + second)):
+            assert torch.equal(out[lo:hi].double(), a[lo:hi].double() @ b[g].double())
+        assert bool((out[first + second:] == 5).all())
 
 
 @pytest.mark.parametrize("grouped", [False, True], ids=["one", "grouped"])
