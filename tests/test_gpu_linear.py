@@ -7,6 +7,7 @@ is NaN outside the matrices.  The bounds are derived in linear_reference."""
 from __future__ import annotations
 
 import math
+import threading
 
 import pytest
 import torch
@@ -577,3 +578,66 @@ def test_streams_and_graphs(libs):
         assert torch.equal(y, eager)
         assert all(torch.equal(p, q) for p, q in zip(g, grads))
         del other
+
+
+def test_packed_and_sliced_calls_captured(libs):
+    """Odd widths (packed) and a last round in slices in one graph, replayed with other inputs between eager calls."""
+    torch.manual_seed(78)
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    M, N, K = 256 * (cus // 16) + 100, 4096, 2113
+    x, w, dy = (torch.randn(*s, device="cuda").to(torch.bfloat16) for s in ((M, K), (K, N), (M, N)))
+
+    def step():
+        z = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+        y = dft.linear(x, w, activation="gelu", preact=z, variant=dft.LINEAR_256x256, splits=1)
+        return [y, z, *dft.linear_grad(dy, x, w, preact=z, activation="gelu")]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for k in range(3):
+        x.normal_()
+        eager = step()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(captured, eager):
+            assert torch.equal(a, b), k
+        del eager
+
+
+def test_calls_from_several_threads(libs):
+    """Each thread on a stream of its own: forward with slices, gradients with every output."""
+    gen = torch.Generator().manual_seed(86)
+    x, w = ref.draw(gen, (16, 2048), torch.bfloat16).cuda(), ref.draw(gen, (2048, 640), torch.bfloat16, scale=0.02).cuda()
+    dy = ref.draw(gen, (16, 640), torch.bfloat16).cuda()
+    want = [dft.linear(x, w, splits=4), *dft.linear_grad(dy, x, w)[:3]]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        for _ in range(20):
+            got = [dft.linear(x, w, splits=4, stream=stream), *dft.linear_grad(dy, x, w, stream=stream)[:3]]
+            stream.synchronize()
+            wrong.extend(k for k, (a, b) in enumerate(zip(got, want)) if not torch.equal(a, b))
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_gradient_of_the_pre_activation_alone(libs):
+    gen = torch.Generator().manual_seed(87)
+    x, w, dy, z = (ref.draw(gen, s, torch.bfloat16) for s in ((40, 24), (24, 56), (40, 56), (40, 56)))
+    g = dft.linear_grad(dy.cuda(), x.cuda(), w.cuda(), preact=z.cuda(), activation="silu", want=())
+    assert g.a is None and g.b is None and g.bias is None
+    exact = dy.double() * ref.slope(z.double(), "silu")
+    # the slope is off by at most 16 u (1 + |z|), the product by u of itself, then one rounding
+    off = 20 * ref.U * (1 + z.double().abs()) * dy.double().abs()
+    assert bool(((g.preact.cpu().double() - exact).abs() <= off + ref.half_step(exact.abs() + off, torch.bfloat16)).all())
