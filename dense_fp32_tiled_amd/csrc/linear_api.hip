@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 #include <stdint.h>
 #include <string.h>
@@ -112,30 +113,37 @@ struct Plan {
     double us;  // as estimated
 };
 
-// Times of the tiles in microseconds, fitted to bf16 products of 1 to 4096
-// rows by 1024 to 16384 columns and 1024 to 8192 deep (forward): a round of
-// workgroups takes `fixed` and, per contraction tile, `alone` with one
-// workgroup per CU and `full` with every place taken.
+// Times of the tiles in microseconds, fitted to 10000 forward products of
+// every tile and slicing, of 1 to 16384 rows by 64 to 8192 columns and 64 to
+// 8192 deep, one matrix or up to 32 groups: `once` for the launch, and for a
+// round of workgroups `fixed` and, per contraction tile, `alone` with one
+// workgroup per CU and `full` with every place taken.  Over those products the
+// choice takes 1.4 % more than the best on average (a fit to products of 1024
+// columns and depth and more took 6.4 %, most of it on short contractions).
 struct TileTime {
     int per_cu;
-    double fixed, alone, full;
+    double once, fixed, alone, full;
 };
-constexpr TileTime kDirectTimes[kTileCount] = {{1, 12, 1.0, 1.42}, {2, 1.8, 0.62, 0.94}, {2, 3, 0.2, 0.40}, {2, 3, 0.2, 0.44}};
-constexpr TileTime kRegisterTimes[kTileCount] = {{1, 0, 0, 0}, {2, 3, 2.5, 3.2}, {2, 3, 1.5, 2.0}, {2, 3, 1.5, 2.0}};
+constexpr TileTime kDirectTimes[kTileCount] = {
+    {1, 3.3, 15.3, 0.98, 1.57}, {2, 4.3, 6.7, 0.69, 1.21}, {2, 4.3, 3.1, 0.24, 0.54}, {2, 4.3, 3.3, 0.24, 0.56}};
+constexpr TileTime kRegisterTimes[kTileCount] = {
+    {1, 0, 0, 0, 0}, {2, 4.3, 3.3, 2.75, 3.5}, {2, 4.3, 3.3, 1.65, 2.2}, {2, 4.3, 3.3, 1.65, 2.2}};
 constexpr int kMaxSlices = 32;
 
 // Estimated microseconds of a plan: its launch, its rounds (the last one by
-// how much of the chip it takes), no less than its operands' bytes at 5 TB/s,
-// and the slices' join.
+// how much of the chip it takes) and its operands' bytes at 4.2 TB/s, the
+// larger of the two counting most (fourth powers), and the slices' join.
 double estimate(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, LinearTile t, bool direct, int splits,
                 int cus) {
     const TileTime time = (direct ? kDirectTimes : kRegisterTimes)[t];
     if (time.alone <= 0) return 1e30;
     const TileSize size = kTileSizes[t];
     double row_tiles = (double)ceil_div(R, size.bm), length = (double)L, copies = 1;
-    if (axis == kGroupRows) {  // on average half a tile more for every group that has rows
+    if (axis == kGroupRows) {
+        // half a tile more on average for every group that has rows, and two standard deviations of their sum: a
+        // round begun costs more than one left out saves
         copies = (double)std::min<int64_t>(groups, R);
-        row_tiles = (double)R / size.bm + 0.5 * copies;
+        row_tiles = std::max((double)R / size.bm + 0.5 * copies + 0.6 * std::sqrt(copies), copies);
     }
     double tiles = row_tiles * (double)ceil_div(C, size.bn) * splits;
     if (axis == kGroupContraction) {
@@ -145,8 +153,7 @@ double estimate(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, Linea
     const double slots = (double)cus * time.per_cu;
     const double depth = (double)ceil_div((int64_t)(length / splits + 0.999), kTileDepth);
     const double whole = (double)(int64_t)(tiles / slots), left = tiles / slots - whole;  // rounds
-    // (128x128 tiles: the epilogues of a round that another follows)
-    double us = whole * (time.fixed + (t == kTile128 ? 4 : 0) + depth * time.full);
+    double us = whole * (time.fixed + depth * time.full);
     if (left > 0) {
         // from `alone` while there is at most one workgroup per CU (one-per-CU tiles: by the share of CUs) to `full`
         const double busy = time.per_cu == 1 ? left : std::max(0.0, left * time.per_cu - 1) / (time.per_cu - 1);
@@ -157,8 +164,9 @@ double estimate(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, Linea
     }
     const double bytes = 2.0 * ((double)R * (double)L + copies * (double)L * (double)C) +
                          2.0 * (double)R * (double)C * (axis == kGroupContraction ? (double)groups : 1.0);
-    us = std::max(us, bytes / 5e6) + 0.1 * us + 2.5;  // (of two plans that wait for memory, the one that computes less)
-    if (splits > 1) us += 3.5 + (splits + 1.0) * (double)R * (double)C * 4.0 / 4e6;
+    const double memory = bytes / 4.2e6, u2 = us * us, m2 = memory * memory;
+    us = time.once + std::sqrt(std::sqrt(u2 * u2 + m2 * m2));
+    if (splits > 1) us += 2.1 + (splits + 1.0) * (double)R * (double)C * 4.0 / 4.4e6;
     return us;
 }
 
@@ -298,7 +306,8 @@ int launch_pack(const Matrix* from, Matrix* to, int n, Space* space, const Slope
         most = std::max(most, from[i].copies * from[i].rows * (to[i].ld / 8));
     }
     void* args[] = {&jobs, &n, &join};
-    const unsigned blocks = (unsigned)std::min<int64_t>(ceil_div(most, 256), 65536);
+    const int64_t joins = bias ? ceil_div(join.N, 64) * join.groups : 0;
+    const unsigned blocks = (unsigned)std::min<int64_t>(std::max(ceil_div(most, 256), joins), 65536);
     return hipLaunchKernel(reinterpret_cast<const void*>(linear_pack_kernel), dim3(blocks, (unsigned)n + (bias ? 1 : 0)),
                            dim3(256), args, 0, stream) == hipSuccess
                ? GEMM_OK

@@ -776,7 +776,7 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
     auto find_work = [&](uint32_t& id, LinearWork& w) {
         if constexpr (PERSISTENT) {
             const LinearProblem p = problem_again();
-            if (p.tail) {
+            if (p.tail || p.axis == kGroupRows) {
                 const uint32_t real_m = p.axis == kGroupRows
                                             ? (uint32_t)count_group_tiles(p.offsets, p.groups, p.R, BM)
                                             : tiles_m;  // (the tiles there are, so that the last ones are the last round)
