@@ -120,6 +120,8 @@ struct Plan {
 // workgroup per CU and `full` with every place taken.  Over those products the
 // choice takes 1.4 % more than the best on average (a fit to products of 1024
 // columns and depth and more took 6.4 %, most of it on short contractions).
+// The register path's, and packing's time, were fitted to 7000 products of odd
+// widths run both ways: 2.4 % more than the best on average (11 % before).
 struct TileTime {
     int per_cu;
     double once, fixed, alone, full;
@@ -127,16 +129,26 @@ struct TileTime {
 constexpr TileTime kDirectTimes[kTileCount] = {
     {1, 3.3, 15.3, 0.98, 1.57}, {2, 4.3, 6.7, 0.69, 1.21}, {2, 4.3, 3.1, 0.24, 0.54}, {2, 4.3, 3.3, 0.24, 0.56}};
 constexpr TileTime kRegisterTimes[kTileCount] = {
-    {1, 0, 0, 0, 0}, {2, 4.3, 3.3, 2.75, 3.5}, {2, 4.3, 3.3, 1.65, 2.2}, {2, 4.3, 3.3, 1.65, 2.2}};
+    {1, 0, 0, 0, 0}, {2, 11.6, 0, 2.2, 3.0}, {2, 5.3, 1.5, 1.13, 0.77}, {2, 5.7, 1.2, 1.45, 0.99}};
+
+// How a product reads its operands, and the register path's time per
+// contraction tile by which of the two are of odd widths.
+struct Path {
+    bool direct;
+    double slow;
+};
 constexpr int kMaxSlices = 32;
 
 // Estimated microseconds of a plan: its launch, its rounds (the last one by
-// how much of the chip it takes) and its operands' bytes at 4.2 TB/s, the
-// larger of the two counting most (fourth powers), and the slices' join.
-double estimate(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, LinearTile t, bool direct, int splits,
+// how much of the chip it takes) and its operands' bytes at 4.2 TB/s (2.2
+// through registers), the larger of the two counting most (fourth powers), and
+// the slices' join.
+double estimate(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, LinearTile t, Path path, int splits,
                 int cus) {
-    const TileTime time = (direct ? kDirectTimes : kRegisterTimes)[t];
+    TileTime time = (path.direct ? kDirectTimes : kRegisterTimes)[t];
     if (time.alone <= 0) return 1e30;
+    time.alone *= path.slow;
+    time.full *= path.slow;
     const TileSize size = kTileSizes[t];
     double row_tiles = (double)ceil_div(R, size.bm), length = (double)L, copies = 1;
     if (axis == kGroupRows) {
@@ -158,24 +170,24 @@ double estimate(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, Linea
         // from `alone` while there is at most one workgroup per CU (one-per-CU tiles: by the share of CUs) to `full`
         const double busy = time.per_cu == 1 ? left : std::max(0.0, left * time.per_cu - 1) / (time.per_cu - 1);
         const double last = time.fixed + depth * (time.alone + busy * (time.full - time.alone));
-        const bool tail = t == kTile256 && direct && axis != kGroupContraction && splits == 1 && whole > 0 &&
+        const bool tail = t == kTile256 && path.direct && axis != kGroupContraction && splits == 1 && whole > 0 &&
                           depth >= kTailDepth && left <= 0.5;
         us += tail ? std::min(last, time.fixed + depth * time.full * left + 30) : last;
     }
     const double bytes = 2.0 * ((double)R * (double)L + copies * (double)L * (double)C) +
                          2.0 * (double)R * (double)C * (axis == kGroupContraction ? (double)groups : 1.0);
-    const double memory = bytes / 4.2e6, u2 = us * us, m2 = memory * memory;
+    const double memory = bytes / (path.direct ? 4.2e6 : 2.2e6), u2 = us * us, m2 = memory * memory;
     us = time.once + std::sqrt(std::sqrt(u2 * u2 + m2 * m2));
     if (splits > 1) us += 2.1 + (splits + 1.0) * (double)R * (double)C * 4.0 / 4.4e6;
     return us;
 }
 
-Plan choose(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, bool direct, int variant, int splits, int cus) {
-    Plan best{kTile128, direct, 1, L, 1e300};
+Plan choose(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, Path path, int variant, int splits, int cus) {
+    Plan best{kTile128, path.direct, 1, L, 1e300};
     for (int t = 0; t < kTileCount; ++t) {
         if (variant != GEMM_LINEAR_AUTO && t != variant - 1) continue;
         LinearTile tile = (LinearTile)t;
-        if (tile == kTile256 && !direct) {
+        if (tile == kTile256 && !path.direct) {
             if (variant == GEMM_LINEAR_AUTO) continue;
             tile = kTile128;
         }
@@ -188,10 +200,10 @@ Plan choose(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, bool dire
                 if (splits == 0 && slice < 4 * kTileDepth) break;
                 use = (int)ceil_div(L, slice);
             }
-            double us = estimate(R, C, L, groups, axis, tile, direct, use, cus);
+            double us = estimate(R, C, L, groups, axis, tile, path, use, cus);
             // at equal times the tile whose rows are used, and fewer slices
             if (tile == kTile32x128 && R > 32 * groups) us += 0.3;
-            if (us < best.us - 0.2) best = Plan{tile, direct, std::max(use, 1), slice, us};
+            if (us < best.us - 0.2) best = Plan{tile, path.direct, std::max(use, 1), slice, us};
             if (splits > 0 || axis != kGroupNone || L == 0) break;
         }
     }
@@ -279,8 +291,16 @@ Matrix packed(const Matrix& m) {
     return r;
 }
 int64_t packed_bytes(const Matrix& m) { return ceil_div(2 * m.copies * m.rows * packed(m).ld, 256) * 256; }
-// Reading and writing every element once at 4 TB/s, beside the launch.
-double pack_us(const Matrix& m) { return 2.0 * (double)packed_bytes(m) / 4e6; }
+// Reading and writing every element once at 5.3 TB/s, beside the launch.
+constexpr double kPackLaunch = 3.5;
+double pack_us(const Matrix& m) { return 2.0 * (double)packed_bytes(m) / 5.3e6; }
+
+constexpr Path kDirect{true, 1};
+Path path_of(const Matrix& a, bool a_kmajor, const Matrix& b, bool b_kmajor) {
+    if (direct_ok(a, a_kmajor, b, b_kmajor)) return kDirect;
+    const bool whole_a = whole_rows(a), whole_b = whole_rows(b);
+    return Path{false, whole_a == whole_b ? 1.0 : whole_b ? 0.55 : 0.94};
+}
 
 // Workspace cut into 256-byte pieces from its start.
 struct Space {
@@ -358,14 +378,14 @@ struct LinearPlan {
     bool tail;          // slices of the last round
 };
 LinearPlan plan_linear(const gemm_linear_args& a, const LinearCall& c, int cus) {
-    LinearPlan best{choose(a.M, a.N, a.K, c.groups, c.axis, direct_ok(c.A, true, c.B, false), a.variant, a.splits, cus),
+    LinearPlan best{choose(a.M, a.N, a.K, c.groups, c.axis, path_of(c.A, true, c.B, false), a.variant, a.splits, cus),
                     false, false, 0, false};
     if (!best.plan.direct && a.K > 0) {
         const bool pack_a = !whole_rows(c.A), pack_b = !whole_rows(c.B);
         const Matrix A = pack_a ? packed(c.A) : c.A, B = pack_b ? packed(c.B) : c.B;
         if (copies_fit(kTile256, A, true, B, false)) {
-            const Plan p = choose(a.M, a.N, a.K, c.groups, c.axis, true, a.variant, a.splits, cus);
-            const double us = p.us + 2.5 + (pack_a ? pack_us(c.A) : 0) + (pack_b ? pack_us(c.B) : 0);
+            const Plan p = choose(a.M, a.N, a.K, c.groups, c.axis, kDirect, a.variant, a.splits, cus);
+            const double us = p.us + kPackLaunch + (pack_a ? pack_us(c.A) : 0) + (pack_b ? pack_us(c.B) : 0);
             if (us < best.plan.us) best = LinearPlan{p, pack_a, pack_b, 0, false};
         }
     }
@@ -456,11 +476,11 @@ int describe(const gemm_linear_grad_args& a, GradCall* c) {
     return out_pitch_ok(c->dA) && out_pitch_ok(c->dB) ? GEMM_OK : GEMM_ERR_TOO_LARGE;
 }
 
-Plan plan_a(const gemm_linear_grad_args& a, const GradCall& c, bool direct, int cus) {
-    return choose(a.M, a.K, a.N, c.groups, c.axis, direct, GEMM_LINEAR_AUTO, 0, cus);
+Plan plan_a(const gemm_linear_grad_args& a, const GradCall& c, Path path, int cus) {
+    return choose(a.M, a.K, a.N, c.groups, c.axis, path, GEMM_LINEAR_AUTO, 0, cus);
 }
-Plan plan_b(const gemm_linear_grad_args& a, const GradCall& c, bool direct, int cus) {
-    return choose(a.K, a.N, a.M, c.groups, c.axis == kGroupRows ? kGroupContraction : kGroupNone, direct,
+Plan plan_b(const gemm_linear_grad_args& a, const GradCall& c, Path path, int cus) {
+    return choose(a.K, a.N, a.M, c.groups, c.axis == kGroupRows ? kGroupContraction : kGroupNone, path,
                   GEMM_LINEAR_AUTO, 0, cus);
 }
 // Few rows of one matrix: one chunk, whose sums need no join (4096 columns: 1
@@ -487,16 +507,16 @@ struct GradPlan {
 GradPlan plan_grad(const gemm_linear_grad_args& a, const GradCall& c, int cus) {
     const Matrix dz = c.slope();
     const bool want_a = a.dA && a.M > 0 && a.K > 0, want_b = a.dB && a.K > 0 && a.N > 0;
-    GradPlan best{plan_a(a, c, direct_ok(dz, true, c.B, true), cus), plan_b(a, c, direct_ok(c.A, false, dz, false), cus),
+    GradPlan best{plan_a(a, c, path_of(dz, true, c.B, true), cus), plan_b(a, c, path_of(c.A, false, dz, false), cus),
                   false, false, false, 0, false, false};
     const bool slow = (want_a && !best.a.direct) || (want_b && !best.b.direct);
     if (slow && a.M > 0 && a.N > 0) {
         const bool z = !whole_rows(dz), pa = want_b && !whole_rows(c.A), pb = want_a && !whole_rows(c.B);
         const Matrix Z = z ? packed(dz) : dz, A = pa ? packed(c.A) : c.A, B = pb ? packed(c.B) : c.B;
         if ((!want_a || copies_fit(kTile256, Z, true, B, true)) && (!want_b || copies_fit(kTile256, A, false, Z, false))) {
-            const Plan p = plan_a(a, c, true, cus), q = plan_b(a, c, true, cus);
+            const Plan p = plan_a(a, c, kDirect, cus), q = plan_b(a, c, kDirect, cus);
             const double before = (want_a ? best.a.us : 0) + (want_b ? best.b.us : 0);
-            const double after = (want_a ? p.us : 0) + (want_b ? q.us : 0) + 2.5 + (z ? pack_us(dz) : 0) +
+            const double after = (want_a ? p.us : 0) + (want_b ? q.us : 0) + kPackLaunch + (z ? pack_us(dz) : 0) +
                                  (pa ? pack_us(c.A) : 0) + (pb ? pack_us(c.B) : 0);
             if (after < before) best = GradPlan{p, q, z, pa, pb, 0, false, false};
         }
