@@ -613,6 +613,14 @@ __device__ inline int64_t count_group_tiles(const int32_t* offsets, int groups, 
     return all;
 }
 
+// Row tiles there are of the tiles_m that any division of the rows into groups
+// has at most (groups that overlap would have more: those are left out).
+__device__ inline uint32_t real_row_tiles(const LinearProblem& p, int tile_rows, uint32_t tiles_m) {
+    if (p.axis != kGroupRows) return tiles_m;
+    const int64_t tiles = count_group_tiles(p.offsets, p.groups, p.R, tile_rows);
+    return tiles < (int64_t)tiles_m ? (uint32_t)tiles : tiles_m;
+}
+
 // The last round of a persistent grid: `left` tiles for `grid` workgroups.
 // Cut along the contraction into `parts` slices each, their partial products
 // go to p.tail, one BM x BN block of fp32 per workgroup, and are joined by
@@ -777,9 +785,8 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
         if constexpr (PERSISTENT) {
             const LinearProblem p = problem_again();
             if (p.tail || p.axis == kGroupRows) {
-                const uint32_t real_m = p.axis == kGroupRows
-                                            ? (uint32_t)count_group_tiles(p.offsets, p.groups, p.R, BM)
-                                            : tiles_m;  // (the tiles there are, so that the last ones are the last round)
+                // (the tiles there are, so that the last ones are the last round)
+                const uint32_t real_m = real_row_tiles(p, BM, tiles_m);
                 const TailSplit t = tail_split(p, real_m * tiles_n, gridDim.x);
                 auto tile_of = [&](uint32_t tile) {
                     return linear_work<AK, BK_, BM, BN>(p, tile, real_m, tiles_n, 0);
@@ -1093,8 +1100,7 @@ __global__ __launch_bounds__(kJoinThreads) void linear_join_kernel(LinearProblem
 template <int TYPE, int BM, int BN>
 __global__ __launch_bounds__(256) void linear_tail_kernel(LinearProblem p, uint32_t tiles_m, uint32_t tiles_n,
                                                           uint32_t grid) {
-    const uint32_t real_m =
-        p.axis == kGroupRows ? (uint32_t)count_group_tiles(p.offsets, p.groups, p.R, BM) : tiles_m;
+    const uint32_t real_m = real_row_tiles(p, BM, tiles_m);
     const TailSplit t = tail_split(p, real_m * tiles_n, grid);
     if (blockIdx.x >= t.left) return;
     const LinearWork w = linear_work<true, false, BM, BN>(p, t.whole + blockIdx.x, real_m, tiles_n, 0);

@@ -546,6 +546,20 @@ def test_descending_offsets_stay_inside(libs):
     assert bool(space[need // 4:].isnan().all())
 
 
+@pytest.mark.parametrize("tile", TILES, ids=TILE_IDS)
+def test_overlapping_groups_do_no_more_work(tile, libs):
+    """Offsets that go back and forth over all rows, 2000 times: no more tiles than a division of the rows needs."""
+    M, K, groups = 4096, 2112, 2000
+    a, b = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda"), torch.zeros(groups, K, 8, dtype=torch.bfloat16, device="cuda")
+    offsets = torch.zeros(groups + 1, dtype=torch.int32, device="cuda")
+    offsets[1::2] = M
+    wide = torch.full((M + 2, 8), 3.0, device="cuda")
+    dft.grouped_linear(a, b, offsets, out=wide[1:M + 1], variant=tile)
+    torch.cuda.synchronize()
+    assert bool((wide[0] == 3).all()) and bool((wide[M + 1] == 3).all())
+    assert bool(((wide == 0) | (wide == 3)).all())
+
+
 def test_streams_and_graphs(libs):
     """Two calls at once on two streams, and a captured call replayed between eager ones."""
     gen = torch.Generator().manual_seed(82)
