@@ -466,9 +466,10 @@ int describe(const gemm_linear_grad_args& a, GradCall* c) {
     const Matrix offsets{a.groups > 0 ? a.offsets : nullptr, 1, a.groups + 1, a.groups + 1, 4};
     if (a.workspace_bytes < 0) return GEMM_ERR_WORKSPACE;
     const Matrix space{a.workspace, 1, a.workspace_bytes, std::max<int64_t>(a.workspace_bytes, 1), 1};
-    const bool in_place = c->dZ.data && c->dZ.same_place(c->dY);  // dZ may overwrite dY
-    const Use uses[] = {{c->dY, false, false}, {c->Z, !act, false},
-                        {in_place ? Matrix{nullptr, 0, 0, 1, 2} : c->dZ, !act || in_place, true},
+    // dZ may overwrite dY, which is then checked as dZ alone: a written matrix
+    const bool in_place = c->dZ.data && c->dZ.same_place(c->dY);
+    const Use uses[] = {{in_place ? Matrix{nullptr, 0, 0, 1, 2} : c->dY, in_place, false}, {c->Z, !act, false},
+                        {c->dZ, !act, true},
                         {c->A, !a.dB, false}, {c->B, !a.dA, false}, {c->dA, true, true}, {c->dB, true, true},
                         {c->dbias, true, true}, {offsets, a.groups == 0, false}, {space, true, true}};
     const int st = check_matrices(uses, 10);

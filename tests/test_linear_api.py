@@ -249,3 +249,17 @@ def test_structures_match_the_header(gemm_lib):
                 fields.append((part.strip(), kind))
         kinds = {ctypes.c_void_p: "p", ctypes.c_int64: "i64", ctypes.c_int32: "i32"}
         assert fields == [(f, kinds[t]) for f, t in struct._fields_]
+
+
+@pytest.mark.parametrize("kw", [
+    dict(A=D), dict(A=D + 2), dict(B=D), dict(B=D + 2), dict(Z=D), dict(Z=D + 2), dict(dA=D + 4), dict(dbias=D),
+    dict(groups=2, offsets=D, b_stride=48 * 32, db_stride=48 * 32), dict(workspace=D + 16, workspace_bytes=64),
+], ids=lambda kw: "-".join(kw))
+def test_grad_in_place_overlaps_nothing_else(kw, gemm_lib):
+    """dZ over dY is written like any other output: what else the call reads or writes may not lie there."""
+    in_place = grad_args(dZ=D)
+    assert dft.gemm_linear_grad_workspace_bytes(in_place, 256) >= 0
+    args = grad_args(dZ=D, **kw)
+    assert dft.gemm_linear_grad(args) == dft.GEMM_ERR_ALIAS
+    if "workspace" not in kw:
+        assert dft.gemm_linear_grad_workspace_bytes(args, 256) == dft.GEMM_ERR_ALIAS
