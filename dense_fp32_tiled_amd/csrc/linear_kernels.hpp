@@ -14,6 +14,7 @@
 #pragma once
 
 #include "mixed_kernels.hpp"
+#include "row_groups.hpp"
 
 namespace dft {
 
@@ -308,19 +309,7 @@ __device__ inline void epilogue8(const LinearEpilogue& ep, const Row8& bias, con
         store8(reinterpret_cast<uint16_t*>(base.out + lane.out), Row8::narrow<TYPE>(z), left);
 }
 
-// ---- groups of rows -----------------------------------------------------------------
-// Group g's rows [lo, hi): offsets outside [0, rows] or not ascending are
-// taken as the nearest range inside, so that no access leaves the matrices.
-struct RowRange {
-    int64_t lo, hi;
-};
-__device__ inline RowRange group_rows(const int32_t* offsets, int g, int64_t rows) {
-    const int64_t a = offsets[g], b = offsets[g + 1];
-    const int64_t lo = a < 0 ? 0 : a > rows ? rows : a;
-    const int64_t hi = b < lo ? lo : b > rows ? rows : b;
-    return RowRange{lo, hi};
-}
-
+// ---- groups of rows (row_groups.hpp) ------------------------------------------------
 // The tile-th tile of `tile_rows` rows when every group's rows are tiled from
 // the group's own start; group < 0: there is no such tile.  Every wave looks
 // it up itself: 64 groups at a time, one per lane.
@@ -337,8 +326,8 @@ __device__ inline GroupTile find_group_tile(const int32_t* offsets, int groups, 
         const int g = g0 + lane;
         RowRange r{0, 0};
         if (g < groups) r = group_rows(offsets, g, rows);
-        const int own = (int)((r.hi - r.lo + tile_rows - 1) / tile_rows);
-        int upto = own;  // inclusive running sum over the lanes
+        const int own = (int)r.tiles(tile_rows);
+        int upto = own;  // inclusive running sum over the lanes (a launch has fewer than 2^23 row tiles, so no group more)
 #pragma unroll
         for (int d = 1; d < kWave; d *= 2) {
             const int other = __shfl_up(upto, d);
@@ -604,7 +593,7 @@ __device__ inline int64_t count_group_tiles(const int32_t* offsets, int groups, 
         int own = 0;
         if (g < groups) {
             const RowRange r = group_rows(offsets, g, rows);
-            own = (int)((r.hi - r.lo + tile_rows - 1) / tile_rows);
+            own = (int)r.tiles(tile_rows);
         }
 #pragma unroll
         for (int d = kWave / 2; d > 0; d /= 2) own += __shfl_xor(own, d);

@@ -91,14 +91,13 @@ __device__ inline void bias_join(const SlopeProblem& p, uint32_t across, int gro
     const int64_t col = (int64_t)across * 64 + c;
     int64_t first = 0, rows = p.M;
     if (p.offsets) {
-        // chunks of the groups before this one, by the same rule as find_group_tile
-        int64_t before = 0;
-        for (int g = c; g < group; g += 64) {
-            const RowRange range = group_rows(p.offsets, g, p.M);
-            before += (range.hi - range.lo + p.chunk_rows - 1) / p.chunk_rows;
-        }
+        // chunks of the groups before this one, by the same rule as find_group_tile: as many as there are places at
+        // most, so that the lanes' sums stay inside 32 bits and `first` inside partial
+        int64_t own_chunks = 0;
+        for (int g = c; g < group; g += 64) own_chunks += group_rows(p.offsets, g, p.M).tiles(p.chunk_rows);
+        int before = count_at_most(own_chunks, p.chunks);
 #pragma unroll
-        for (int d = 32; d > 0; d /= 2) before += __shfl_xor((int)before, d);
+        for (int d = 32; d > 0; d /= 2) before = count_at_most((int64_t)before + __shfl_xor(before, d), p.chunks);
         first = before;
         const RowRange own = group_rows(p.offsets, group, p.M);
         rows = own.hi - own.lo;
