@@ -105,12 +105,15 @@ bool known_act(int a) { return a >= 0 && a < kActCount; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ---- the choice of tile and slices ----------------------------------------------------
+constexpr double kNoPlan = 1e300;
 struct Plan {
     LinearTile tile;
     bool direct;
     int splits;
     int64_t slice;
     double us;  // as estimated
+
+    bool found() const { return us < kNoPlan; }
 };
 
 // Times of the tiles in microseconds, fitted to 10000 forward products of
@@ -182,8 +185,24 @@ double estimate(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, Linea
     return us;
 }
 
+// Row tiles enough for any division of R rows into groups.
+int64_t row_tiles(int64_t R, int64_t groups, int axis, int64_t bm) {
+    if (axis != kGroupRows) return ceil_div(R, bm);
+    return (R + groups * (bm - 1)) / bm;
+}
+
+// Whether a launch holds the tiles (it has fewer than 2^31 threads, of tiles
+// with 512 each).
+constexpr int64_t kMaxTiles = kMaxGrid / 512;
+bool grid_fits(int64_t R, int64_t C, int64_t groups, int axis, LinearTile tile, int splits) {
+    const TileSize size = kTileSizes[tile];
+    const int64_t tiles_m = row_tiles(R, groups, axis, size.bm), tiles_n = ceil_div(C, size.bn);
+    return tiles_n == 0 || tiles_m <= kMaxTiles / tiles_n / (axis == kGroupContraction ? groups : splits);
+}
+
+// The quickest of the plans that a launch holds; none of them: not found().
 Plan choose(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, Path path, int variant, int splits, int cus) {
-    Plan best{kTile128, path.direct, 1, L, 1e300};
+    Plan best{kTile128, path.direct, 1, L, kNoPlan};
     for (int t = 0; t < kTileCount; ++t) {
         if (variant != GEMM_LINEAR_AUTO && t != variant - 1) continue;
         LinearTile tile = (LinearTile)t;
@@ -200,6 +219,7 @@ Plan choose(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, Path path
                 if (splits == 0 && slice < 4 * kTileDepth) break;
                 use = (int)ceil_div(L, slice);
             }
+            if (!grid_fits(R, C, groups, axis, tile, std::max(use, 1))) break;
             double us = estimate(R, C, L, groups, axis, tile, path, use, cus);
             // at equal times the tile whose rows are used, and fewer slices
             if (tile == kTile32x128 && R > 32 * groups) us += 0.3;
@@ -221,20 +241,6 @@ int64_t tail_bytes(const Plan& plan, int64_t R, int64_t C, int64_t L, int64_t gr
     if (most <= cus) return 0;
     if (axis == kGroupNone && (most % cus == 0 || cus / (most % cus) < 2)) return 0;
     return (int64_t)cus * 256 * 256 * 4;
-}
-
-// Row tiles enough for any division of R rows into groups.
-int64_t row_tiles(int64_t R, int64_t groups, int axis, int64_t bm) {
-    if (axis != kGroupRows) return ceil_div(R, bm);
-    return (R + groups * (bm - 1)) / bm;
-}
-
-int check_grid(const Plan& plan, int64_t R, int64_t C, int64_t groups, int axis) {
-    const TileSize size = kTileSizes[plan.tile];
-    const int64_t tiles_m = row_tiles(R, groups, axis, size.bm), tiles_n = ceil_div(C, size.bn);
-    const int64_t y = axis == kGroupContraction ? groups : plan.splits;
-    if (tiles_n > 0 && tiles_m > kMaxGrid / 512 / tiles_n / y) return GEMM_ERR_TOO_LARGE;
-    return GEMM_OK;
 }
 
 hipError_t launch(int type, const LinearProblem& p, LinearLayout layout, const Plan& plan, int cus,
@@ -377,9 +383,10 @@ struct LinearPlan {
     int64_t workspace;  // bytes
     bool tail;          // slices of the last round
 };
-LinearPlan plan_linear(const gemm_linear_args& a, const LinearCall& c, int cus) {
-    LinearPlan best{choose(a.M, a.N, a.K, c.groups, c.axis, path_of(c.A, true, c.B, false), a.variant, a.splits, cus),
-                    false, false, 0, false};
+int plan_linear(const gemm_linear_args& a, const LinearCall& c, int cus, LinearPlan* plan) {
+    LinearPlan& best = *plan;
+    best = LinearPlan{choose(a.M, a.N, a.K, c.groups, c.axis, path_of(c.A, true, c.B, false), a.variant, a.splits, cus),
+                      false, false, 0, false};
     if (!best.plan.direct && a.K > 0) {
         const bool pack_a = !whole_rows(c.A), pack_b = !whole_rows(c.B);
         const Matrix A = pack_a ? packed(c.A) : c.A, B = pack_b ? packed(c.B) : c.B;
@@ -389,10 +396,11 @@ LinearPlan plan_linear(const gemm_linear_args& a, const LinearCall& c, int cus) 
             if (us < best.plan.us) best = LinearPlan{p, pack_a, pack_b, 0, false};
         }
     }
+    if (!best.plan.found()) return GEMM_ERR_TOO_LARGE;
     best.tail = tail_bytes(best.plan, a.M, a.N, a.K, c.groups, c.axis, cus) > 0;
     best.workspace = (best.pack_a ? packed_bytes(c.A) : 0) + (best.pack_b ? packed_bytes(c.B) : 0) +
                      partial_bytes(best.plan, a.M, a.N) + tail_bytes(best.plan, a.M, a.N, a.K, c.groups, c.axis, cus);
-    return best;
+    return GEMM_OK;
 }
 
 bool workspace_ok(int64_t need, const void* workspace, int64_t bytes) {
@@ -407,10 +415,10 @@ int run_linear(const gemm_linear_args& a, hipStream_t stream) {
     int cus = 0;
     st = current_cus(&cus);
     if (st != GEMM_OK) return st;
-    const LinearPlan chosen = plan_linear(a, c, cus);
-    const Plan& plan = chosen.plan;
-    st = check_grid(plan, a.M, a.N, c.groups, c.axis);
+    LinearPlan chosen;
+    st = plan_linear(a, c, cus, &chosen);
     if (st != GEMM_OK) return st;
+    const Plan& plan = chosen.plan;
     if (!workspace_ok(chosen.workspace, a.workspace, a.workspace_bytes)) return GEMM_ERR_WORKSPACE;
     Space space{static_cast<char*>(a.workspace)};
     Matrix A = c.A, B = c.B, from[2], to[2];
@@ -505,11 +513,15 @@ struct GradPlan {
     int64_t workspace;
     bool tail_a, tail_b;  // slices of the last rounds
 };
-GradPlan plan_grad(const gemm_linear_grad_args& a, const GradCall& c, int cus) {
+int plan_grad(const gemm_linear_grad_args& a, const GradCall& c, int cus, GradPlan* plan) {
+    // the slope kernel's grid: 256 columns by a chunk of rows per workgroup
+    const bool slopes = a.N > 0 && (c.dZ.data || a.dbias);
+    if (slopes && (slope_chunks(a, c) > kMaxGrid / 256 || a.N > (int64_t)0xffff * 256)) return GEMM_ERR_TOO_LARGE;
     const Matrix dz = c.slope();
     const bool want_a = a.dA && a.M > 0 && a.K > 0, want_b = a.dB && a.K > 0 && a.N > 0;
-    GradPlan best{plan_a(a, c, path_of(dz, true, c.B, true), cus), plan_b(a, c, path_of(c.A, false, dz, false), cus),
-                  false, false, false, 0, false, false};
+    GradPlan& best = *plan;
+    best = GradPlan{plan_a(a, c, path_of(dz, true, c.B, true), cus), plan_b(a, c, path_of(c.A, false, dz, false), cus),
+                    false, false, false, 0, false, false};
     const bool slow = (want_a && !best.a.direct) || (want_b && !best.b.direct);
     if (slow && a.M > 0 && a.N > 0) {
         const bool z = !whole_rows(dz), pa = want_b && !whole_rows(c.A), pb = want_a && !whole_rows(c.B);
@@ -522,6 +534,7 @@ GradPlan plan_grad(const gemm_linear_grad_args& a, const GradCall& c, int cus) {
             if (after < before) best = GradPlan{p, q, z, pa, pb, 0, false, false};
         }
     }
+    if ((want_a && !best.a.found()) || (want_b && !best.b.found())) return GEMM_ERR_TOO_LARGE;
     int64_t rest = a.dbias && !one_chunk(a) ? slope_chunks(a, c) * a.N * 4 : 0;
     const int axis_b = c.axis == kGroupRows ? kGroupContraction : kGroupNone;
     const int64_t tail_a = want_a ? tail_bytes(best.a, a.M, a.K, a.N, c.groups, c.axis, cus) : 0;
@@ -532,7 +545,7 @@ GradPlan plan_grad(const gemm_linear_grad_args& a, const GradCall& c, int cus) {
     if (want_b) rest = std::max({rest, partial_bytes(best.b, a.K, a.N), tail_b});
     best.workspace = (best.pack_z ? packed_bytes(dz) : 0) + (best.pack_a ? packed_bytes(c.A) : 0) +
                      (best.pack_b ? packed_bytes(c.B) : 0) + rest;
-    return best;
+    return GEMM_OK;
 }
 
 // dZ and the chunks' sums; what is left to join of them.
@@ -573,13 +586,12 @@ int run_grad(const gemm_linear_grad_args& a, hipStream_t stream) {
     int cus = 0;
     st = current_cus(&cus);
     if (st != GEMM_OK) return st;
-    const GradPlan plan = plan_grad(a, c, cus);
+    GradPlan plan;
+    st = plan_grad(a, c, cus, &plan);
+    if (st != GEMM_OK) return st;
     if (!workspace_ok(plan.workspace, a.workspace, a.workspace_bytes)) return GEMM_ERR_WORKSPACE;
     const Plan &pa = plan.a, &pb = plan.b;
     const int axis_b = c.axis == kGroupRows ? kGroupContraction : kGroupNone;
-    if (a.dA && (st = check_grid(pa, a.M, a.K, c.groups, c.axis)) != GEMM_OK) return st;
-    if (a.dB && (st = check_grid(pb, a.K, a.N, c.groups, axis_b)) != GEMM_OK) return st;
-    if (slope_chunks(a, c) > kMaxGrid / 256 || a.N > (int64_t)0xffff * 64) return GEMM_ERR_TOO_LARGE;
     Space space{static_cast<char*>(a.workspace)};
     // places of what is packed, in front of the rest (its kernel runs after dZ's)
     Matrix from[3], to[3], dz = c.slope(), A = c.A, B = c.B;
@@ -687,20 +699,24 @@ int64_t gemm_linear_workspace_bytes(const gemm_linear_args* args, int32_t num_cu
     a.workspace = nullptr;
     a.workspace_bytes = 0;
     LinearCall c;
-    const int st = describe(a, &c);
-    if (st != GEMM_OK) return st;
-    return a.M == 0 || a.N == 0 ? 0 : plan_linear(a, c, num_cus).workspace;
+    int st = describe(a, &c);
+    if (st != GEMM_OK || a.M == 0 || a.N == 0) return st;
+    LinearPlan plan;
+    st = plan_linear(a, c, num_cus, &plan);
+    return st != GEMM_OK ? st : plan.workspace;
 }
 
 int gemm_linear_choice(const gemm_linear_args* args, int32_t num_cus, int32_t* variant, int32_t* splits) {
     if (!args || !variant || !splits) return GEMM_ERR_NULL;
     if (num_cus < 1) return GEMM_ERR_INVALID_DIM;
     LinearCall c;
-    const int st = describe(*args, &c);
+    int st = describe(*args, &c);
     if (st != GEMM_OK) return st;
-    const Plan plan = plan_linear(*args, c, num_cus).plan;
-    *variant = plan.tile + 1;
-    *splits = plan.splits;
+    LinearPlan plan;
+    st = plan_linear(*args, c, num_cus, &plan);
+    if (st != GEMM_OK) return st;
+    *variant = plan.plan.tile + 1;
+    *splits = plan.plan.splits;
     return GEMM_OK;
 }
 
@@ -715,8 +731,11 @@ int64_t gemm_linear_grad_workspace_bytes(const gemm_linear_grad_args* args, int3
     a.workspace = nullptr;
     a.workspace_bytes = 0;
     GradCall c;
-    const int st = describe(a, &c);
-    return st != GEMM_OK ? st : plan_grad(a, c, num_cus).workspace;
+    int st = describe(a, &c);
+    if (st != GEMM_OK) return st;
+    GradPlan plan;
+    st = plan_grad(a, c, num_cus, &plan);
+    return st != GEMM_OK ? st : plan.workspace;
 }
 
 int64_t gemm_expert_sort_workspace_bytes(int64_t tokens, int32_t top_k, int32_t num_experts) {

@@ -466,7 +466,11 @@ int gemm_mixed_auto_variant(int64_t M, int64_t N, int64_t K, int32_t num_cus);
  *     no other output may overlap any operand (GEMM_ERR_ALIAS).
  *   - K == 0 gives Z = bias; M == 0 gives dB = 0 and dbias = 0; N == 0 gives dA = 0.
  *   - GEMM_ERR_TOO_LARGE: M N, M K or K N above 2^50, grouped M above 2^31 - 1,
- *     and pitches of D, residual, preact, dA and dB above 2^26 elements.
+ *     and pitches of D, residual, preact, dA and dB above 2^26 elements; an
+ *     output of 2^22 workgroup tiles or more with every tile that may take it
+ *     (`variant`, and of dB all groups' together); for gradients with an
+ *     activation or dbias, M + 63 * max(groups, 1) of 2^29 or more, or N above
+ *     65535 * 256.  The workspace queries refuse what the calls refuse.
  *   - The activations' limits hold for large |Z|: no infinite intermediate
  *     makes a NaN of a finite Z. */
 typedef enum {
@@ -581,9 +585,10 @@ int64_t gemm_linear_grad_workspace_bytes(const gemm_linear_grad_args *args, int3
  *     offsets[e]                    first sorted row of expert e; offsets[num_experts]: rows in all
  *     order[s]                      pair (token * top_k + choice) of sorted row s; -1 from offsets[num_experts] on
  *     position[token * top_k + j]   sorted row of that pair; -1 when its expert is outside [0, num_experts) (dropped)
- * num_experts is 1..1024; more than 2^31 - 1 pairs (rows, below) are
- * GEMM_ERR_TOO_LARGE.  All arrays are on the device; workspace (4-byte
- * aligned) as gemm_expert_sort_workspace_bytes says, 0 up to 4096 pairs. */
+ * num_experts is 1..1024.  GEMM_ERR_TOO_LARGE: more than 2^31 - 1 pairs, and
+ * for the row operators below more rows than that or more than 65535 * 512
+ * columns.  All arrays are on the device; workspace (4-byte aligned) as
+ * gemm_expert_sort_workspace_bytes says, 0 up to 4096 pairs. */
 int gemm_expert_sort(int64_t tokens, int32_t top_k, int32_t num_experts, const int32_t *experts, int32_t *offsets,
                      int32_t *order, int32_t *position, void *workspace, int64_t workspace_bytes, void *stream);
 int64_t gemm_expert_sort_workspace_bytes(int64_t tokens, int32_t top_k, int32_t num_experts);

@@ -263,3 +263,48 @@ def test_grad_in_place_overlaps_nothing_else(kw, gemm_lib):
     assert dft.gemm_linear_grad(args) == dft.GEMM_ERR_ALIAS
     if "workspace" not in kw:
         assert dft.gemm_linear_grad_workspace_bytes(args, 256) == dft.GEMM_ERR_ALIAS
+
+
+MOST_TILES = 2 ** 22 - 1  # workgroups of a launch
+SIZES = {dft.LINEAR_256x256: (256, 256), dft.LINEAR_128x128: (128, 128), dft.LINEAR_64x64: (64, 64), dft.LINEAR_32x128: (32, 128)}
+
+
+@pytest.mark.parametrize("M,N,K", [(1 << 28, 8, 8), (300_000_000, 8, 8), (300_000_000, 64, 64), ((1 << 28) + 5, 9, 7),
+                                   (1, 1 << 26, 8), (1 << 29, 30, 1), (1000, 60_000_000, 16)])
+def test_large_sizes_take_a_tile_that_a_launch_holds(M, N, K, gemm_lib):
+    variant, splits = choice(M, N, K)
+    bm, bn = SIZES[variant]
+    assert -(-M // bm) * -(-N // bn) * splits <= MOST_TILES
+    assert dft.gemm_linear_workspace_bytes(linear_args(M, N, K), 256) >= 0
+    assert dft.gemm_linear_grad_workspace_bytes(grad_args(M, N, K, activation=0, Z=None, dZ=None), 256) >= 0
+
+
+def test_sizes_that_no_launch_holds(gemm_lib):
+    """Refused by the queries as by the calls."""
+    for kw in (dict(M=1 << 31, N=1, K=1), dict(M=1 << 28, N=64, K=64, variant=dft.LINEAR_64x64),
+               dict(M=1 << 28, N=64, K=64, variant=dft.LINEAR_64x64, splits=2)):
+        assert dft.gemm_linear_workspace_bytes(linear_args(**kw), 256) == dft.GEMM_ERR_TOO_LARGE
+        assert dft.gemm_linear_choice(linear_args(**kw), 256)[0] == dft.GEMM_ERR_TOO_LARGE
+
+    def grouped(n):  # the weights' gradient: the groups' tiles together
+        return grad_args(M=64, N=n, K=n, groups=65535, offsets=0x123000, b_stride=n * n, db_stride=n * n, A=1 << 60,
+                         B=1 << 61, dB=1 << 62, activation=0, Z=None, dZ=None)
+
+    assert dft.gemm_linear_grad_workspace_bytes(grouped(1792), 256) >= 0  # 49 tiles of 256x256 each
+    assert dft.gemm_linear_grad_workspace_bytes(grouped(2304), 256) == dft.GEMM_ERR_TOO_LARGE
+
+
+def test_gradient_sizes_that_the_slopes_take(gemm_lib):
+    def need(M, N, K=1, **kw):
+        return dft.gemm_linear_grad_workspace_bytes(grad_args(M, N, K, dA=None, B=None, **kw), 256)
+
+    plain = dict(activation=0, Z=None, dZ=None)
+    assert need(2, 5_000_000) >= 0
+    assert need(2, 65535 * 256) >= 0
+    assert need(2, 65535 * 256 + 1) == dft.GEMM_ERR_TOO_LARGE
+    assert need(2, 65535 * 256 + 1, **plain) >= 0
+    assert need(2, 65535 * 256 + 1, dbias=0x123000, **plain) == dft.GEMM_ERR_TOO_LARGE
+    assert need((1 << 29) - 64, 1) >= 0
+    assert need((1 << 29) - 63, 1) == dft.GEMM_ERR_TOO_LARGE
+    assert need((1 << 29) - 63, 1, **plain) >= 0
+    assert need((1 << 29), 0) == 0
