@@ -185,10 +185,11 @@ double estimate(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, Linea
     return us;
 }
 
-// Row tiles enough for any division of R rows into groups.
+// Row tiles enough for any division of R rows into groups, R of which have
+// rows at most.
 int64_t row_tiles(int64_t R, int64_t groups, int axis, int64_t bm) {
     if (axis != kGroupRows) return ceil_div(R, bm);
-    return (R + groups * (bm - 1)) / bm;
+    return (R + std::min(groups, R) * (bm - 1)) / bm;
 }
 
 // Whether a launch holds the tiles (it has fewer than 2^31 threads, of tiles
@@ -237,7 +238,7 @@ int64_t partial_bytes(const Plan& plan, int64_t R, int64_t C) { return plan.spli
 int64_t tail_bytes(const Plan& plan, int64_t R, int64_t C, int64_t L, int64_t groups, int axis, int cus) {
     if (plan.tile != kTile256 || !plan.direct || plan.splits > 1 || axis == kGroupContraction) return 0;
     if (ceil_div(L, kTileDepth) < kTailDepth) return 0;
-    const int64_t across = ceil_div(C, 256), most = (axis == kGroupRows ? (R + groups * 255) / 256 : ceil_div(R, 256)) * across;
+    const int64_t most = row_tiles(R, groups, axis, 256) * ceil_div(C, 256);
     if (most <= cus) return 0;
     if (axis == kGroupNone && (most % cus == 0 || cus / (most % cus) < 2)) return 0;
     return (int64_t)cus * 256 * 256 * 4;

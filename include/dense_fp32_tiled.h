@@ -469,8 +469,9 @@ int gemm_mixed_auto_variant(int64_t M, int64_t N, int64_t K, int32_t num_cus);
  *     and pitches of D, residual, preact, dA and dB above 2^26 elements; an
  *     output of 2^22 workgroup tiles or more with every tile that may take it
  *     (`variant`, and of dB all groups' together); for gradients with an
- *     activation or dbias, M + 63 * max(groups, 1) of 2^29 or more, or N above
- *     65535 * 256.  The workspace queries refuse what the calls refuse.
+ *     activation or dbias, M + 63 * groups (1 for one matrix, and M at most) of
+ *     2^29 or more, or N above 65535 * 256.  The workspace queries refuse what
+ *     the calls refuse.
  *   - The activations' limits hold for large |Z|: no infinite intermediate
  *     makes a NaN of a finite Z. */
 typedef enum {

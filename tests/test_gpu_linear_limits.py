@@ -47,3 +47,27 @@ def test_more_columns_than_a_grid_has_tiles_of_64():
     assert torch.equal(g.bias, dz.float().sum(0))
     assert torch.equal(g.b.cpu(), a.cpu().float().t() @ dz.cpu().float())
     assert torch.equal(g.a.cpu().double(), dz.cpu().double() @ b.cpu().double().t())
+
+
+@pytest.mark.parametrize("rows", [1, 5])
+def test_few_rows_of_as_many_groups_as_there_may_be(rows):
+    gen = torch.Generator(device="cuda").manual_seed(93)
+    groups, N, K = 65535, 8456, 8
+    used = sorted([0, groups - 1, 1, 30000, 64][:rows])
+    offsets = torch.searchsorted(torch.tensor(used), torch.arange(groups + 1)).to(torch.int32).cuda()
+    a, dy, z = whole(gen, rows, K), whole(gen, rows, N), whole(gen, rows, N)
+    b = torch.full((groups, K, N), float("nan"), dtype=torch.bfloat16, device="cuda")  # (groups without rows: not read)
+    b[used] = whole(gen, rows, K, N)
+    d = dft.grouped_linear(a, b, offsets, out_dtype=torch.float32)
+    want = torch.stack([a[r].cpu().double() @ b[used[r]].cpu().double() for r in range(rows)])
+    assert torch.equal(d.cpu().double(), want)
+    g = dft.grouped_linear_grad(dy, a, b, offsets, preact=z, activation="relu", a_dtype=torch.float32)
+    dz = torch.where(z > 0, dy, torch.zeros_like(dy))
+    assert torch.equal(g.preact, dz)
+    want = torch.stack([b[used[r]].cpu().double() @ dz[r].cpu().double() for r in range(rows)])
+    assert torch.equal(g.a.cpu().double(), want)
+    for r in range(rows):
+        assert torch.equal(g.b[used[r]].cpu().float(), torch.outer(a[r], dz[r]).cpu().float())
+        assert torch.equal(g.bias[used[r]], dz[r].float())
+        g.b[used[r]], g.bias[used[r]] = 0, 0
+    assert not bool(g.bias.any()) and all(not bool(part.any()) for part in g.b.split(8192))

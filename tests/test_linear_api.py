@@ -308,3 +308,20 @@ def test_gradient_sizes_that_the_slopes_take(gemm_lib):
     assert need((1 << 29) - 63, 1) == dft.GEMM_ERR_TOO_LARGE
     assert need((1 << 29) - 63, 1, **plain) >= 0
     assert need((1 << 29), 0) == 0
+
+
+def test_few_rows_of_many_groups_need_little(gemm_lib):
+    """Only as many groups have rows as there are rows: what a call takes of the workspace and of a launch goes by
+    those."""
+    def forward(M, groups, N, K, **kw):
+        return linear_args(M, N, K, groups=groups, offsets=0x123000, b_stride=K * N, A=1 << 58, B=1 << 60, D=1 << 59, **kw)
+
+    # one row: one tile row, with a whole round of 256x256 tiles or without
+    assert dft.gemm_linear_workspace_bytes(forward(1, 65535, 8192, 4096, variant=dft.LINEAR_256x256), 256) == 0
+    assert dft.gemm_linear_choice(forward(1, 65535, 65536, 64), 256)[0] == dft.GEMM_OK
+    assert dft.gemm_linear_workspace_bytes(forward(1, 65535, 65536, 64), 256) == 0
+    # the bias's gradient: one chunk of sums a row
+    for M in (1, 5, 300):
+        g = grad_args(M=M, N=8192, K=64, groups=65535, offsets=0x123000, b_stride=64 * 8192, A=1 << 58, B=1 << 60,
+                      dA=None, dB=None, dbias=1 << 59)
+        assert dft.gemm_linear_grad_workspace_bytes(g, 256) == M * 8192 * 4
