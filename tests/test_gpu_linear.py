@@ -655,3 +655,30 @@ def test_gradient_of_the_pre_activation_alone(libs):
     # the slope is off by at most 16 u (1 + |z|), the product by u of itself, then one rounding
     off = 20 * ref.U * (1 + z.double().abs()) * dy.double().abs()
     assert bool(((g.preact.cpu().double() - exact).abs() <= off + ref.half_step(exact.abs() + off, torch.bfloat16)).all())
+
+
+@pytest.mark.parametrize("act", ("none", "gelu", "gelu_tanh", "silu"))
+@pytest.mark.parametrize("counts", [None, [5, 0, 1, 33]], ids=["one", "grouped"])
+def test_bias_gradient_against_differences(counts, act, libs):
+    """Every column of dbias against the central difference of sum(G * D) over that column's bias, in float64.  With
+    step h the difference is off by at most h^2 / 6 times the sum of |G| times the third derivative (below 1 for these
+    activations), and by two roundings of the sums that are subtracted, 2^-52 of their size over 2 h; dbias itself by
+    the bound of linear_reference."""
+    gen = torch.Generator().manual_seed(74)
+    offsets, M, groups = None, 39, 1
+    if counts is not None:
+        offsets, groups = [0], len(counts)
+        for c in counts:
+            offsets.append(offsets[-1] + c)
+    N, K, h = 24, 16, 1e-4
+    a, b = ref.draw(gen, (M, K), torch.bfloat16), ref.draw(gen, (groups, K, N), torch.bfloat16, scale=0.25)
+    dy, z = ref.draw(gen, (M, N), torch.bfloat16), ref.draw(gen, (M, N), torch.bfloat16)
+    got = ref.run_grad(libs["plain"], dy, a, b, offsets, preact=z, kind=act, want=("bias",))["bias"]
+    _, bound = ref.grad(dy, a, b, offsets, preact=z, kind=act)["bias"]
+    G, Z = dy.double(), z.double()
+    for g, lo, hi in ref.ranges(offsets, groups, M):
+        # (each column's bias enters that column's values alone, so all columns are moved at once)
+        up, down = ((G[lo:hi] * ref.act(Z[lo:hi] + s, act)).sum(0) for s in (h, -h))
+        size = (G[lo:hi].abs() * (ref.act(Z[lo:hi], act).abs() + 1)).sum(0)
+        tol = bound[g] + G[lo:hi].abs().sum(0) * h * h / 6 + (hi - lo + 2) * 2.0 ** -52 * size / h
+        assert bool(((got[g].double() - (up - down) / (2 * h)).abs() <= tol).all()), (g, act)
