@@ -273,7 +273,7 @@ hipError_t launch(int type, const LinearProblem& p, LinearLayout layout, const P
 
 // ---- gemm_linear ----------------------------------------------------------------------
 bool copies_fit(LinearTile tile, const Matrix& a, bool a_kmajor, const Matrix& b, bool b_kmajor) {
-    // OperandCopy::fits of the tile's rows: offsets within a tile below 2^30
+    // OperandCopy's offsets: within a tile, k-major within the whole contraction, they stay below 2^30
     const TileSize size = kTileSizes[tile];
     const auto fits = [](int64_t ld, int64_t rows, int64_t cols) { return ld <= 0x3fffffff / (2 * rows) - cols; };
     return fits(a.ld, a_kmajor ? size.bm : kTileDepth, a_kmajor ? kTileDepth : size.bm) &&

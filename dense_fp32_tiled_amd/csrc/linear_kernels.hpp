@@ -316,7 +316,6 @@ __device__ inline void epilogue8(const LinearEpilogue& ep, const Row8& bias, con
 struct GroupTile {
     int group;
     int64_t row0, row_end;
-    int64_t first;  // first tile of that group
 };
 __device__ inline GroupTile find_group_tile(const int32_t* offsets, int groups, int64_t rows, int tile_rows,
                                             int64_t tile) {
@@ -340,11 +339,11 @@ __device__ inline GroupTile find_group_tile(const int32_t* offsets, int groups, 
             // (lane l's values, uniform: the tile's addresses stay in scalar registers)
             const int64_t first = before + __builtin_amdgcn_readlane(upto - own, l);
             const int64_t lo = __builtin_amdgcn_readlane((int)r.lo, l), hi = __builtin_amdgcn_readlane((int)r.hi, l);
-            return GroupTile{g0 + l, lo + (tile - first) * tile_rows, hi, first};
+            return GroupTile{g0 + l, lo + (tile - first) * tile_rows, hi};
         }
         before += __builtin_amdgcn_readlane(upto, kWave - 1);
     }
-    return GroupTile{-1, 0, 0, 0};
+    return GroupTile{-1, 0, 0};
 }
 
 // Orders a wave's own LDS accesses before it and after it: its lanes exchange
@@ -445,10 +444,6 @@ struct OperandCopy {
         const int64_t bytes = size < 0 ? 0 : size > 0x7fffffff ? 0x7fffffff : size;
         buffer = u32x4{first_lane((uint32_t)b), first_lane((uint32_t)(b >> 32) & 0xffffu), first_lane((uint32_t)bytes),
                        0x00020000u};
-    }
-    // Offsets within a tile stay below 2^30, k-major within the whole contraction.
-    __host__ __device__ static constexpr bool fits(int64_t ld) {
-        return ld <= 0x3fffffff / (2 * Tile::rows) - 2 * Tile::cols;
     }
     // Copy i of the tile into `stage` (a tile past the end fills it with zeros).
     struct Issue {
