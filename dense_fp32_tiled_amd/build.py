@@ -123,8 +123,8 @@ def build_all() -> list[Path]:
 
 def device_assembly(source: Path | None = None) -> str:
     """The gfx950 assembly hipcc emits for the library's device code (the
-    same flags as the build), as text: of `source`, or of every library
-    source concatenated."""
+    same flags as the build), as text: of `source`, or of all SOURCES
+    concatenated."""
     if source is None:
         return "\n".join(device_assembly(src) for src in SOURCES)
     generate_layouts()
@@ -144,7 +144,7 @@ def resource_report(source: Path | None = None) -> dict[str, dict[str, int]]:
     """The compiler's per-kernel resource usage for the library's device code
     (hipcc -Rpass-analysis=kernel-resource-usage): {mangled kernel name:
     {"vgpr", "agpr", "scratch" (bytes per lane), "occupancy" (waves per SIMD),
-    "lds" (bytes per workgroup)}}, of `source` or of every library source.
+    "lds" (bytes per workgroup)}}, of `source` or of all SOURCES.
     Compiles device code only, to a temporary object."""
     import re
 

@@ -132,7 +132,7 @@ __global__ __launch_bounds__(kSortThreads) void expert_sort_small_kernel(SortPro
 }
 
 // The same over several workgroups: counts of each, their running sums, places
-// (5 + 6 + 10 us for 65536 pairs of 64 experts; the pairs' bytes would take 1 us).
+// (5 + 6 to 8 + 10 us for 65536 pairs of 64 experts; the pairs' bytes would take 1 us).
 __global__ __launch_bounds__(kSortThreads) void expert_count_kernel(SortProblem p) {
     __shared__ int32_t totals[kMaxExperts];
     const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;

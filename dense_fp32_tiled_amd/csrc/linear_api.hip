@@ -186,7 +186,9 @@ double estimate(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, Linea
 }
 
 // Row tiles enough for any division of R rows into groups, R of which have
-// rows at most.
+// rows at most (places that no tile takes are not only launched: they leave
+// the real tiles to fewer XCDs.  Counted for all groups, 1 row of 32 experts
+// of 4096x4096 took 48.7 us, 8 rows 105; so 19.6 and 44.8).
 int64_t row_tiles(int64_t R, int64_t groups, int axis, int64_t bm) {
     if (axis != kGroupRows) return ceil_div(R, bm);
     return (R + std::min(groups, R) * (bm - 1)) / bm;

@@ -62,7 +62,7 @@ struct LinearProblem {
 // place each) and no library functions.
 
 // 1 / (1 + exp(-u)); exp2 overflows to infinity and the reciprocal to 0, the
-// limit, for u below -128.
+// limit, for u below -88.7.
 __device__ inline float logistic(float u) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.4426950408889634f * u));
 }
@@ -733,7 +733,7 @@ __device__ inline void slice_work(const LinearProblem& p, const TailSplit& t, Li
 // tiles: 9 us a round for storing plain results, 15 with the epilogue's
 // branches, 27 with silu, residual and pre-activation): 8192^3 826 us forward
 // (1.33 PFLOP/s), 836 with the full epilogue, 745 dA (1.48), 795 dB (1.38).
-// Few rows are bound by B's bytes: 24 rows of 4096 by 16384 25.6 us (5.4 TB/s).
+// Few rows are bound by B's bytes: 24 rows of 4096 by 16384 24.5 us (5.5 TB/s).
 template <int TYPE, bool AK, bool BK_, class Shape, bool DIRECT>
 __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_kernel(LinearProblem, uint32_t tiles_m,
                                                                                    uint32_t tiles_n, uint32_t grid_y) {
@@ -758,6 +758,10 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
     const int tid = threadIdx.x, every_lane = tid % kWave;
     const int every_wave = __builtin_amdgcn_readfirstlane(tid / kWave);
 
+    // Grouped rows: tiles_m is the most that their division may need (row_tiles), and places past the real tiles stay
+    // empty.  Counting the real ones first, as the persistent tiles do, spreads them evenly over the XCDs but costs a
+    // wave another scan of the offsets before its first copy: 128 rows of 32 experts of 4096x4096 249 -> 201 us, 2048
+    // rows 347 -> 288, but dA of 512 rows 248 -> 269, and calls of up to 20 us 0.4 to 2 us more.
     const uint32_t tiles = tiles_m * tiles_n, total = tiles * grid_y;
     auto work_of = [&](uint32_t id) {
         return linear_work<AK, BK_, BM, BN>(problem_again(), id % tiles, tiles_m, tiles_n, id / tiles);
