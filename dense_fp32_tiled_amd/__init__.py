@@ -136,6 +136,10 @@ EXPORTS = (
     "gemm_expert_gather",
     "gemm_expert_combine",
     "gemm_expert_combine_grad",
+    "gemm_layer_norm",
+    "gemm_layer_norm_grad",
+    "gemm_layer_norm_grad_workspace_bytes",
+    "gemm_dropout",
 )
 
 
@@ -232,9 +236,10 @@ def library(path: Path | None = None):
     lib.gemm_lds_access_cycles.restype = i32
     lib.gemm_lds_page_pad.argtypes = [i32, i32, i32]
     lib.gemm_lds_page_pad.restype = i32
-    from . import products
+    from . import norms, products
 
     products.declare(lib)
+    norms.declare(lib)
     if path is None:
         _lib = lib
     return lib
@@ -477,3 +482,6 @@ from .products import (  # noqa: E402
     gemm_expert_sort_workspace_bytes, gemm_linear, gemm_linear_choice, gemm_linear_grad,
     gemm_linear_grad_workspace_bytes, gemm_linear_workspace_bytes, grouped_linear, grouped_linear_grad, linear,
     linear_grad)
+from .norms import (  # noqa: E402
+    VALUE_BF16, VALUE_F16, VALUE_F32, LayerNormArgs, LayerNormGradArgs, NormGrads, NormState, dropout, gemm_dropout,
+    gemm_layer_norm, gemm_layer_norm_grad, gemm_layer_norm_grad_workspace_bytes, layer_norm, layer_norm_grad)

@@ -5,7 +5,7 @@
 first runs the host LDS layout search (csrc/layout_gen.cpp ->
 csrc/generated/mfma_layouts.hpp), then produces
 dense_fp32_tiled_amd/libdense_fp32_tiled.so from csrc/gemm_api.hip,
-csrc/gemm_default.hip and csrc/linear_*.hip (one object per source, compiled
+csrc/gemm_default.hip, csrc/linear_*.hip and csrc/norm_api.hip (one object per source, compiled
 at once), the same library built with DFT_LDS_POISON=1
 (libdense_fp32_tiled_poison.so, for the LDS-poison parity tests), and the
 measurement probes liblds_probe.so from csrc/lds_probe.hip.
@@ -32,6 +32,8 @@ SOURCES = [CSRC / "gemm_api.hip", CSRC / "gemm_default.hip"]
 # their direct copies are buffer loads (range-checked), SOURCES' global ones; each list has its own checks of the
 # compiled code.
 LINEAR_SOURCES = [CSRC / "linear_api.hip", CSRC / "linear_bf16.hip", CSRC / "linear_f16.hip"]
+# What stands between the products and after the last one: the layer norm and dropout.
+MORE_SOURCES = [CSRC / "norm_api.hip"]
 PROBE_LIB = PKG / "liblds_probe.so"
 PROBE_SOURCES = [CSRC / "lds_probe.hip"]
 ARCH = "gfx950"
@@ -79,7 +81,7 @@ def _start(out: Path, extra: list[str] | None, sources: list[Path] | None):
     """Starts one compiler per source; _finish links what they make."""
     work = tempfile.TemporaryDirectory()
     jobs = []
-    for src in sources or [*SOURCES, *LINEAR_SOURCES]:
+    for src in sources or [*SOURCES, *LINEAR_SOURCES, *MORE_SOURCES]:
         obj = Path(work.name) / f"{src.stem}.o"
         cmd = [hipcc(), *HIPCC_FLAGS, *(extra or []), f"-I{ROOT / 'include'}", f"-I{CSRC}", "-c", str(src), "-o",
                str(obj)]

@@ -1,250 +1,22 @@
 // linear_api.hip -- the C ABI of the products with an epilogue, their
-// gradients and the token sort (include/dense_fp32_tiled.h): argument checks,
-// the choice of tile and slices, and the launches.
+// gradients and the token sort (include/dense_fp32_tiled.h): what each call
+// takes, and the launches.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <cmath>
-#include <mutex>
 #include <stdint.h>
-#include <string.h>
 
 #include "dense_fp32_tiled.h"
 #include "expert_kernels.hpp"
-#include "linear_shapes.hpp"
+#include "host_checks.hpp"
+#include "linear_plan.hpp"
 #include "slope_kernels.hpp"
 
 namespace {
 
 using namespace dft;
 
-// ---- the device ---------------------------------------------------------------------
-constexpr int kMaxDevices = 64;
-int g_cus[kMaxDevices];  // 0 unknown, -1 not gfx950, else compute units
-std::mutex g_cus_mu;
-
-int current_cus(int* cus) {
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess) return GEMM_ERR_HIP;
-    if (dev < 0 || dev >= kMaxDevices) return GEMM_ERR_UNSUPPORTED;
-    std::lock_guard<std::mutex> lock(g_cus_mu);
-    if (g_cus[dev] == 0) {
-        hipDeviceProp_t prop;
-        if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return GEMM_ERR_HIP;
-        g_cus[dev] = strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? prop.multiProcessorCount : -1;
-    }
-    if (g_cus[dev] < 0) return GEMM_ERR_UNSUPPORTED;
-    *cus = g_cus[dev];
-    return GEMM_OK;
-}
-
-// ---- argument checks ----------------------------------------------------------------
-constexpr int64_t kMaxDim = (int64_t)1 << 40;  // products of a size, a pitch and an element's bytes stay inside int64
-constexpr int64_t kMaxElements = (int64_t)1 << 59;
-constexpr int64_t kMaxProduct = (int64_t)1 << 50;   // M N, M K, K N: 32 fp32 slices of one stay inside int64
-constexpr int64_t kMaxOutPitch = (int64_t)1 << 26;  // 16 rows of fp32 stay inside the epilogue's 32-bit lane offsets
-constexpr int64_t kMaxGrid = 0x7fffffff;
-
-struct Matrix {
-    const void* data;
-    int64_t rows, cols, ld, elem, copies = 1, copy_stride = 0;
-
-    bool empty() const { return rows == 0 || cols == 0 || copies == 0; }
-    bool pitch_ok() const {
-        if (ld < std::max<int64_t>(cols, 1)) return false;
-        // (rows too long to count are refused by small_enough)
-        return copies <= 1 || rows == 0 || rows > kMaxElements / ld || copy_stride >= (rows - 1) * ld + cols;
-    }
-    bool small_enough() const {
-        return rows <= kMaxElements / ld && (copies <= 1 || copy_stride <= kMaxElements / copies);
-    }
-    int64_t bytes() const {
-        return empty() ? 0 : ((copies - 1) * copy_stride + (rows - 1) * ld + cols) * elem;
-    }
-    bool overlaps(const Matrix& o) const {
-        if (!data || !o.data || empty() || o.empty()) return false;
-        const uintptr_t a = (uintptr_t)data, b = (uintptr_t)o.data;
-        return a < b + (uintptr_t)o.bytes() && b < a + (uintptr_t)bytes();
-    }
-    bool same_place(const Matrix& o) const { return data == o.data && ld == o.ld && elem == o.elem; }
-    // Every row starts on 16 bytes (and every copy).
-    bool aligned16() const {
-        return ((uintptr_t)data & 15) == 0 && ld % 8 == 0 && (copies <= 1 || copy_stride % 8 == 0);
-    }
-};
-
-bool products_ok(int64_t m, int64_t n, int64_t k) {
-    const auto ok = [](int64_t a, int64_t b) { return b == 0 || a <= kMaxProduct / b; };
-    return ok(m, n) && ok(m, k) && ok(k, n);
-}
-bool out_pitch_ok(const Matrix& m) { return !m.data || m.rows <= 1 || m.ld <= kMaxOutPitch; }
-
-// Pitches, sizes and presence of every matrix; an optional one may be NULL.
-struct Use {
-    Matrix m;
-    bool optional, written;
-};
-int check_matrices(const Use* uses, int n) {
-    for (int i = 0; i < n; ++i)
-        if ((uses[i].m.data || !uses[i].optional) && !uses[i].m.pitch_ok()) return GEMM_ERR_INVALID_LD;
-    for (int i = 0; i < n; ++i)
-        if ((uses[i].m.data || !uses[i].optional) && !uses[i].m.small_enough()) return GEMM_ERR_TOO_LARGE;
-    for (int i = 0; i < n; ++i)
-        if (!uses[i].optional && !uses[i].m.empty() && !uses[i].m.data) return GEMM_ERR_NULL;
-    for (int i = 0; i < n; ++i)
-        for (int j = 0; j < n; ++j)
-            if (i != j && uses[i].written && uses[i].m.overlaps(uses[j].m)) return GEMM_ERR_ALIAS;
-    return GEMM_OK;
-}
-
-int64_t elem_bytes(int output_type) { return output_type == GEMM_OUTPUT_F32 ? 4 : 2; }
-bool known_type(int input_type) { return input_type == GEMM_INPUT_BF16 || input_type == GEMM_INPUT_F16; }
-bool known_output(int t) { return t == GEMM_OUTPUT_SAME || t == GEMM_OUTPUT_F32; }
 bool known_act(int a) { return a >= 0 && a < kActCount; }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-// ---- the choice of tile and slices ----------------------------------------------------
-constexpr double kNoPlan = 1e300;
-struct Plan {
-    LinearTile tile;
-    bool direct;
-    int splits;
-    int64_t slice;
-    double us;  // as estimated
-
-    bool found() const { return us < kNoPlan; }
-};
-
-// Times of the tiles in microseconds, fitted to 10000 forward products of
-// every tile and slicing, of 1 to 16384 rows by 64 to 8192 columns and 64 to
-// 8192 deep, one matrix or up to 32 groups: `once` for the launch, and for a
-// round of workgroups `fixed` and, per contraction tile, `alone` with one
-// workgroup per CU and `full` with every place taken.  Over those products the
-// choice takes 1.4 % more than the best on average (a fit to products of 1024
-// columns and depth and more took 6.4 %, most of it on short contractions).
-// The register path's, and packing's time, were fitted to 7000 products of odd
-// widths run both ways: 2.4 % more than the best on average (11 % before).
-struct TileTime {
-    int per_cu;
-    double once, fixed, alone, full;
-};
-constexpr TileTime kDirectTimes[kTileCount] = {
-    {1, 3.3, 15.3, 0.98, 1.57}, {2, 4.3, 6.7, 0.69, 1.21}, {2, 4.3, 3.1, 0.24, 0.54}, {2, 4.3, 3.3, 0.24, 0.56}};
-constexpr TileTime kRegisterTimes[kTileCount] = {
-    {1, 0, 0, 0, 0}, {2, 11.6, 0, 2.2, 3.0}, {2, 5.3, 1.5, 1.13, 0.77}, {2, 5.7, 1.2, 1.45, 0.99}};
-
-// How a product reads its operands, and the register path's time per
-// contraction tile by which of the two are of odd widths.
-struct Path {
-    bool direct;
-    double slow;
-};
-constexpr int kMaxSlices = 32;
-
-// Estimated microseconds of a plan: its launch, its rounds (the last one by
-// how much of the chip it takes) and its operands' bytes at 4.2 TB/s (2.2
-// through registers), the larger of the two counting most (fourth powers), and
-// the slices' join.
-double estimate(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, LinearTile t, Path path, int splits,
-                int cus) {
-    TileTime time = (path.direct ? kDirectTimes : kRegisterTimes)[t];
-    if (time.alone <= 0) return 1e30;
-    time.alone *= path.slow;
-    time.full *= path.slow;
-    const TileSize size = kTileSizes[t];
-    double row_tiles = (double)ceil_div(R, size.bm), length = (double)L, copies = 1;
-    if (axis == kGroupRows) {
-        // half a tile more on average for every group that has rows, and two standard deviations of their sum: a
-        // round begun costs more than one left out saves
-        copies = (double)std::min<int64_t>(groups, R);
-        row_tiles = std::max((double)R / size.bm + 0.5 * copies + 0.6 * std::sqrt(copies), copies);
-    }
-    double tiles = row_tiles * (double)ceil_div(C, size.bn) * splits;
-    if (axis == kGroupContraction) {
-        tiles *= (double)groups;
-        length = (double)L / (double)groups;
-    }
-    const double slots = (double)cus * time.per_cu;
-    const double depth = (double)ceil_div((int64_t)(length / splits + 0.999), kTileDepth);
-    const double whole = (double)(int64_t)(tiles / slots), left = tiles / slots - whole;  // rounds
-    double us = whole * (time.fixed + depth * time.full);
-    if (left > 0) {
-        // from `alone` while there is at most one workgroup per CU (one-per-CU tiles: by the share of CUs) to `full`
-        const double busy = time.per_cu == 1 ? left : std::max(0.0, left * time.per_cu - 1) / (time.per_cu - 1);
-        const double last = time.fixed + depth * (time.alone + busy * (time.full - time.alone));
-        const bool tail = t == kTile256 && path.direct && axis != kGroupContraction && splits == 1 && whole > 0 &&
-                          depth >= kTailDepth && left <= 0.5;
-        us += tail ? std::min(last, time.fixed + depth * time.full * left + 30) : last;
-    }
-    const double bytes = 2.0 * ((double)R * (double)L + copies * (double)L * (double)C) +
-                         2.0 * (double)R * (double)C * (axis == kGroupContraction ? (double)groups : 1.0);
-    const double memory = bytes / (path.direct ? 4.2e6 : 2.2e6), u2 = us * us, m2 = memory * memory;
-    us = time.once + std::sqrt(std::sqrt(u2 * u2 + m2 * m2));
-    if (splits > 1) us += 2.1 + (splits + 1.0) * (double)R * (double)C * 4.0 / 4.4e6;
-    return us;
-}
-
-// Row tiles enough for any division of R rows into groups, R of which have
-// rows at most (places that no tile takes are not only launched: they leave
-// the real tiles to fewer XCDs.  Counted for all groups, 1 row of 32 experts
-// of 4096x4096 took 48.7 us, 8 rows 105; so 19.6 and 44.8).
-int64_t row_tiles(int64_t R, int64_t groups, int axis, int64_t bm) {
-    if (axis != kGroupRows) return ceil_div(R, bm);
-    return (R + std::min(groups, R) * (bm - 1)) / bm;
-}
-
-// Whether a launch holds the tiles (it has fewer than 2^31 threads, of tiles
-// with 512 each).
-constexpr int64_t kMaxTiles = kMaxGrid / 512;
-bool grid_fits(int64_t R, int64_t C, int64_t groups, int axis, LinearTile tile, int splits) {
-    const TileSize size = kTileSizes[tile];
-    const int64_t tiles_m = row_tiles(R, groups, axis, size.bm), tiles_n = ceil_div(C, size.bn);
-    return tiles_n == 0 || tiles_m <= kMaxTiles / tiles_n / (axis == kGroupContraction ? groups : splits);
-}
-
-// The quickest of the plans that a launch holds; none of them: not found().
-Plan choose(int64_t R, int64_t C, int64_t L, int64_t groups, int axis, Path path, int variant, int splits, int cus) {
-    Plan best{kTile128, path.direct, 1, L, kNoPlan};
-    for (int t = 0; t < kTileCount; ++t) {
-        if (variant != GEMM_LINEAR_AUTO && t != variant - 1) continue;
-        LinearTile tile = (LinearTile)t;
-        if (tile == kTile256 && !path.direct) {
-            if (variant == GEMM_LINEAR_AUTO) continue;
-            tile = kTile128;
-        }
-        for (int s = 1; s <= kMaxSlices; s *= 2) {
-            int use = splits > 0 ? splits : s;
-            if (axis != kGroupNone || L == 0) use = 1;
-            // slices of whole tiles, none of them empty, at least four deep unless asked for
-            const int64_t slice = ceil_div(ceil_div(L, kTileDepth), use) * kTileDepth;
-            if (use > 1) {
-                if (splits == 0 && slice < 4 * kTileDepth) break;
-                use = (int)ceil_div(L, slice);
-            }
-            if (!grid_fits(R, C, groups, axis, tile, std::max(use, 1))) break;
-            double us = estimate(R, C, L, groups, axis, tile, path, use, cus);
-            // at equal times the tile whose rows are used, and fewer slices
-            if (tile == kTile32x128 && R > 32 * groups) us += 0.3;
-            if (us < best.us - 0.2) best = Plan{tile, path.direct, std::max(use, 1), slice, us};
-            if (splits > 0 || axis != kGroupNone || L == 0) break;
-        }
-    }
-    return best;
-}
-
-int64_t partial_bytes(const Plan& plan, int64_t R, int64_t C) { return plan.splits > 1 ? plan.splits * R * C * 4 : 0; }
-
-// The blocks for the slices of a last round (tail_split): one per workgroup
-// of a persistent grid, where it has whole rounds before it.
-int64_t tail_bytes(const Plan& plan, int64_t R, int64_t C, int64_t L, int64_t groups, int axis, int cus) {
-    if (plan.tile != kTile256 || !plan.direct || plan.splits > 1 || axis == kGroupContraction) return 0;
-    if (ceil_div(L, kTileDepth) < kTailDepth) return 0;
-    const int64_t most = row_tiles(R, groups, axis, 256) * ceil_div(C, 256);
-    if (most <= cus) return 0;
-    if (axis == kGroupNone && (most % cus == 0 || cus / (most % cus) < 2)) return 0;
-    return (int64_t)cus * 256 * 256 * 4;
-}
 
 hipError_t launch(int type, const LinearProblem& p, LinearLayout layout, const Plan& plan, int cus,
                   hipStream_t stream) {
@@ -274,53 +46,6 @@ hipError_t launch(int type, const LinearProblem& p, LinearLayout layout, const P
 }
 
 // ---- gemm_linear ----------------------------------------------------------------------
-bool copies_fit(LinearTile tile, const Matrix& a, bool a_kmajor, const Matrix& b, bool b_kmajor) {
-    // OperandCopy's offsets: within a tile, k-major within the whole contraction, they stay below 2^30
-    const TileSize size = kTileSizes[tile];
-    const auto fits = [](int64_t ld, int64_t rows, int64_t cols) { return ld <= 0x3fffffff / (2 * rows) - cols; };
-    return fits(a.ld, a_kmajor ? size.bm : kTileDepth, a_kmajor ? kTileDepth : size.bm) &&
-           fits(b.ld, b_kmajor ? size.bn : kTileDepth, b_kmajor ? kTileDepth : size.bn);
-}
-
-// 16-byte copies of both operands: rows and widths in whole 16 bytes, and
-// offsets inside a tile that fit whatever tile is chosen.
-bool direct_ok(const Matrix& a, bool a_kmajor, const Matrix& b, bool b_kmajor) {
-    return a.aligned16() && b.aligned16() && a.cols % 8 == 0 && b.cols % 8 == 0 &&
-           copies_fit(kTile256, a, a_kmajor, b, b_kmajor);
-}
-
-// An operand as the products read it: itself, or packed to rows of whole 16
-// bytes in the workspace.
-bool whole_rows(const Matrix& m) { return m.aligned16() && m.cols % 8 == 0; }
-Matrix packed(const Matrix& m) {
-    Matrix r = m;
-    r.ld = ceil_div(std::max<int64_t>(m.cols, 1), 8) * 8;
-    r.copy_stride = m.rows * r.ld;
-    r.data = nullptr;  // (placed when the workspace is known)
-    return r;
-}
-int64_t packed_bytes(const Matrix& m) { return ceil_div(2 * m.copies * m.rows * packed(m).ld, 256) * 256; }
-// Reading and writing every element once at 5.3 TB/s, beside the launch.
-constexpr double kPackLaunch = 3.5;
-double pack_us(const Matrix& m) { return 2.0 * (double)packed_bytes(m) / 5.3e6; }
-
-constexpr Path kDirect{true, 1};
-Path path_of(const Matrix& a, bool a_kmajor, const Matrix& b, bool b_kmajor) {
-    if (direct_ok(a, a_kmajor, b, b_kmajor)) return kDirect;
-    const bool whole_a = whole_rows(a), whole_b = whole_rows(b);
-    return Path{false, whole_a == whole_b ? 1.0 : whole_b ? 0.55 : 0.94};
-}
-
-// Workspace cut into 256-byte pieces from its start.
-struct Space {
-    char* at;
-    void* take(int64_t bytes) {
-        void* p = at;
-        at += ceil_div(bytes, 256) * 256;
-        return p;
-    }
-};
-
 // `bias`: joined by the same launch; nullptr: nothing to join.
 int launch_pack(const Matrix* from, Matrix* to, int n, Space* space, const SlopeProblem* bias, hipStream_t stream) {
     PackJobs jobs{};

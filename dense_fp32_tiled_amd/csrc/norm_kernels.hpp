@@ -1,0 +1,543 @@
+// norm_kernels.hpp -- gfx950 kernels of the layer norm with the residual
+// stream's addition and the dropout before it, of their gradients, and of
+// dropout alone.
+//
+//   total = dropout(x) + residual          rounded to the type: the stream that the next block adds to
+//   mean, rstd = of each row of total, rstd = (mean of (total - mean)^2 + eps)^-1/2
+//   y = (total - mean) rstd weight + bias
+//
+//   u = (total - mean) rstd,  g = dy weight
+//   dtotal = rstd (g - mean(g) - u mean(g u)) + dstream,   dx = dropout of dtotal with the same mask
+//   dweight = sum over the rows of dy u,  dbias = sum over the rows of dy
+//
+// All are bound by bytes: each row is read once, kept in registers between
+// its sums and its results, and written once.  Statistics and sums are fp32;
+// the variance is the mean of squared deviations from the mean, taken in a
+// second pass over the registers, so a mean far from zero costs no digits.
+// The gradient of weight and bias is summed in registers over the rows that a
+// workgroup takes, and joined over the workgroups in a fixed order.
+#pragma once
+
+#include "dropout.hpp"
+#include "values8.hpp"
+
+namespace dft {
+
+struct NormProblem {
+    int64_t rows, cols;
+    float eps;
+    Dropout dropout;
+    const void* x;        // forward; the gradient's `total` is read at `total`
+    int64_t ldx;
+    const void* residual;  // or nullptr
+    int64_t ldr;
+    const void *weight, *bias;  // or nullptr
+    void* total;           // forward: nullptr when total is x itself
+    int64_t ldt;
+    void* y;               // forward: written; gradient: dy, read
+    int64_t ldy;
+    float *mean, *rstd;
+    // gradient
+    const void* dstream;   // gradient that reaches total by another way, or nullptr
+    int64_t lds;
+    void* dtotal;          // or nullptr
+    int64_t lddt;
+    void* dx;              // or nullptr
+    int64_t lddx;
+    float* partial;        // places x 2 x cols: sums of dy u and of dy; nullptr: not wanted
+    int32_t places;
+    float *dweight, *dbias;
+};
+
+// A row is WAVES waves' work, CHUNKS chunks of eight per lane; waves that
+// share no row stand in one workgroup of at least four.
+template <int WAVES_, int CHUNKS_>
+struct NormShape {
+    static constexpr int WAVES = WAVES_, CHUNKS = CHUNKS_, COLS = WAVES * kWave * 8 * CHUNKS;
+    static constexpr int ROWS = WAVES >= 4 ? 1 : 4 / WAVES, THREADS = WAVES * ROWS * kWave;
+};
+
+// Sums of N values over a row's waves, the same in every lane.  `at` alternates
+// between the two halves of the array, so that one barrier does: a wave that
+// writes a half again has passed the barrier after all reads of it.
+template <int WAVES, int N>
+__device__ inline void row_sums(float (&v)[N], float (*shared)[WAVES][N], int at) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = wave_sum(v[n]);
+    if constexpr (WAVES > 1) {
+        const int wave = threadIdx.x / kWave;
+        if (threadIdx.x % kWave == 0) {
+#pragma unroll
+            for (int n = 0; n < N; ++n) shared[at][wave][n] = v[n];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            v[n] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) v[n] += shared[at][w][n];
+        }
+    }
+}
+
+// A row's statistics from the rounded mean `near` of a first pass, and the
+// mean deviation from it and mean squared deviation of a second: what the
+// first rounding left out (`shift`) moves mean, variance and deviations.
+struct NormStatistics {
+    float mean, shift, rstd;
+};
+__device__ inline NormStatistics norm_statistics(float near, float shift, float square, float eps) {
+    const float variance = square - shift * shift;
+    return NormStatistics{near + shift, shift, 1.0f / sqrtf((variance < 0.0f ? 0.0f : variance) + eps)};
+}
+
+template <int TYPE, class Shape, bool WHOLE>
+__global__ __launch_bounds__(Shape::THREADS) void norm_kernel(NormProblem p) {
+    using V = Values8<TYPE>;
+    using E = typename V::element;
+    constexpr int WAVES = Shape::WAVES, CHUNKS = Shape::CHUNKS;
+    __shared__ float shared[2][WAVES][2];
+    const int lane = threadIdx.x % (WAVES * kWave), part = threadIdx.x / (WAVES * kWave);
+    const int64_t chunks = (p.cols + 7) / 8;
+    const uint64_t offset = p.dropout.drop ? dropout_offset(p.dropout) : 0;
+    const float n = (float)p.cols;
+    for (int64_t first = (int64_t)blockIdx.x * Shape::ROWS; first < p.rows; first += (int64_t)gridDim.x * Shape::ROWS) {
+        const int64_t row = first + part;
+        if (WAVES < 4 && row >= p.rows) break;  // (whole waves: nothing is waited for together)
+        const E* x = static_cast<const E*>(p.x) + row * p.ldx;
+        const E* residual = p.residual ? static_cast<const E*>(p.residual) + row * p.ldr : nullptr;
+        E* total = p.total ? static_cast<E*>(p.total) + row * p.ldt : nullptr;
+        V in[CHUNKS], add[CHUNKS], weight[CHUNKS], bias[CHUNKS];
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int64_t chunk = lane + c * WAVES * kWave, left = p.cols - chunk * 8;
+            in[c].template load<WHOLE>(x + chunk * 8, left);
+        }
+        if (p.residual) {
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) {
+                const int64_t chunk = lane + c * WAVES * kWave;
+                add[c].template load<WHOLE>(residual + chunk * 8, p.cols - chunk * 8);
+            }
+        }
+        if (p.weight) {
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) {
+                const int64_t chunk = lane + c * WAVES * kWave;
+                weight[c].template load<WHOLE>(static_cast<const E*>(p.weight) + chunk * 8, p.cols - chunk * 8);
+            }
+        }
+        if (p.bias) {
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c) {
+                const int64_t chunk = lane + c * WAVES * kWave;
+                bias[c].template load<WHOLE>(static_cast<const E*>(p.bias) + chunk * 8, p.cols - chunk * 8);
+            }
+        }
+        float t[CHUNKS][8], sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int64_t chunk = lane + c * WAVES * kWave, left = p.cols - chunk * 8;
+            in[c].widen(t[c]);
+            if (p.total) {
+                if (p.dropout.drop) drop8(p.dropout, offset, (uint64_t)(row * chunks + chunk), t[c]);
+                if (p.residual) {
+                    float r[8];
+                    add[c].widen(r);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) t[c][e] += r[e];
+                }
+                const V kept = V::narrow(t[c]);
+                kept.template store<WHOLE>(total + chunk * 8, left);
+                kept.widen(t[c]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[0] += t[c][e];  // (zeros past the row)
+        }
+        row_sums<WAVES, 2>(sum, shared, 0);
+        const float near = sum[0] / n;
+        float off[2] = {0.0f, 0.0f};  // sums of the deviations and of their squares
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int64_t left = p.cols - (lane + c * WAVES * kWave) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                t[c][e] -= near;
+                const float d = (WHOLE ? left > 0 : e < left) ? t[c][e] : 0.0f;
+                off[0] += d;
+                off[1] += d * d;
+            }
+        }
+        row_sums<WAVES, 2>(off, shared, 1);
+        const NormStatistics s = norm_statistics(near, off[0] / n, off[1] / n, p.eps);
+        if (lane == 0) {
+            if (p.mean) p.mean[row] = s.mean;
+            if (p.rstd) p.rstd[row] = s.rstd;
+        }
+        E* y = static_cast<E*>(p.y) + row * p.ldy;
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int64_t chunk = lane + c * WAVES * kWave, left = p.cols - chunk * 8;
+            float w[8], b[8];
+            if (p.weight) weight[c].widen(w);
+            if (p.bias) bias[c].widen(b);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                t[c][e] = (t[c][e] - s.shift) * s.rstd;
+                if (p.weight) t[c][e] *= w[e];
+                if (p.bias) t[c][e] += b[e];
+            }
+            V::narrow(t[c]).template store<WHOLE>(y + chunk * 8, left);
+        }
+    }
+}
+
+// Rows too wide for the registers: the row is read three times, from the
+// caches after the first.
+constexpr int kWideThreads = 1024;
+template <int TYPE>
+__global__ __launch_bounds__(kWideThreads) void norm_wide_kernel(NormProblem p) {
+    using V = Values8<TYPE>;
+    using E = typename V::element;
+    constexpr int WAVES = kWideThreads / kWave;
+    __shared__ float shared[2][WAVES][2];
+    const int64_t chunks = (p.cols + 7) / 8;
+    const uint64_t offset = p.dropout.drop ? dropout_offset(p.dropout) : 0;
+    const float n = (float)p.cols;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const E* x = static_cast<const E*>(p.x) + row * p.ldx;
+        const E* residual = p.residual ? static_cast<const E*>(p.residual) + row * p.ldr : nullptr;
+        E* total = p.total ? static_cast<E*>(p.total) + row * p.ldt : nullptr;
+        float sum[2] = {0.0f, 0.0f}, off[2] = {0.0f, 0.0f}, t[8];
+        V v;
+        for (int64_t chunk = threadIdx.x; chunk < chunks; chunk += kWideThreads) {
+            const int64_t left = p.cols - chunk * 8;
+            v.template load<false>(x + chunk * 8, left);
+            v.widen(t);
+            if (p.total) {
+                if (p.dropout.drop) drop8(p.dropout, offset, (uint64_t)(row * chunks + chunk), t);
+                if (p.residual) {
+                    float r[8];
+                    v.template load<false>(residual + chunk * 8, left);
+                    v.widen(r);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) t[e] += r[e];
+                }
+                v = V::narrow(t);
+                v.template store<false>(total + chunk * 8, left);
+                v.widen(t);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[0] += e < left ? t[e] : 0.0f;
+        }
+        row_sums<WAVES, 2>(sum, shared, 0);
+        const float near = sum[0] / n;
+        const E* kept = p.total ? total : x;  // (each thread reads back what it wrote)
+        for (int64_t chunk = threadIdx.x; chunk < chunks; chunk += kWideThreads) {
+            const int64_t left = p.cols - chunk * 8;
+            v.template load<false>(kept + chunk * 8, left);
+            v.widen(t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float d = e < left ? t[e] - near : 0.0f;
+                off[0] += d;
+                off[1] += d * d;
+            }
+        }
+        row_sums<WAVES, 2>(off, shared, 1);
+        const NormStatistics s = norm_statistics(near, off[0] / n, off[1] / n, p.eps);
+        if (threadIdx.x == 0) {
+            if (p.mean) p.mean[row] = s.mean;
+            if (p.rstd) p.rstd[row] = s.rstd;
+        }
+        for (int64_t chunk = threadIdx.x; chunk < chunks; chunk += kWideThreads) {
+            const int64_t left = p.cols - chunk * 8;
+            float w[8];
+            v.template load<false>(kept + chunk * 8, left);
+            v.widen(t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) t[e] = (t[e] - near - s.shift) * s.rstd;
+            if (p.weight) {
+                v.template load<false>(static_cast<const E*>(p.weight) + chunk * 8, left);
+                v.widen(w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[e] *= w[e];
+            }
+            if (p.bias) {
+                v.template load<false>(static_cast<const E*>(p.bias) + chunk * 8, left);
+                v.widen(w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) t[e] += w[e];
+            }
+            V::narrow(t).template store<false>(static_cast<E*>(p.y) + row * p.ldy + chunk * 8, left);
+        }
+    }
+}
+
+// ---- gradients ------------------------------------------------------------------------
+// Eight columns of one row's results: dtotal and, through the mask, dx.
+template <int TYPE, bool WHOLE>
+__device__ inline void norm_grad_store(const NormProblem& p, uint64_t offset, int64_t row, int64_t chunk, float (&d)[8]) {
+    using V = Values8<TYPE>;
+    using E = typename V::element;
+    const int64_t left = p.cols - chunk * 8;
+    if (p.dtotal) V::narrow(d).template store<WHOLE>(static_cast<E*>(p.dtotal) + row * p.lddt + chunk * 8, left);
+    if (p.dx) {
+        if (p.dropout.drop) drop8(p.dropout, offset, (uint64_t)(row * ((p.cols + 7) / 8) + chunk), d);
+        V::narrow(d).template store<WHOLE>(static_cast<E*>(p.dx) + row * p.lddx + chunk * 8, left);
+    }
+}
+
+template <int TYPE, class Shape, bool WHOLE>
+__global__ __launch_bounds__(Shape::THREADS) void norm_grad_kernel(NormProblem p) {
+    using V = Values8<TYPE>;
+    using E = typename V::element;
+    constexpr int WAVES = Shape::WAVES, CHUNKS = Shape::CHUNKS;
+    __shared__ float shared[2][WAVES][2];
+    const int lane = threadIdx.x % (WAVES * kWave), part = threadIdx.x / (WAVES * kWave);
+    const uint64_t offset = p.dropout.drop ? dropout_offset(p.dropout) : 0;
+    const float each = 1.0f / (float)p.cols;
+    auto column = [&](int c) { return (int64_t)(lane + c * WAVES * kWave); };  // (in chunks of eight)
+    V weight[CHUNKS];
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c)
+        if (p.weight) weight[c].template load<WHOLE>(static_cast<const E*>(p.weight) + column(c) * 8, p.cols - column(c) * 8);
+    float dweight[CHUNKS][8] = {}, dbias[CHUNKS][8] = {};
+    const int64_t step = (int64_t)gridDim.x * Shape::ROWS;
+    int at = 0;
+    for (int64_t row = (int64_t)blockIdx.x * Shape::ROWS + part; row < p.rows; row += step) {
+        V dy[CHUNKS], total[CHUNKS], stream[CHUNKS];
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int64_t left = p.cols - column(c) * 8;
+            dy[c].template load<WHOLE>(static_cast<const E*>(p.y) + row * p.ldy + column(c) * 8, left);
+            total[c].template load<WHOLE>(static_cast<const E*>(p.total) + row * p.ldt + column(c) * 8, left);
+        }
+        if (p.dstream) {
+#pragma unroll
+            for (int c = 0; c < CHUNKS; ++c)
+                stream[c].template load<WHOLE>(static_cast<const E*>(p.dstream) + row * p.lds + column(c) * 8,
+                                               p.cols - column(c) * 8);
+        }
+        const float mean = p.mean[row], rstd = p.rstd[row];
+        float g[CHUNKS][8], u[CHUNKS][8], sums[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int64_t left = p.cols - column(c) * 8;
+            float w[8];
+            dy[c].widen(g[c]);
+            total[c].widen(u[c]);
+            if (p.weight) weight[c].widen(w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                // (past the row dy is zero, and u finite)
+                u[c][e] = (WHOLE ? left > 0 : e < left) ? (u[c][e] - mean) * rstd : 0.0f;
+                dweight[c][e] += g[c][e] * u[c][e];
+                dbias[c][e] += g[c][e];
+                if (p.weight) g[c][e] *= w[e];
+                sums[0] += g[c][e];
+                sums[1] += g[c][e] * u[c][e];
+            }
+        }
+        row_sums<WAVES, 2>(sums, shared, at);
+        at ^= 1;
+        const float m = sums[0] * each, mu = sums[1] * each;
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+            float add[8];
+            if (p.dstream) stream[c].widen(add);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                g[c][e] = (g[c][e] - m - u[c][e] * mu) * rstd;
+                if (p.dstream) g[c][e] += add[e];
+            }
+            if (p.cols > column(c) * 8) norm_grad_store<TYPE, WHOLE>(p, offset, row, column(c), g[c]);
+        }
+    }
+    if (!p.partial) return;
+    // Rows that different waves of the workgroup took are added in the waves' order.
+    if constexpr (Shape::ROWS > 1) {
+        __shared__ float sums[Shape::ROWS][2][Shape::COLS];
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                sums[part][0][column(c) * 8 + e] = dweight[c][e];
+                sums[part][1][column(c) * 8 + e] = dbias[c][e];
+            }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * Shape::COLS; i += Shape::THREADS) {
+            const int which = i / Shape::COLS, col = i % Shape::COLS;
+            float v = 0.0f;
+#pragma unroll
+            for (int r = 0; r < Shape::ROWS; ++r) v += sums[r][which][col];
+            if (col < p.cols) p.partial[((int64_t)which * p.places + blockIdx.x) * p.cols + col] = v;
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+            const int64_t left = p.cols - column(c) * 8;
+            float* to = p.partial + (int64_t)blockIdx.x * p.cols + column(c) * 8;
+            if (left > 0) {
+                store8(to, dweight[c], WHOLE ? 8 : left);
+                store8(to + (int64_t)p.places * p.cols, dbias[c], WHOLE ? 8 : left);
+            }
+        }
+    }
+}
+
+// dweight and dbias over the workgroups' sums: 32 columns by 32 strides of
+// places per workgroup, the strides' sums added in ascending order.
+constexpr int kNormJoinCols = 32, kNormJoinStrides = 32;
+__global__ __launch_bounds__(kNormJoinCols * kNormJoinStrides) void norm_join_kernel(NormProblem p) {
+    __shared__ float sums[kNormJoinStrides][kNormJoinCols + 1];
+    const int c = threadIdx.x % kNormJoinCols, r = threadIdx.x / kNormJoinCols;
+    const int64_t col = (int64_t)blockIdx.x * kNormJoinCols + c;
+    float* const out = blockIdx.y == 0 ? p.dweight : p.dbias;
+    if (!out) return;
+    float sum = 0.0f;
+    if (col < p.cols) {
+        const float* from = p.partial + (int64_t)blockIdx.y * p.places * p.cols + col;
+#pragma unroll 8
+        for (int k = r; k < p.places; k += kNormJoinStrides) sum += from[k * p.cols];
+    }
+    sums[r][c] = sum;
+    __syncthreads();
+    if (r == 0 && col < p.cols) {
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kNormJoinStrides; ++k) v += sums[k][c];
+        out[col] = v;
+    }
+}
+
+// Rows too wide for the registers: the row's sums and results in two passes,
+// and the columns' sums in a kernel of their own.
+template <int TYPE>
+__global__ __launch_bounds__(kWideThreads) void norm_grad_wide_kernel(NormProblem p) {
+    using V = Values8<TYPE>;
+    using E = typename V::element;
+    constexpr int WAVES = kWideThreads / kWave;
+    __shared__ float shared[2][WAVES][2];
+    const int64_t chunks = (p.cols + 7) / 8;
+    const uint64_t offset = p.dropout.drop ? dropout_offset(p.dropout) : 0;
+    const float each = 1.0f / (float)p.cols;
+    int at = 0;
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        const float mean = p.mean[row], rstd = p.rstd[row];
+        float sums[2] = {0.0f, 0.0f}, g[8], u[8];
+        auto read = [&](int64_t chunk, int64_t left) {
+            V v;
+            v.template load<false>(static_cast<const E*>(p.y) + row * p.ldy + chunk * 8, left);
+            v.widen(g);
+            v.template load<false>(static_cast<const E*>(p.total) + row * p.ldt + chunk * 8, left);
+            v.widen(u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] = e < left ? (u[e] - mean) * rstd : 0.0f;
+            if (p.weight) {
+                float w[8];
+                v.template load<false>(static_cast<const E*>(p.weight) + chunk * 8, left);
+                v.widen(w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) g[e] *= w[e];
+            }
+        };
+        for (int64_t chunk = threadIdx.x; chunk < chunks; chunk += kWideThreads) {
+            read(chunk, p.cols - chunk * 8);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                sums[0] += g[e];
+                sums[1] += g[e] * u[e];
+            }
+        }
+        row_sums<WAVES, 2>(sums, shared, at);
+        at ^= 1;
+        const float m = sums[0] * each, mu = sums[1] * each;
+        for (int64_t chunk = threadIdx.x; chunk < chunks; chunk += kWideThreads) {
+            const int64_t left = p.cols - chunk * 8;
+            read(chunk, left);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = (g[e] - m - u[e] * mu) * rstd;
+            if (p.dstream) {
+                V v;
+                float add[8];
+                v.template load<false>(static_cast<const E*>(p.dstream) + row * p.lds + chunk * 8, left);
+                v.widen(add);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) g[e] += add[e];
+            }
+            norm_grad_store<TYPE, false>(p, offset, row, chunk, g);
+        }
+    }
+}
+
+// Sums of dy u and of dy over every places-th row, 2048 columns per workgroup.
+template <int TYPE>
+__global__ __launch_bounds__(256) void norm_columns_kernel(NormProblem p) {
+    using V = Values8<TYPE>;
+    using E = typename V::element;
+    const int64_t chunk = (int64_t)blockIdx.y * 256 + threadIdx.x, left = p.cols - chunk * 8;
+    if (left <= 0) return;
+    float dweight[8] = {}, dbias[8] = {};
+#pragma unroll 2
+    for (int64_t row = blockIdx.x; row < p.rows; row += p.places) {
+        const float mean = p.mean[row], rstd = p.rstd[row];
+        V v;
+        float d[8], u[8];
+        v.template load<false>(static_cast<const E*>(p.y) + row * p.ldy + chunk * 8, left);
+        v.widen(d);
+        v.template load<false>(static_cast<const E*>(p.total) + row * p.ldt + chunk * 8, left);
+        v.widen(u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            dweight[e] += d[e] * ((u[e] - mean) * rstd);
+            dbias[e] += d[e];
+        }
+    }
+    float* to = p.partial + (int64_t)blockIdx.x * p.cols + chunk * 8;
+    store8(to, dweight, left);
+    store8(to + (int64_t)p.places * p.cols, dbias, left);
+}
+
+// ---- dropout alone ---------------------------------------------------------------------
+struct DropoutProblem {
+    int64_t rows, cols;
+    Dropout dropout;
+    const void* x;
+    int64_t ldx;
+    const void* residual;  // or nullptr
+    int64_t ldr;
+    void* y;
+    int64_t ldy;
+};
+
+// A thread takes a chunk of eight, or every stride-th where a launch does not
+// hold them all.  Rows that lie without gaps in whole chunks come as one row:
+// their chunks count on from row to row.
+template <int TYPE, bool WHOLE>
+__global__ __launch_bounds__(256) void dropout_kernel(DropoutProblem p) {
+    using V = Values8<TYPE>;
+    using E = typename V::element;
+    const int64_t chunks = (p.cols + 7) / 8, total = p.rows * chunks, stride = (int64_t)gridDim.x * 256;
+    const uint64_t offset = p.dropout.drop ? dropout_offset(p.dropout) : 0;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += stride) {
+        // (64-bit divisions would take as long as the generator)
+        const int64_t row = total <= 0xffffffff ? (uint32_t)i / (uint32_t)chunks : i / chunks;
+        const int64_t chunk = i - row * chunks, left = p.cols - chunk * 8;
+        V in, add;
+        in.template load<WHOLE>(static_cast<const E*>(p.x) + row * p.ldx + chunk * 8, left);
+        if (p.residual) add.template load<WHOLE>(static_cast<const E*>(p.residual) + row * p.ldr + chunk * 8, left);
+        float v[8];
+        in.widen(v);
+        if (p.dropout.drop) drop8(p.dropout, offset, (uint64_t)i, v);
+        if (p.residual) {
+            float r[8];
+            add.widen(r);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += r[e];
+        }
+        V::narrow(v).template store<WHOLE>(static_cast<E*>(p.y) + row * p.ldy + chunk * 8, left);
+    }
+}
+
+}  // namespace dft

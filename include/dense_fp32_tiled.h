@@ -616,6 +616,111 @@ int gemm_expert_combine_grad(int input_type, int64_t tokens, int64_t rows, int32
                              const void *dout, int64_t ldd, const void *Y, int64_t ldy, const int32_t *position,
                              const float *weights, void *dY, int64_t lddy, float *dweights, void *stream);
 
+/* ---- Between the products: layer norm and dropout ------------------------------
+ * What stands between the products of a model, over `rows` rows of `cols`
+ * values of value_type, with arithmetic, statistics and sums in fp32:
+ *     total = dropout(x) + residual   rounded to the type (the stream that the next block adds to)
+ *     mean, rstd                      of each row of total: rstd = (mean of (total - mean)^2 + eps)^-1/2
+ *     y = (total - mean) * rstd * weight + bias
+ * without dropout when p is 0 and without residual when it is NULL; with
+ * neither, total is x itself and is not written.
+ *
+ * dropout(x) is x / (1 - p) where kept and zero where dropped, whatever x holds
+ * there.  The mask is a function of (seed, offset + *step) and the element's row
+ * and column, and is never stored: the gradient passes the same values again.
+ * Philox4x32-10 under the key `seed`, of the counter (row * ceil(cols / 8) +
+ * column / 8, offset + *step), gives each eight columns 128 bits, of which each
+ * column takes 16, words' low halves first; an element is dropped when that
+ * number is below p * 65536 rounded to the nearest, and 1 - p above is the share
+ * of the 65536 numbers that keep.  p == 1 drops everything.  `step` is an
+ * optional DEVICE value, read when the kernel runs: a captured graph draws
+ * another mask at each replay when the program counts it up.
+ *
+ * Gradients, from dY and from dstream, the gradient that reaches total by
+ * other ways (optional), with u = (total - mean) * rstd and g = dY * weight:
+ *     dtotal = rstd * (g - mean(g) - u * mean(g * u)) + dstream      the residual's gradient too
+ *     dx = dropout of dtotal with the same mask
+ *     dweight = sum over the rows of dY * u,  dbias = sum over the rows of dY      (fp32)
+ *
+ * Conventions are those at the top of this header, and:
+ *   - total may be x or the residual (same address and pitch), and Y of gemm_dropout
+ *     X or the residual; no other output may overlap any operand (GEMM_ERR_ALIAS).
+ *   - rows == 0: nothing, but dweight and dbias are zero.  cols is at least 1
+ *     (gemm_dropout: 0 does nothing).
+ *   - GEMM_ERR_UNSUPPORTED: a p outside [0, 1], an eps that is negative, infinite
+ *     or NaN.  GEMM_ERR_TOO_LARGE: rows * cols above 2^50, cols above 2^31 (of
+ *     gradients, 65535 * 2048).
+ *   - Sums run in a fixed order: the same arguments and inputs give the same bits. */
+typedef enum {
+    GEMM_VALUE_BF16 = 0,
+    GEMM_VALUE_F16 = 1,
+    GEMM_VALUE_F32 = 2
+} gemm_value_type;
+
+typedef struct {
+    int32_t value_type;     /* gemm_value_type of x, residual, weight, bias, total and y */
+    float eps;
+    double p;               /* 0: no dropout, and seed, offset and step are ignored */
+    uint64_t seed, offset;
+    const int64_t *step;    /* DEVICE, one value; or NULL */
+    int64_t rows, cols;
+    const void *x;
+    int64_t ldx;
+    const void *residual;   /* or NULL */
+    int64_t ldr;
+    const void *weight;     /* cols values, or NULL: ones */
+    const void *bias;       /* cols values, or NULL: zeros */
+    void *total;            /* ignored without residual and dropout */
+    int64_t ldt;
+    void *y;
+    int64_t ldy;
+    float *mean;            /* rows values, or NULL: not wanted */
+    float *rstd;            /* rows values, or NULL */
+} gemm_layer_norm_args;
+
+/* total, y, mean and rstd as above, enqueued on `stream`.  Returns a gemm_status. */
+int gemm_layer_norm(const gemm_layer_norm_args *args, void *stream);
+
+typedef struct {
+    int32_t value_type;     /* of dY, total, weight, dstream, dtotal and dx */
+    double p;
+    uint64_t seed, offset;
+    const int64_t *step;
+    int64_t rows, cols;
+    const void *dY;
+    int64_t ldy;
+    const void *total;      /* what the forward pass normalised */
+    int64_t ldt;
+    const float *mean;
+    const float *rstd;
+    const void *weight;     /* or NULL: ones */
+    const void *dstream;    /* or NULL */
+    int64_t lds;
+    void *dtotal;           /* or NULL: not wanted */
+    int64_t lddt;
+    void *dx;               /* or NULL */
+    int64_t lddx;
+    float *dweight;         /* cols values, or NULL */
+    float *dbias;           /* cols values, or NULL */
+    void *workspace;        /* DEVICE, 16-byte aligned; may be NULL when gemm_layer_norm_grad_workspace_bytes is 0 */
+    int64_t workspace_bytes;
+} gemm_layer_norm_grad_args;
+
+/* The gradients above, enqueued on `stream`; the workspace is the call's until
+ * its work on `stream` has ended.  Returns a gemm_status. */
+int gemm_layer_norm_grad(const gemm_layer_norm_grad_args *args, void *stream);
+
+/* Bytes gemm_layer_norm_grad needs on a device with num_cus compute units: each
+ * workgroup's sums for dweight and dbias.  Pure host call; a negative
+ * gemm_status on bad arguments. */
+int64_t gemm_layer_norm_grad_workspace_bytes(const gemm_layer_norm_grad_args *args, int32_t num_cus);
+
+/* Y = dropout(X) + residual (or without), rounded once.  Its own gradient:
+ * dropout of Y's gradient with the same p, seed, offset and step is X's. */
+int gemm_dropout(int value_type, int64_t rows, int64_t cols, double p, uint64_t seed, uint64_t offset,
+                 const int64_t *step, const void *X, int64_t ldx, const void *residual, int64_t ldr, void *Y,
+                 int64_t ldy, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
