@@ -140,6 +140,10 @@ EXPORTS = (
     "gemm_layer_norm_grad",
     "gemm_layer_norm_grad_workspace_bytes",
     "gemm_dropout",
+    "gemm_cross_entropy",
+    "gemm_cross_entropy_workspace_bytes",
+    "gemm_cross_entropy_grad",
+    "gemm_cross_entropy_grad_workspace_bytes",
 )
 
 
@@ -236,10 +240,10 @@ def library(path: Path | None = None):
     lib.gemm_lds_access_cycles.restype = i32
     lib.gemm_lds_page_pad.argtypes = [i32, i32, i32]
     lib.gemm_lds_page_pad.restype = i32
-    from . import norms, products
+    from . import losses, norms, products
 
-    products.declare(lib)
-    norms.declare(lib)
+    for module in (products, norms, losses):
+        module.declare(lib)
     if path is None:
         _lib = lib
     return lib
@@ -485,3 +489,7 @@ from .products import (  # noqa: E402
 from .norms import (  # noqa: E402
     VALUE_BF16, VALUE_F16, VALUE_F32, LayerNormArgs, LayerNormGradArgs, NormGrads, NormState, dropout, gemm_dropout,
     gemm_layer_norm, gemm_layer_norm_grad, gemm_layer_norm_grad_workspace_bytes, layer_norm, layer_norm_grad)
+from .losses import (  # noqa: E402
+    TARGET_I32, TARGET_I64, CrossEntropyArgs, CrossEntropyGradArgs, CrossEntropyGrads, gemm_cross_entropy,
+    gemm_cross_entropy_grad, gemm_cross_entropy_grad_workspace_bytes, gemm_cross_entropy_workspace_bytes,
+    linear_cross_entropy, linear_cross_entropy_grad)

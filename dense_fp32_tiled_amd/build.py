@@ -32,8 +32,8 @@ SOURCES = [CSRC / "gemm_api.hip", CSRC / "gemm_default.hip"]
 # their direct copies are buffer loads (range-checked), SOURCES' global ones; each list has its own checks of the
 # compiled code.
 LINEAR_SOURCES = [CSRC / "linear_api.hip", CSRC / "linear_bf16.hip", CSRC / "linear_f16.hip"]
-# What stands between the products and after the last one: the layer norm and dropout.
-MORE_SOURCES = [CSRC / "norm_api.hip"]
+# What stands between the products and after the last one: the layer norm, dropout and the vocabulary's loss.
+MORE_SOURCES = [CSRC / f"{n}.hip" for n in ("norm_api", "loss_api", "loss_bf16", "loss_f16", "loss_grad_bf16", "loss_grad_f16")]
 PROBE_LIB = PKG / "liblds_probe.so"
 PROBE_SOURCES = [CSRC / "lds_probe.hip"]
 ARCH = "gfx950"

@@ -131,10 +131,6 @@ int plan_linear(const gemm_linear_args& a, const LinearCall& c, int cus, LinearP
     return GEMM_OK;
 }
 
-bool workspace_ok(int64_t need, const void* workspace, int64_t bytes) {
-    return need == 0 || (workspace && bytes >= need && ((uintptr_t)workspace & 15) == 0);
-}
-
 int run_linear(const gemm_linear_args& a, hipStream_t stream) {
     LinearCall c;
     int st = describe(a, &c);

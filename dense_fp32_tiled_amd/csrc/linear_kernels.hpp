@@ -39,7 +39,12 @@ struct LinearEpilogue {
     int32_t out_f32;
 };
 
+// What a launch does with the sums of a tile: the layer's epilogue here; others
+// in problems that add to this one (loss_kernels.hpp).
+enum TileEpilogue { kEpilogueLayer = 0, kEpilogueRows = 1, kEpilogueValues = 2 };
+
 struct LinearProblem {
+    static constexpr int EPILOGUE = kEpilogueLayer;
     int64_t R, C, L;             // output rows, output columns, contraction length
     const uint16_t* A;           // k-major: R x L; else L x R
     int64_t lda;
@@ -543,6 +548,17 @@ struct OperandRead {
     }
 };
 
+// What a problem of its own epilogue keeps for a wave's rows, and does with
+// eight columns of one (specialised beside the problem).
+template <class Problem>
+struct EpilogueRows {
+    __device__ void load(const Problem&, int64_t, int64_t, int, int) {}
+    __device__ void of_row(int, int) {}
+    template <int TYPE>
+    __device__ void finish(const Problem&, const EpilogueBase&, const EpilogueLane&, int64_t, int64_t, int64_t,
+                           float (&)[8]) const {}
+};
+
 // ---- the product --------------------------------------------------------------------
 // PERSISTENT: one workgroup per place on the chip works through many tiles;
 // the first copies of the next tile are issued before the epilogue of this
@@ -628,15 +644,16 @@ __device__ inline TailSplit tail_split(const LinearProblem& p, uint32_t tiles, u
     return t;
 }
 
-// The kernel's own LinearProblem argument, read again from the argument
+// The kernel's own problem argument, read again from the argument
 // segment (scalar loads).  Kept live from the kernel's start, its fields and
 // the K loop's would not fit the scalar registers together, and what does not
 // fit is moved to vector registers that the sums need.
-__device__ inline LinearProblem problem_again() {
-    typedef __attribute__((address_space(4))) const LinearProblem constant_problem;
+template <class Problem>
+__device__ inline Problem problem_again() {
+    typedef __attribute__((address_space(4))) const Problem constant_problem;
     auto* at = (constant_problem*)__builtin_amdgcn_kernarg_segment_ptr();
     asm volatile("" : "+s"(at));
-    LinearProblem p;
+    Problem p;
     __builtin_memcpy(&p, at, sizeof(p));
     return p;
 }
@@ -734,13 +751,14 @@ __device__ inline void slice_work(const LinearProblem& p, const TailSplit& t, Li
 // branches, 27 with silu, residual and pre-activation): 8192^3 826 us forward
 // (1.33 PFLOP/s), 836 with the full epilogue, 745 dA (1.48), 795 dB (1.38).
 // Few rows are bound by B's bytes: 24 rows of 4096 by 16384 24.5 us (5.5 TB/s).
-template <int TYPE, bool AK, bool BK_, class Shape, bool DIRECT>
-__global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_kernel(LinearProblem, uint32_t tiles_m,
+template <int TYPE, bool AK, bool BK_, class Shape, bool DIRECT, class Problem = LinearProblem>
+__global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_kernel(Problem, uint32_t tiles_m,
                                                                                    uint32_t tiles_n, uint32_t grid_y) {
     using Op = Mfma16Op<TYPE, 16>;
     constexpr int BM = Shape::BM, BN = Shape::BN, BK = kDepth, S = DIRECT ? Shape::STAGES : 2;
     constexpr int MI = Shape::MI, NI = Shape::NI, THREADS = Shape::THREADS, STEPS = BK / 32;
-    constexpr bool PERSISTENT = Shape::PERSISTENT && DIRECT, PLAIN = !AK || BK_;
+    constexpr bool PERSISTENT = Shape::PERSISTENT && DIRECT, LAYER = Problem::EPILOGUE == kEpilogueLayer;
+    constexpr bool PLAIN = LAYER && (!AK || BK_);
     using TileA = OperandTile<AK, BM, S>;
     using TileB = OperandTile<BK_, BN, S>;
     constexpr int RING = 5;
@@ -764,14 +782,14 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
     // rows 347 -> 288, but dA of 512 rows 248 -> 269, and calls of up to 20 us 0.4 to 2 us more.
     const uint32_t tiles = tiles_m * tiles_n, total = tiles * grid_y;
     auto work_of = [&](uint32_t id) {
-        return linear_work<AK, BK_, BM, BN>(problem_again(), id % tiles, tiles_m, tiles_n, id / tiles);
+        return linear_work<AK, BK_, BM, BN>(problem_again<Problem>(), id % tiles, tiles_m, tiles_n, id / tiles);
     };
     // The share of tile number id, or the next that exists (grouped rows may need fewer tiles than were counted for
     // them); in the last round, a slice of a tile.
     bool sliced = false;
     auto find_work = [&](uint32_t& id, LinearWork& w) {
         if constexpr (PERSISTENT) {
-            const LinearProblem p = problem_again();
+            const Problem p = problem_again<Problem>();
             if (p.tail || p.axis == kGroupRows) {
                 // (the tiles there are, so that the last ones are the last round)
                 const uint32_t real_m = real_row_tiles(p, BM, tiles_m);
@@ -808,7 +826,7 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
     // The first copies of a share.
     auto start_copies = [&](const LinearWork& w) {
         if constexpr (DIRECT) {
-            const LinearProblem p = problem_again();
+            const Problem p = problem_again<Problem>();
             const int lane = afresh(every_lane), wave = afresh_uniform(every_wave);
             CA copy_a(w.A, p.lda, w.m_end - w.m0, w.L, wave, lane);
             CB copy_b(w.B, p.ldb, p.C - w.n0, w.L, wave, lane);
@@ -846,7 +864,7 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
         };
 
         if constexpr (DIRECT) {
-            const LinearProblem p = problem_again();
+            const Problem p = problem_again<Problem>();
             CA copy_a(w.A, p.lda, w.m_end - w.m0, w.L, wave, lane);
             CB copy_b(w.B, p.ldb, p.C - w.n0, w.L, wave, lane);
 #pragma unroll
@@ -914,7 +932,7 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
         } else {
             // Two stages; the loads of tile t+1 are issued before the
             // multiply of tile t and stored to LDS after it.
-            const LinearProblem p = problem_again();
+            const Problem p = problem_again<Problem>();
             OperandLoad<AK, BM, S, THREADS> load_a(w.A, p.lda, w.m_end - w.m0);
             OperandLoad<BK_, BN, S, THREADS> load_b(w.B, p.ldb, p.C - w.n0);
             if (T > 0) {
@@ -965,7 +983,14 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
         // row's lanes cover whole 128-byte lines of a 16-bit output (64-byte pieces cost the stores up to a fifth more
         // time).  A tile wholly inside the matrix takes a copy of the
         // code without masks.
-        const LinearProblem p = problem_again();
+        const Problem p = problem_again<Problem>();
+        if constexpr (Problem::EPILOGUE == kEpilogueRows) {
+            p.template rows_epilogue<MI, NI>(acc, scalar(w.m0 + wm0), w.m_end, scalar(w.n0 + wn0), Shape::WN,
+                                             afresh(every_lane));
+            if (!more) return;
+            w = then;
+            continue;
+        }
         constexpr int LANES = Shape::WN / 8, ROWS = kWave / LANES, PARTS = BR / ROWS;
         const int out_lane = afresh(every_lane), r = out_lane / LANES, c = out_lane % LANES * 8;
         float* const staged = reinterpret_cast<float*>(lds) + (PERSISTENT ? 4 * TileA::stage_words : 0) + wave * BLOCK_WORDS;
@@ -983,7 +1008,9 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
                 return !w.partial && inside(m) ? residual_reads(p.ep, base(m), lane_at, left) : Row8{};
             };
             Row8 bias{};
-            if (!PLAIN && !w.partial && left > 0) bias = bias_reads(p.ep, group * p.ep.bias_group + tile_col + c, left);
+            if (LAYER && !PLAIN && !w.partial && left > 0) bias = bias_reads(p.ep, group * p.ep.bias_group + tile_col + c, left);
+            EpilogueRows<Problem> values;
+            if constexpr (!LAYER) values.load(p, tile_row, w.m_end, Shape::WM, out_lane);
             // The residual is read for a group of parts at a time: loads and stores complete in order, so a load
             // waits for every store before it.
             constexpr int ALL = Shape::WM / ROWS, GROUP = WHOLE ? (ALL < 4 ? ALL : 4) : 1;
@@ -996,7 +1023,7 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
                 asm volatile("" : "+v"(bias.w));
                 Row8 residual[GROUP];
 #pragma unroll
-                for (int u = 0; u < GROUP; ++u) residual[u] = PLAIN ? Row8{} : read_residual(m0 + u, lane_at);
+                for (int u = 0; u < GROUP; ++u) residual[u] = PLAIN || !LAYER ? Row8{} : read_residual(m0 + u, lane_at);
                 static_for<GROUP>([&](auto U_) {
                     constexpr int U = decltype(U_)::value;
                     const int m = m0 + U;
@@ -1022,11 +1049,14 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
 #pragma unroll
                         for (int e = 0; e < 4; ++e) z[4 * g + e] = x[e];
                     }
+                    if constexpr (!LAYER) values.of_row(m * ROWS, r);
                     if (inside(m)) {
                         if (w.partial)
                             store8(w.partial + (tile_row + m * ROWS + r) * w.partial_ld + tile_col + c, z, left);
-                        else
+                        else if constexpr (LAYER)
                             epilogue8<TYPE, PLAIN>(p.ep, bias, residual[U], base(m), lane_at, left, z);
+                        else
+                            values.template finish<TYPE>(p, base(m), lane_at, tile_row + m * ROWS + r, tile_col + c, left, z);
                     }
                 });
             }
@@ -1047,8 +1077,8 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
 // launch and two dependent loads.
 constexpr int kJoinThreads = 256, kJoinGroups = kJoinThreads / 4;  // column groups per workgroup
 
-template <int TYPE>
-__global__ __launch_bounds__(kJoinThreads) void linear_join_kernel(LinearProblem p) {
+template <int TYPE, class Problem = LinearProblem>
+__global__ __launch_bounds__(kJoinThreads) void linear_join_kernel(Problem p) {
     const int lane = threadIdx.x % kWave, slice0 = lane / 16;
     const int64_t row_groups = (p.C + 7) / 8, total = p.R * row_groups, stride = p.R * p.C;
     for (int64_t first = (int64_t)blockIdx.x * kJoinGroups + threadIdx.x / kWave * 16; first < total;
@@ -1060,7 +1090,7 @@ __global__ __launch_bounds__(kJoinThreads) void linear_join_kernel(LinearProblem
         const EpilogueBase base = epilogue_base(p.ep, 0, row, col);
         const EpilogueLane none{0, 0, 0};
         Row8 bias{}, residual{};
-        if (slice0 == 0) {
+        if (Problem::EPILOGUE == kEpilogueLayer && slice0 == 0) {
             bias = bias_reads(p.ep, col, left);
             residual = residual_reads(p.ep, base, none, left);
         }
@@ -1077,7 +1107,12 @@ __global__ __launch_bounds__(kJoinThreads) void linear_join_kernel(LinearProblem
             z[e] += __shfl_xor(z[e], 16);
             z[e] += __shfl_xor(z[e], 32);
         }
-        if (slice0 == 0 && left > 0) epilogue8<TYPE>(p.ep, bias, residual, base, none, left, z);
+        if (slice0 == 0 && left > 0) {
+            if constexpr (Problem::EPILOGUE == kEpilogueLayer)
+                epilogue8<TYPE>(p.ep, bias, residual, base, none, left, z);
+            else
+                EpilogueRows<Problem>{}.template finish<TYPE>(p, base, none, row, col, left, z);
+        }
     }
 }
 
@@ -1085,9 +1120,8 @@ __global__ __launch_bounds__(kJoinThreads) void linear_join_kernel(LinearProblem
 // arguments) in ascending order: workgroup (j, part) sums 32 rows of its j-th
 // tile.  17 us after 16384 rows in 8 groups by 4096 (64 MiB of partial sums,
 // most of them still in the last-level cache).
-template <int TYPE, int BM, int BN>
-__global__ __launch_bounds__(256) void linear_tail_kernel(LinearProblem p, uint32_t tiles_m, uint32_t tiles_n,
-                                                          uint32_t grid) {
+template <int TYPE, int BM, int BN, class Problem = LinearProblem>
+__global__ __launch_bounds__(256) void linear_tail_kernel(Problem p, uint32_t tiles_m, uint32_t tiles_n, uint32_t grid) {
     const uint32_t real_m = real_row_tiles(p, BM, tiles_m);
     const TailSplit t = tail_split(p, real_m * tiles_n, grid);
     if (blockIdx.x >= t.left) return;
@@ -1100,8 +1134,11 @@ __global__ __launch_bounds__(256) void linear_tail_kernel(LinearProblem p, uint3
         if (row >= w.m_end || left <= 0) continue;
         const EpilogueBase base = epilogue_base(p.ep, w.group, row, col);
         const EpilogueLane none{0, 0, 0};
-        const Row8 bias = bias_reads(p.ep, w.group * p.ep.bias_group + col, left),
-                   residual = residual_reads(p.ep, base, none, left);
+        Row8 bias{}, residual{};
+        if constexpr (Problem::EPILOGUE == kEpilogueLayer) {
+            bias = bias_reads(p.ep, w.group * p.ep.bias_group + col, left);
+            residual = residual_reads(p.ep, base, none, left);
+        }
         float z[8] = {};
 #pragma unroll 4
         for (uint32_t s = 0; s < t.parts; ++s) {
@@ -1110,7 +1147,10 @@ __global__ __launch_bounds__(256) void linear_tail_kernel(LinearProblem p, uint3
 #pragma unroll
             for (int e = 0; e < 8; ++e) z[e] += more[e];
         }
-        epilogue8<TYPE>(p.ep, bias, residual, base, none, left, z);
+        if constexpr (Problem::EPILOGUE == kEpilogueLayer)
+            epilogue8<TYPE>(p.ep, bias, residual, base, none, left, z);
+        else
+            EpilogueRows<Problem>{}.template finish<TYPE>(p, base, none, row, col, left, z);
     }
 }
 

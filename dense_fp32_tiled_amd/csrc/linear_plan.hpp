@@ -201,4 +201,8 @@ struct Space {
     }
 };
 
+inline bool workspace_ok(int64_t need, const void* workspace, int64_t bytes) {
+    return need == 0 || (workspace && bytes >= need && ((uintptr_t)workspace & 15) == 0);
+}
+
 }  // namespace dft

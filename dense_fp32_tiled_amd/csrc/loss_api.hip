@@ -1,0 +1,423 @@
+// loss_api.hip -- the C ABI of the cross entropy of a product over a
+// vocabulary, and of its gradients (include/dense_fp32_tiled.h): argument
+// checks, the pieces of the vocabulary, and the launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <stdint.h>
+
+#include "dense_fp32_tiled.h"
+#include "host_checks.hpp"
+#include "linear_plan.hpp"
+#include "loss_kernels.hpp"
+
+namespace {
+
+using namespace dft;
+
+__global__ __launch_bounds__(kLossJoinThreads) void loss_join_kernel(LossRowsProblem p, int64_t slots, int rows,
+                                                                     float* loss, float* lse) {
+    loss_join(p, slots, rows, loss, lse);
+}
+__global__ __launch_bounds__(kLossPrepareThreads) void loss_prepare_kernel(LossPrepare p) { loss_prepare(p); }
+__global__ __launch_bounds__(256) void loss_pack_kernel(LossPack p) { loss_pack(p); }
+
+template <class... Args>
+int launch(void (*kernel)(Args...), int64_t blocks, int threads, hipStream_t stream, Args... values) {
+    void* args[] = {&values...};
+    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((unsigned)blocks), dim3((unsigned)threads), args, 0,
+                           stream) == hipSuccess
+               ? GEMM_OK
+               : GEMM_ERR_HIP;
+}
+int status(hipError_t e) { return e == hipSuccess ? GEMM_OK : GEMM_ERR_HIP; }
+
+bool known_target(int t) { return t == GEMM_TARGET_I32 || t == GEMM_TARGET_I64; }
+int64_t target_bytes(int t) { return t == GEMM_TARGET_I64 ? 8 : 4; }
+int64_t round_up(int64_t n, int64_t to) { return ceil_div(n, to) * to; }
+
+// The rows times the width of a vocabulary's matrix as it lies in memory.
+Matrix words_matrix(const void* data, bool transposed, int64_t N, int64_t K, int64_t ld, int64_t elem) {
+    return transposed ? Matrix{data, N, K, ld, elem} : Matrix{data, K, N, ld, elem};
+}
+// Its columns [first, first + words) of the vocabulary.
+Matrix piece_of(const Matrix& b, bool transposed, int64_t first, int64_t words) {
+    Matrix m = b;
+    (transposed ? m.rows : m.cols) = words;
+    m.data = static_cast<const char*>(b.data) + first * (transposed ? b.ld : 1) * b.elem;
+    return m;
+}
+
+constexpr int64_t kMostWords = (int64_t)1 << 20;   // of a piece: dZ's pitch, whose offsets within a tile stay below 2^30
+constexpr int64_t kPieceStep = 256;                // pieces end where tiles do
+constexpr int64_t kPackedPiece = (int64_t)1 << 26;  // values of a packed piece: 128 MiB, read again from the last-level cache
+
+struct LossSizes {
+    int32_t input_type, target_type, b_transposed, variant;
+    int64_t M, N, K, piece;
+};
+template <class Args>
+LossSizes sizes_of(const Args& a) {
+    return LossSizes{a.input_type, a.target_type, a.b_transposed, a.variant, a.M, a.N, a.K, a.piece};
+}
+int check_sizes(const LossSizes& s) {
+    if (!known_type(s.input_type) || !known_target(s.target_type)) return GEMM_ERR_UNSUPPORTED;
+    if (s.b_transposed != 0 && s.b_transposed != 1) return GEMM_ERR_UNSUPPORTED;
+    if (s.variant < 0 || s.variant >= GEMM_LINEAR_COUNT) return GEMM_ERR_UNSUPPORTED;
+    if (s.M < 0 || s.N < 1 || s.K < 0 || s.M > kMaxDim || s.N > kMaxDim || s.K > kMaxDim) return GEMM_ERR_INVALID_DIM;
+    if (s.piece < 0 || s.piece % kPieceStep != 0) return GEMM_ERR_INVALID_DIM;
+    if (s.N > 0x7fffffff || s.M > 0x7fffffff || !products_ok(s.M, s.N, s.K)) return GEMM_ERR_TOO_LARGE;
+    return GEMM_OK;
+}
+
+int pack(const Matrix& from, const Matrix& to, const Targets& targets, int64_t words, hipStream_t stream) {
+    const LossPack job{static_cast<const uint16_t*>(from.data), from.rows, from.cols, from.ld,
+                       static_cast<uint16_t*>(const_cast<void*>(to.data)), to.ld, targets, words};
+    const int64_t groups = from.rows * (to.ld / 8);
+    if (groups == 0) return GEMM_OK;
+    return launch(loss_pack_kernel, std::min<int64_t>(ceil_div(groups, 256), 65536), 256, stream, job);
+}
+
+// The tile of a piece's logits: never sliced, since its epilogue needs whole sums.
+Plan logits_plan(const LossSizes& s, int64_t words, int cus) {
+    return choose(s.M, words, s.K, 1, kGroupNone, kDirect, s.variant, 1, cus);
+}
+
+void describe_logits(LinearProblem& p, const LossSizes& s, const Matrix& a, const Matrix& b, int64_t words) {
+    p.R = s.M; p.C = words; p.L = s.K;
+    p.A = static_cast<const uint16_t*>(a.data); p.lda = a.ld;
+    p.B = static_cast<const uint16_t*>(b.data); p.ldb = b.ld;
+    p.groups = 1; p.axis = kGroupNone; p.splits = 1; p.slice = s.K;
+}
+template <class Problem>
+int launch_logits(const LossSizes& s, const Problem& p, LinearTile tile, int cus, hipStream_t stream) {
+    const TileSize size = kTileSizes[tile];
+    const uint32_t m = (uint32_t)ceil_div(p.R, size.bm), n = (uint32_t)ceil_div(p.C, size.bn);
+    const bool k = s.b_transposed != 0;
+    return status(s.input_type == GEMM_INPUT_BF16 ? launch_loss_bf16(p, k, tile, m, n, 1, cus, stream)
+                                                  : launch_loss_f16(p, k, tile, m, n, 1, cus, stream));
+}
+
+// ---- forward ----------------------------------------------------------------------------
+// In the workspace, one after the other: A packed, a piece of B packed, the
+// rows' pieces, the targets' logits.
+struct ForwardPlan {
+    bool pack_a, pack_b;
+    int64_t piece, slots;
+    int width;  // columns of a slot: a wave's
+    LinearTile tile;
+    int64_t a_bytes, b_bytes, pieces_bytes, target_bytes, workspace;
+};
+int wave_columns(LinearTile tile) { return tile == kTile256 || tile == kTile128 ? 64 : 32; }
+
+int plan_forward(const gemm_cross_entropy_args& a, const Matrix& A, const Matrix& B, int cus, ForwardPlan* plan) {
+    const LossSizes s = sizes_of(a);
+    ForwardPlan& f = *plan;
+    const bool work = s.K > 0;
+    f.pack_a = work && !whole_rows(A);
+    f.pack_b = work && !whole_rows(B);
+    // (B as it is: all of it at once)
+    f.piece = s.piece > 0 ? s.piece : f.pack_b ? std::max(kPackedPiece / s.K / kPieceStep, (int64_t)1) * kPieceStep : s.N;
+    f.piece = std::min(f.piece, s.N);
+    const Matrix a_read = f.pack_a ? packed(A) : A;
+    const Matrix b_piece = piece_of(B, s.b_transposed, 0, f.piece), b_read = f.pack_b ? packed(b_piece) : b_piece;
+    if (!copies_fit(kTile256, a_read, true, b_read, s.b_transposed)) return GEMM_ERR_TOO_LARGE;
+    const Plan logits = logits_plan(s, f.piece, cus);
+    if (!logits.found()) return GEMM_ERR_TOO_LARGE;
+    f.tile = logits.tile;
+    f.width = wave_columns(f.tile);
+    // (whole tiles of columns: the last one's waves past the vocabulary leave empty slots)
+    f.slots = round_up(s.N, kTileSizes[f.tile].bn) / f.width;
+    f.a_bytes = f.pack_a ? packed_bytes(A) : 0;
+    f.b_bytes = f.pack_b ? packed_bytes(b_piece) : 0;
+    f.pieces_bytes = round_up(f.slots * s.M * (int64_t)sizeof(RowPiece), 256);
+    f.target_bytes = round_up(s.M * 4, 256);
+    f.workspace = f.a_bytes + f.b_bytes + f.pieces_bytes + f.target_bytes;
+    return GEMM_OK;
+}
+
+int check_forward(const gemm_cross_entropy_args& a, Matrix* A, Matrix* B) {
+    const int st = check_sizes(sizes_of(a));
+    if (st != GEMM_OK) return st;
+    if (a.workspace_bytes < 0) return GEMM_ERR_WORKSPACE;
+    *A = Matrix{a.A, a.M, a.K, a.lda, 2};
+    *B = words_matrix(a.B, a.b_transposed, a.N, a.K, a.ldb, 2);
+    const auto list = [](const void* p, int64_t n, int64_t elem) { return Matrix{p, 1, n, std::max<int64_t>(n, 1), elem}; };
+    const bool work = a.M > 0;
+    const Use uses[] = {{*A, !work, false}, {*B, !work, false},
+                        {list(a.targets, a.M, target_bytes(a.target_type)), a.loss == nullptr, false},
+                        {list(a.loss, a.M, 4), true, true}, {list(a.lse, a.M, 4), !work, true},
+                        {list(a.workspace, a.workspace_bytes, 1), true, true}};
+    return check_matrices(uses, 6);
+}
+
+// Rows of a join's workgroup: as many as leave a workgroup for every CU.
+int join_rows(int64_t M, int cus) {
+    int rows = 32;
+    while (rows > 1 && ceil_div(M, rows) < cus) rows /= 2;
+    return rows;
+}
+
+int run_forward(const gemm_cross_entropy_args& a, hipStream_t stream) {
+    Matrix A, B;
+    int st = check_forward(a, &A, &B);
+    if (st != GEMM_OK || a.M == 0) return st;
+    int cus = 0;
+    st = current_cus(&cus);
+    if (st != GEMM_OK) return st;
+    const LossSizes s = sizes_of(a);
+    ForwardPlan f;
+    st = plan_forward(a, A, B, cus, &f);
+    if (st != GEMM_OK) return st;
+    if (!workspace_ok(f.workspace, a.workspace, a.workspace_bytes)) return GEMM_ERR_WORKSPACE;
+    Space space{static_cast<char*>(a.workspace)};
+    void* const a_space = space.take(f.a_bytes);
+    void* const b_space = space.take(f.b_bytes);
+    LossRowsProblem p{};
+    p.pieces = static_cast<RowPiece*>(space.take(f.pieces_bytes));
+    p.at_target = static_cast<float*>(space.take(f.target_bytes));
+    p.targets = Targets{a.loss ? a.targets : nullptr, a.target_type == GEMM_TARGET_I64};  // (loss alone reads them)
+    p.words = s.N;
+    if (f.pack_a) {
+        Matrix to = packed(A);
+        to.data = a_space;
+        if ((st = pack(A, to, Targets{nullptr, 0}, 0, stream)) != GEMM_OK) return st;
+        A = to;
+    }
+    for (int64_t first = 0; first < s.N; first += f.piece) {
+        const int64_t words = std::min(f.piece, s.N - first);
+        Matrix b = piece_of(B, s.b_transposed, first, words);
+        if (f.pack_b) {
+            Matrix to = packed(b);
+            to.data = b_space;
+            if ((st = pack(b, to, Targets{nullptr, 0}, 0, stream)) != GEMM_OK) return st;
+            b = to;
+        }
+        describe_logits(p, s, A, b, words);
+        p.first = first;
+        if ((st = launch_logits(s, p, f.tile, cus, stream)) != GEMM_OK) return st;
+    }
+    const int rows = join_rows(s.M, cus);
+    return launch(loss_join_kernel, ceil_div(s.M, rows), kLossJoinThreads, stream, p, f.slots, rows, a.loss, a.lse);
+}
+
+// ---- gradients ----------------------------------------------------------------------------
+// In the workspace: the rows' values and the scale, A packed (always: rows
+// without a target are zeros in it), a piece of B packed, a piece's dZ, dA's
+// sums over the pieces, and the slices of the product that runs.
+struct GradPlan {
+    bool pack_b, a_held;
+    int64_t piece;
+    LinearTile tile;
+    Plan a, b;  // the gradients' products of a whole piece
+    int64_t rows_bytes, a_bytes, b_bytes, slope_bytes, held_bytes, rest_bytes, workspace;
+};
+// Words of a piece: dZ of 512 MiB, so that a piece is many rounds of tiles and
+// dA's sums are read and written again a few times only, and for many tokens
+// still 4096 words.
+constexpr int64_t kSlopeValues = (int64_t)1 << 28, kLeastWords = 4096;
+int64_t words_at_once(int64_t M) {
+    return std::max(kSlopeValues / std::max<int64_t>(M, 1) / kPieceStep * kPieceStep, kLeastWords);
+}
+
+Plan plan_a(const LossSizes& s, int64_t words, int cus) {
+    return choose(s.M, s.K, words, 1, kGroupNone, kDirect, s.variant, 0, cus);
+}
+Plan plan_b(const LossSizes& s, int64_t words, int cus) {
+    return s.b_transposed ? choose(words, s.K, s.M, 1, kGroupNone, kDirect, s.variant, 0, cus)
+                          : choose(s.K, words, s.M, 1, kGroupNone, kDirect, s.variant, 0, cus);
+}
+// Slices of a product, of all of it or of its last round.
+int64_t rest_bytes(const Plan& plan, int64_t R, int64_t C, int64_t L, int cus) {
+    return partial_bytes(plan, R, C) + tail_bytes(plan, R, C, L, 1, kGroupNone, cus);
+}
+
+int plan_grad(const gemm_cross_entropy_grad_args& a, const Matrix& A, const Matrix& B, int cus, GradPlan* plan) {
+    const LossSizes s = sizes_of(a);
+    GradPlan& g = *plan;
+    g = GradPlan{};
+    g.pack_b = s.K > 0 && !whole_rows(B);
+    g.piece = s.piece > 0 ? s.piece : words_at_once(s.M);
+    if (s.piece == 0 && g.pack_b)  // (what is packed counts too, four times over: it is not used again)
+        g.piece = std::min(g.piece, std::max(4 * kPackedPiece / s.K / kPieceStep, (int64_t)1) * kPieceStep);
+    g.piece = std::min({g.piece, s.N, kMostWords});
+    const Matrix b_piece = piece_of(B, s.b_transposed, 0, g.piece), b_read = g.pack_b ? packed(b_piece) : b_piece;
+    const Matrix a_read = packed(A), slope{nullptr, s.M, g.piece, round_up(g.piece, 8), 2};
+    const bool kmajor = s.b_transposed != 0;
+    if (!copies_fit(kTile256, a_read, true, b_read, kmajor) || !copies_fit(kTile256, slope, true, b_read, !kmajor) ||
+        !copies_fit(kTile256, a_read, false, slope, false))
+        return GEMM_ERR_TOO_LARGE;
+    const Plan logits = logits_plan(s, g.piece, cus);
+    g.a = plan_a(s, g.piece, cus);
+    g.b = plan_b(s, g.piece, cus);
+    if (!logits.found() || !g.a.found() || !g.b.found()) return GEMM_ERR_TOO_LARGE;
+    g.tile = logits.tile;
+    g.a_held = a.dA && s.N > g.piece;
+    g.rows_bytes = round_up(s.M * (int64_t)sizeof(LossRow), 256) + 256;
+    g.a_bytes = packed_bytes(A);
+    g.b_bytes = g.pack_b ? packed_bytes(b_piece) : 0;
+    g.slope_bytes = packed_bytes(slope);
+    g.held_bytes = g.a_held ? round_up(s.M * s.K * 4, 256) : 0;
+    // (the last piece, which may be of another size, has a plan of its own)
+    const int64_t last = s.N - (s.N - 1) / g.piece * g.piece;
+    for (const int64_t words : {g.piece, last}) {
+        if (a.dA) g.rest_bytes = std::max(g.rest_bytes, rest_bytes(plan_a(s, words, cus), s.M, s.K, words, cus));
+        if (a.dB) {
+            const int64_t R = kmajor ? words : s.K, C = kmajor ? s.K : words;
+            g.rest_bytes = std::max(g.rest_bytes, rest_bytes(plan_b(s, words, cus), R, C, s.M, cus));
+        }
+    }
+    g.workspace = g.rows_bytes + g.a_bytes + g.b_bytes + g.slope_bytes + g.held_bytes + g.rest_bytes;
+    return GEMM_OK;
+}
+
+int check_grad(const gemm_cross_entropy_grad_args& a, Matrix* A, Matrix* B, Matrix* dB) {
+    const int st = check_sizes(sizes_of(a));
+    if (st != GEMM_OK) return st;
+    if (!known_output(a.a_grad_type) || !known_output(a.b_grad_type)) return GEMM_ERR_UNSUPPORTED;
+    if (a.workspace_bytes < 0) return GEMM_ERR_WORKSPACE;
+    *A = Matrix{a.A, a.M, a.K, a.lda, 2};
+    *B = words_matrix(a.B, a.b_transposed, a.N, a.K, a.ldb, 2);
+    *dB = words_matrix(a.dB, a.b_transposed, a.N, a.K, a.lddb, elem_bytes(a.b_grad_type));
+    const Matrix dA{a.dA, a.M, a.K, a.ldda, elem_bytes(a.a_grad_type)};
+    const auto list = [](const void* p, int64_t n, int64_t elem) { return Matrix{p, 1, n, std::max<int64_t>(n, 1), elem}; };
+    const bool work = a.dA || a.dB;
+    const Use uses[] = {{*A, !work, false}, {*B, !work, false},
+                        {list(a.targets, a.M, target_bytes(a.target_type)), !work, false},
+                        {list(a.lse, a.M, 4), !work, false}, {list(a.dloss, a.M, 4), !work, false}, {dA, true, true},
+                        {*dB, true, true}, {list(a.workspace, a.workspace_bytes, 1), true, true}};
+    const int bad = check_matrices(uses, 8);
+    if (bad != GEMM_OK) return bad;
+    return out_pitch_ok(dA) && out_pitch_ok(*dB) ? GEMM_OK : GEMM_ERR_TOO_LARGE;
+}
+
+template <class Problem>
+int launch_product(const LossSizes& s, Problem& p, const Plan& plan, void* rest, int cus, hipStream_t stream) {
+    const TileSize size = kTileSizes[plan.tile];
+    const uint32_t m = (uint32_t)ceil_div(p.R, size.bm), n = (uint32_t)ceil_div(p.C, size.bn);
+    p.groups = 1; p.axis = kGroupNone; p.splits = plan.splits; p.slice = plan.slice;
+    p.partial = static_cast<float*>(rest);
+    p.tail = tail_bytes(plan, p.R, p.C, p.L, 1, kGroupNone, cus) > 0 ? p.partial : nullptr;
+    const uint32_t slices = (uint32_t)plan.splits;
+    const bool k = s.b_transposed != 0;
+    return status(s.input_type == GEMM_INPUT_BF16 ? launch_loss_bf16(p, k, plan.tile, m, n, slices, cus, stream)
+                                                  : launch_loss_f16(p, k, plan.tile, m, n, slices, cus, stream));
+}
+
+int run_grad(const gemm_cross_entropy_grad_args& a, hipStream_t stream) {
+    Matrix A, B, dB;
+    int st = check_grad(a, &A, &B, &dB);
+    if (st != GEMM_OK || (!a.dA && !a.dB) || a.K == 0 || (a.M == 0 && !a.dB)) return st;
+    int cus = 0;
+    st = current_cus(&cus);
+    if (st != GEMM_OK) return st;
+    const LossSizes s = sizes_of(a);
+    GradPlan g;
+    st = plan_grad(a, A, B, cus, &g);
+    if (st != GEMM_OK) return st;
+    if (!workspace_ok(g.workspace, a.workspace, a.workspace_bytes)) return GEMM_ERR_WORKSPACE;
+    const bool kmajor = s.b_transposed != 0;
+    const Targets targets{a.targets, a.target_type == GEMM_TARGET_I64};
+    Space space{static_cast<char*>(a.workspace)};
+    char* const rows = static_cast<char*>(space.take(g.rows_bytes));
+    float* const back = reinterpret_cast<float*>(rows + g.rows_bytes - 256);
+    Matrix x = packed(A);
+    x.data = space.take(g.a_bytes);
+    void* const b_space = space.take(g.b_bytes);
+    void* const slopes = space.take(g.slope_bytes);
+    float* const held = static_cast<float*>(space.take(g.held_bytes));
+    void* const rest = space.take(g.rest_bytes);
+    const LossPrepare prepare{s.M, s.N, targets, a.lse, a.dloss, reinterpret_cast<LossRow*>(rows), back};
+    st = launch(loss_prepare_kernel, std::min<int64_t>(std::max<int64_t>(ceil_div(s.M, kLossPrepareThreads), 1), 16),
+                kLossPrepareThreads, stream, prepare);
+    if (st != GEMM_OK) return st;
+    if ((st = pack(A, x, targets, s.N, stream)) != GEMM_OK) return st;
+    for (int64_t first = 0; first < s.N; first += g.piece) {
+        const int64_t words = std::min(g.piece, s.N - first);
+        Matrix b = piece_of(B, kmajor, first, words);
+        if (g.pack_b) {
+            Matrix to = packed(b);
+            to.data = b_space;
+            if ((st = pack(b, to, Targets{nullptr, 0}, 0, stream)) != GEMM_OK) return st;
+            b = to;
+        }
+        const Matrix z{slopes, s.M, words, round_up(words, 8), 2};
+        if (s.M > 0) {
+            LossSlopeProblem p{};
+            describe_logits(p, s, x, b, words);
+            p.ep.out = slopes; p.ep.ldo = z.ld;
+            p.row = reinterpret_cast<const LossRow*>(rows);
+            p.first = first;
+            if ((st = launch_logits(s, p, g.tile, cus, stream)) != GEMM_OK) return st;
+        }
+        if (a.dB) {
+            const Matrix out = piece_of(dB, kmajor, first, words);
+            LossWordsGradProblem p{};
+            const Matrix &left = kmajor ? z : x, &right = kmajor ? x : z;
+            p.R = kmajor ? words : s.K; p.C = kmajor ? s.K : words; p.L = s.M;
+            p.A = static_cast<const uint16_t*>(left.data); p.lda = left.ld;
+            p.B = static_cast<const uint16_t*>(right.data); p.ldb = right.ld;
+            p.ep.out = const_cast<void*>(out.data); p.ep.ldo = out.ld; p.ep.out_f32 = a.b_grad_type == GEMM_OUTPUT_F32;
+            p.back = back;
+            st = launch_product(s, p, plan_b(s, words, cus), rest, cus, stream);
+            if (st != GEMM_OK) return st;
+        }
+        if (a.dA && s.M > 0) {
+            const bool last = first + words >= s.N;
+            LossTokensGradProblem p{};
+            p.R = s.M; p.C = s.K; p.L = words;
+            p.A = static_cast<const uint16_t*>(z.data); p.lda = z.ld;
+            p.B = static_cast<const uint16_t*>(b.data); p.ldb = b.ld;
+            p.before = first > 0 ? held : nullptr; p.before_ld = s.K;
+            p.back = last ? back : nullptr;
+            p.ep.out = last ? a.dA : held; p.ep.ldo = last ? a.ldda : s.K;
+            p.ep.out_f32 = !last || a.a_grad_type == GEMM_OUTPUT_F32;
+            st = launch_product(s, p, plan_a(s, words, cus), rest, cus, stream);
+            if (st != GEMM_OK) return st;
+        }
+    }
+    return GEMM_OK;
+}
+
+}  // namespace
+
+// ---- exported C ABI ---------------------------------------------------------------------
+extern "C" {
+
+int gemm_cross_entropy(const gemm_cross_entropy_args* args, void* stream) {
+    return args ? run_forward(*args, (hipStream_t)stream) : GEMM_ERR_NULL;
+}
+
+int64_t gemm_cross_entropy_workspace_bytes(const gemm_cross_entropy_args* args, int32_t num_cus) {
+    if (!args) return GEMM_ERR_NULL;
+    if (num_cus < 1) return GEMM_ERR_INVALID_DIM;
+    gemm_cross_entropy_args a = *args;
+    a.workspace = nullptr;
+    a.workspace_bytes = 0;
+    Matrix A, B;
+    int st = check_forward(a, &A, &B);
+    if (st != GEMM_OK || a.M == 0) return st;
+    ForwardPlan f;
+    st = plan_forward(a, A, B, num_cus, &f);
+    return st != GEMM_OK ? st : f.workspace;
+}
+
+int gemm_cross_entropy_grad(const gemm_cross_entropy_grad_args* args, void* stream) {
+    return args ? run_grad(*args, (hipStream_t)stream) : GEMM_ERR_NULL;
+}
+
+int64_t gemm_cross_entropy_grad_workspace_bytes(const gemm_cross_entropy_grad_args* args, int32_t num_cus) {
+    if (!args) return GEMM_ERR_NULL;
+    if (num_cus < 1) return GEMM_ERR_INVALID_DIM;
+    gemm_cross_entropy_grad_args a = *args;
+    a.workspace = nullptr;
+    a.workspace_bytes = 0;
+    Matrix A, B, dB;
+    int st = check_grad(a, &A, &B, &dB);
+    if (st != GEMM_OK || (!a.dA && !a.dB) || a.K == 0 || (a.M == 0 && !a.dB)) return st;
+    GradPlan g;
+    st = plan_grad(a, A, B, num_cus, &g);
+    return st != GEMM_OK ? st : g.workspace;
+}
+
+}  // extern "C"

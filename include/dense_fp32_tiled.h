@@ -721,6 +721,97 @@ int gemm_dropout(int value_type, int64_t rows, int64_t cols, double p, uint64_t 
                  const int64_t *step, const void *X, int64_t ldx, const void *residual, int64_t ldr, void *Y,
                  int64_t ldy, void *stream);
 
+/* ---- After the last product: cross entropy over a vocabulary ---------------------
+ * The loss of a model's last product, M tokens by N words, whose logits are
+ * never stored: with A (M x K) and B (K x N) of input_type and sums in fp32,
+ *     Z = A @ B,   lse[t] = log(sum over w of exp(Z[t][w])),   loss[t] = lse[t] - Z[t][targets[t]]
+ * and from dloss, the gradient of loss:
+ *     dZ[t][w] = (exp(Z[t][w] - lse[t]) - (w == targets[t])) * dloss[t]
+ *     dA = dZ @ B^T,   dB = A^T @ dZ
+ * The gradients compute Z again, a piece of the vocabulary at a time; a piece's
+ * dZ lies in the workspace, rounded to the input type (times the power of two
+ * that makes the largest |dloss| about 2^14, so that fp16 holds small
+ * probabilities), and dA's sums over the pieces are fp32.
+ *
+ * Conventions are those at the top of this header, and:
+ *   - A target outside [0, N) is none: the token's loss and gradients are zero,
+ *     whatever its row of A holds (its lse is computed all the same).
+ *   - b_transposed: B and dB lie as N x K, a word per row, as an embedding does.
+ *   - M == 0: dB is zero.  K == 0: loss is log N.  N is at least 1.
+ *   - An infinite or NaN logit makes its row's lse NaN, except -infinity, whose
+ *     word has no part in the row.
+ *   - `piece`: words at a time, a multiple of 256; 0: as many as dZ has in 512 MiB, 4096
+ *     at least (forward: all, or 128 MiB of packed operand at a time).
+ *     It sets the workspace and changes dA and lse by roundings only.
+ *   - Outputs overlap no operand (GEMM_ERR_ALIAS).  GEMM_ERR_TOO_LARGE: M or N above
+ *     2^31 - 1, M N, M K or K N above 2^50, pitches of dA and dB above 2^26, of A and B
+ *     (packed, a row's width) above 2^21 - 65 elements, more tiles of a piece than a
+ *     launch holds (2^22).
+ *   - Sums run in a fixed order: the same arguments and inputs give the same bits. */
+typedef enum {
+    GEMM_TARGET_I32 = 0,
+    GEMM_TARGET_I64 = 1
+} gemm_target_type;
+
+typedef struct {
+    int32_t input_type;     /* gemm_input_type of A and B */
+    int32_t target_type;    /* gemm_target_type */
+    int32_t b_transposed;   /* 0 or 1 */
+    int32_t variant;        /* gemm_linear_variant of the logits */
+    int64_t M, N, K;
+    int64_t piece;
+    const void *A;          /* M x K */
+    int64_t lda;
+    const void *B;          /* K x N, or N x K */
+    int64_t ldb;
+    const void *targets;    /* DEVICE, M values; ignored when loss is NULL */
+    float *loss;            /* M values, or NULL: lse alone */
+    float *lse;             /* M values */
+    void *workspace;        /* DEVICE, 16-byte aligned, gemm_cross_entropy_workspace_bytes */
+    int64_t workspace_bytes;
+} gemm_cross_entropy_args;
+
+/* loss and lse as above, enqueued on `stream`; the workspace is the call's
+ * until its work on `stream` has ended.  Returns a gemm_status. */
+int gemm_cross_entropy(const gemm_cross_entropy_args *args, void *stream);
+
+/* Bytes gemm_cross_entropy needs on a device with num_cus compute units: two
+ * values for every 32 or 64 words of a token, and packed operands.  Pure host
+ * call; a negative gemm_status on bad arguments. */
+int64_t gemm_cross_entropy_workspace_bytes(const gemm_cross_entropy_args *args, int32_t num_cus);
+
+typedef struct {
+    int32_t input_type;     /* of A and B */
+    int32_t target_type;
+    int32_t b_transposed;
+    int32_t variant;        /* of all products */
+    int32_t a_grad_type;    /* gemm_output_type of dA */
+    int32_t b_grad_type;    /* gemm_output_type of dB */
+    int64_t M, N, K;
+    int64_t piece;
+    const void *A;
+    int64_t lda;
+    const void *B;
+    int64_t ldb;
+    const void *targets;
+    const float *lse;       /* M values: the forward pass's */
+    const float *dloss;     /* M values */
+    void *dA;               /* M x K, or NULL: not wanted */
+    int64_t ldda;
+    void *dB;               /* as B lies, or NULL */
+    int64_t lddb;
+    void *workspace;
+    int64_t workspace_bytes;
+} gemm_cross_entropy_grad_args;
+
+/* The gradients above, enqueued on `stream`; workspace and order of sums as
+ * gemm_cross_entropy's.  Returns a gemm_status. */
+int gemm_cross_entropy_grad(const gemm_cross_entropy_grad_args *args, void *stream);
+
+/* Bytes gemm_cross_entropy_grad needs: A packed, a piece's dZ, dA's sums where
+ * there is more than one piece, packed pieces of B and the products' slices. */
+int64_t gemm_cross_entropy_grad_workspace_bytes(const gemm_cross_entropy_grad_args *args, int32_t num_cus);
+
 #ifdef __cplusplus
 }
 #endif
