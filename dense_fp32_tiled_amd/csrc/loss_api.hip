@@ -19,13 +19,22 @@ __global__ __launch_bounds__(kLossJoinThreads) void loss_join_kernel(LossRowsPro
                                                                      float* loss, float* lse) {
     loss_join(p, slots, rows, loss, lse);
 }
-__global__ __launch_bounds__(kLossPrepareThreads) void loss_prepare_kernel(LossPrepare p) { loss_prepare(p); }
-__global__ __launch_bounds__(256) void loss_pack_kernel(LossPack p) { loss_pack(p); }
+constexpr uint32_t kPrepareBlocks = 64;
+__global__ __launch_bounds__(kLossBeginThreads) void loss_begin_kernel(LossBegin p) {
+    if ((int)blockIdx.y < p.packs)
+        loss_pack(p.pack[blockIdx.y]);
+    else
+        loss_prepare(p.prepare, gridDim.x < kPrepareBlocks ? gridDim.x : kPrepareBlocks);
+}
+template <int TYPE>
+__global__ __launch_bounds__(256) void loss_fold_kernel(LossFold p) {
+    loss_fold<TYPE>(p);
+}
 
 template <class... Args>
-int launch(void (*kernel)(Args...), int64_t blocks, int threads, hipStream_t stream, Args... values) {
+int launch(void (*kernel)(Args...), dim3 blocks, int threads, hipStream_t stream, Args... values) {
     void* args[] = {&values...};
-    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((unsigned)blocks), dim3((unsigned)threads), args, 0,
+    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), blocks, dim3((unsigned)threads), args, 0,
                            stream) == hipSuccess
                ? GEMM_OK
                : GEMM_ERR_HIP;
@@ -70,12 +79,19 @@ int check_sizes(const LossSizes& s) {
     return GEMM_OK;
 }
 
-int pack(const Matrix& from, const Matrix& to, const Targets& targets, int64_t words, hipStream_t stream) {
-    const LossPack job{static_cast<const uint16_t*>(from.data), from.rows, from.cols, from.ld,
-                       static_cast<uint16_t*>(const_cast<void*>(to.data)), to.ld, targets, words};
-    const int64_t groups = from.rows * (to.ld / 8);
-    if (groups == 0) return GEMM_OK;
-    return launch(loss_pack_kernel, std::min<int64_t>(ceil_div(groups, 256), 65536), 256, stream, job);
+LossPack pack_job(const Matrix& from, const Matrix& to, int32_t copies, const Targets& targets, int64_t words) {
+    return LossPack{static_cast<const uint16_t*>(from.data), from.rows, from.cols, from.ld,
+                    static_cast<uint16_t*>(const_cast<void*>(to.data)), to.ld, copies, targets, words};
+}
+// Copies, and the rows' values if they are wanted.
+int begin(const LossBegin& jobs, bool prepare, hipStream_t stream) {
+    if (jobs.packs == 0 && !prepare) return GEMM_OK;
+    int64_t most = 1;
+    for (int i = 0; i < jobs.packs; ++i) most = std::max(most, jobs.pack[i].copies * jobs.pack[i].rows * (jobs.pack[i].ldd / 8));
+    if (prepare) most = std::max(most, std::min<int64_t>(jobs.prepare.rows, kPrepareBlocks * kLossBeginThreads));
+    return launch(loss_begin_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(most, kLossBeginThreads), 65536),
+                                          (unsigned)jobs.packs + (prepare ? 1 : 0)),
+                  kLossBeginThreads, stream, jobs);
 }
 
 // The tile of a piece's logits: never sliced, since its epilogue needs whole sums.
@@ -151,10 +167,11 @@ int check_forward(const gemm_cross_entropy_args& a, Matrix* A, Matrix* B) {
     return check_matrices(uses, 6);
 }
 
-// Rows of a join's workgroup: as many as leave a workgroup for every CU.
-int join_rows(int64_t M, int cus) {
+// Rows of a join's workgroup, whose pieces lie together: as many as leave a
+// workgroup for every CU, or four pieces for every thread.
+int join_rows(int64_t M, int64_t slots, int cus) {
     int rows = 32;
-    while (rows > 1 && ceil_div(M, rows) < cus) rows /= 2;
+    while (rows > 1 && ceil_div(M, rows) < cus && slots * rows > 4 * kLossJoinThreads) rows /= 2;
     return rows;
 }
 
@@ -178,10 +195,12 @@ int run_forward(const gemm_cross_entropy_args& a, hipStream_t stream) {
     p.at_target = static_cast<float*>(space.take(f.target_bytes));
     p.targets = Targets{a.loss ? a.targets : nullptr, a.target_type == GEMM_TARGET_I64};  // (loss alone reads them)
     p.words = s.N;
+    const Targets every{nullptr, 0};
+    LossBegin jobs{};
     if (f.pack_a) {
         Matrix to = packed(A);
         to.data = a_space;
-        if ((st = pack(A, to, Targets{nullptr, 0}, 0, stream)) != GEMM_OK) return st;
+        jobs.pack[jobs.packs++] = pack_job(A, to, 1, every, 0);
         A = to;
     }
     for (int64_t first = 0; first < s.N; first += f.piece) {
@@ -190,15 +209,17 @@ int run_forward(const gemm_cross_entropy_args& a, hipStream_t stream) {
         if (f.pack_b) {
             Matrix to = packed(b);
             to.data = b_space;
-            if ((st = pack(b, to, Targets{nullptr, 0}, 0, stream)) != GEMM_OK) return st;
+            jobs.pack[jobs.packs++] = pack_job(b, to, 1, every, 0);
             b = to;
         }
+        if ((st = begin(jobs, false, stream)) != GEMM_OK) return st;
+        jobs.packs = 0;
         describe_logits(p, s, A, b, words);
         p.first = first;
         if ((st = launch_logits(s, p, f.tile, cus, stream)) != GEMM_OK) return st;
     }
-    const int rows = join_rows(s.M, cus);
-    return launch(loss_join_kernel, ceil_div(s.M, rows), kLossJoinThreads, stream, p, f.slots, rows, a.loss, a.lse);
+    const int rows = join_rows(s.M, f.slots, cus);
+    return launch(loss_join_kernel, dim3((unsigned)ceil_div(s.M, rows)), kLossJoinThreads, stream, p, f.slots, rows, a.loss, a.lse);
 }
 
 // ---- gradients ----------------------------------------------------------------------------
@@ -207,6 +228,8 @@ int run_forward(const gemm_cross_entropy_args& a, hipStream_t stream) {
 // sums over the pieces, and the slices of the product that runs.
 struct GradPlan {
     bool pack_b, a_held;
+    int parts;      // dZ's: 2 for few tokens
+    int64_t rows;   // of dZ: tokens times parts
     int64_t piece;
     LinearTile tile;
     Plan a, b;  // the gradients' products of a whole piece
@@ -220,12 +243,14 @@ int64_t words_at_once(int64_t M) {
     return std::max(kSlopeValues / std::max<int64_t>(M, 1) / kPieceStep * kPieceStep, kLeastWords);
 }
 
+int parts_of(const LossSizes& s) { return s.M <= kSplitTokens ? 2 : 1; }
 Plan plan_a(const LossSizes& s, int64_t words, int cus) {
-    return choose(s.M, s.K, words, 1, kGroupNone, kDirect, s.variant, 0, cus);
+    return choose(parts_of(s) * s.M, s.K, words, 1, kGroupNone, kDirect, s.variant, 0, cus);
 }
 Plan plan_b(const LossSizes& s, int64_t words, int cus) {
-    return s.b_transposed ? choose(words, s.K, s.M, 1, kGroupNone, kDirect, s.variant, 0, cus)
-                          : choose(s.K, words, s.M, 1, kGroupNone, kDirect, s.variant, 0, cus);
+    const int64_t rows = parts_of(s) * s.M;
+    return s.b_transposed ? choose(words, s.K, rows, 1, kGroupNone, kDirect, s.variant, 0, cus)
+                          : choose(s.K, words, rows, 1, kGroupNone, kDirect, s.variant, 0, cus);
 }
 // Slices of a product, of all of it or of its last round.
 int64_t rest_bytes(const Plan& plan, int64_t R, int64_t C, int64_t L, int cus) {
@@ -236,13 +261,17 @@ int plan_grad(const gemm_cross_entropy_grad_args& a, const Matrix& A, const Matr
     const LossSizes s = sizes_of(a);
     GradPlan& g = *plan;
     g = GradPlan{};
+    g.parts = parts_of(s);
+    g.rows = g.parts * s.M;
     g.pack_b = s.K > 0 && !whole_rows(B);
     g.piece = s.piece > 0 ? s.piece : words_at_once(s.M);
     if (s.piece == 0 && g.pack_b)  // (what is packed counts too, four times over: it is not used again)
         g.piece = std::min(g.piece, std::max(4 * kPackedPiece / s.K / kPieceStep, (int64_t)1) * kPieceStep);
     g.piece = std::min({g.piece, s.N, kMostWords});
     const Matrix b_piece = piece_of(B, s.b_transposed, 0, g.piece), b_read = g.pack_b ? packed(b_piece) : b_piece;
-    const Matrix a_read = packed(A), slope{nullptr, s.M, g.piece, round_up(g.piece, 8), 2};
+    Matrix a_read = packed(A);
+    a_read.rows = g.rows;
+    const Matrix slope{nullptr, g.rows, g.piece, round_up(g.piece, 8), 2};
     const bool kmajor = s.b_transposed != 0;
     if (!copies_fit(kTile256, a_read, true, b_read, kmajor) || !copies_fit(kTile256, slope, true, b_read, !kmajor) ||
         !copies_fit(kTile256, a_read, false, slope, false))
@@ -252,19 +281,19 @@ int plan_grad(const gemm_cross_entropy_grad_args& a, const Matrix& A, const Matr
     g.b = plan_b(s, g.piece, cus);
     if (!logits.found() || !g.a.found() || !g.b.found()) return GEMM_ERR_TOO_LARGE;
     g.tile = logits.tile;
-    g.a_held = a.dA && s.N > g.piece;
+    g.a_held = a.dA && (s.N > g.piece || g.parts > 1);
     g.rows_bytes = round_up(s.M * (int64_t)sizeof(LossRow), 256) + 256;
-    g.a_bytes = packed_bytes(A);
+    g.a_bytes = packed_bytes(a_read);
     g.b_bytes = g.pack_b ? packed_bytes(b_piece) : 0;
     g.slope_bytes = packed_bytes(slope);
-    g.held_bytes = g.a_held ? round_up(s.M * s.K * 4, 256) : 0;
+    g.held_bytes = g.a_held ? round_up(g.rows * s.K * 4, 256) : 0;
     // (the last piece, which may be of another size, has a plan of its own)
     const int64_t last = s.N - (s.N - 1) / g.piece * g.piece;
     for (const int64_t words : {g.piece, last}) {
-        if (a.dA) g.rest_bytes = std::max(g.rest_bytes, rest_bytes(plan_a(s, words, cus), s.M, s.K, words, cus));
+        if (a.dA) g.rest_bytes = std::max(g.rest_bytes, rest_bytes(plan_a(s, words, cus), g.rows, s.K, words, cus));
         if (a.dB) {
             const int64_t R = kmajor ? words : s.K, C = kmajor ? s.K : words;
-            g.rest_bytes = std::max(g.rest_bytes, rest_bytes(plan_b(s, words, cus), R, C, s.M, cus));
+            g.rest_bytes = std::max(g.rest_bytes, rest_bytes(plan_b(s, words, cus), R, C, g.rows, cus));
         }
     }
     g.workspace = g.rows_bytes + g.a_bytes + g.b_bytes + g.slope_bytes + g.held_bytes + g.rest_bytes;
@@ -327,34 +356,36 @@ int run_grad(const gemm_cross_entropy_grad_args& a, hipStream_t stream) {
     void* const slopes = space.take(g.slope_bytes);
     float* const held = static_cast<float*>(space.take(g.held_bytes));
     void* const rest = space.take(g.rest_bytes);
-    const LossPrepare prepare{s.M, s.N, targets, a.lse, a.dloss, reinterpret_cast<LossRow*>(rows), back};
-    st = launch(loss_prepare_kernel, std::min<int64_t>(std::max<int64_t>(ceil_div(s.M, kLossPrepareThreads), 1), 16),
-                kLossPrepareThreads, stream, prepare);
-    if (st != GEMM_OK) return st;
-    if ((st = pack(A, x, targets, s.N, stream)) != GEMM_OK) return st;
+    LossBegin jobs{};
+    jobs.prepare = LossPrepare{s.M, s.N, targets, a.lse, a.dloss, reinterpret_cast<LossRow*>(rows), back};
+    jobs.pack[jobs.packs++] = pack_job(A, x, g.parts, targets, s.N);
+    x.rows = g.rows;
     for (int64_t first = 0; first < s.N; first += g.piece) {
         const int64_t words = std::min(g.piece, s.N - first);
         Matrix b = piece_of(B, kmajor, first, words);
         if (g.pack_b) {
             Matrix to = packed(b);
             to.data = b_space;
-            if ((st = pack(b, to, Targets{nullptr, 0}, 0, stream)) != GEMM_OK) return st;
+            jobs.pack[jobs.packs++] = pack_job(b, to, 1, Targets{nullptr, 0}, 0);
             b = to;
         }
-        const Matrix z{slopes, s.M, words, round_up(words, 8), 2};
+        if ((st = begin(jobs, first == 0, stream)) != GEMM_OK) return st;
+        jobs.packs = 0;
+        const Matrix z{slopes, g.rows, words, round_up(words, 8), 2};
         if (s.M > 0) {
             LossSlopeProblem p{};
             describe_logits(p, s, x, b, words);
             p.ep.out = slopes; p.ep.ldo = z.ld;
             p.row = reinterpret_cast<const LossRow*>(rows);
             p.first = first;
+            p.rest = g.parts > 1 ? s.M * z.ld * 2 : 0;
             if ((st = launch_logits(s, p, g.tile, cus, stream)) != GEMM_OK) return st;
         }
         if (a.dB) {
             const Matrix out = piece_of(dB, kmajor, first, words);
             LossWordsGradProblem p{};
             const Matrix &left = kmajor ? z : x, &right = kmajor ? x : z;
-            p.R = kmajor ? words : s.K; p.C = kmajor ? s.K : words; p.L = s.M;
+            p.R = kmajor ? words : s.K; p.C = kmajor ? s.K : words; p.L = g.rows;
             p.A = static_cast<const uint16_t*>(left.data); p.lda = left.ld;
             p.B = static_cast<const uint16_t*>(right.data); p.ldb = right.ld;
             p.ep.out = const_cast<void*>(out.data); p.ep.ldo = out.ld; p.ep.out_f32 = a.b_grad_type == GEMM_OUTPUT_F32;
@@ -363,9 +394,9 @@ int run_grad(const gemm_cross_entropy_grad_args& a, hipStream_t stream) {
             if (st != GEMM_OK) return st;
         }
         if (a.dA && s.M > 0) {
-            const bool last = first + words >= s.N;
+            const bool last = first + words >= s.N && g.parts == 1;
             LossTokensGradProblem p{};
-            p.R = s.M; p.C = s.K; p.L = words;
+            p.R = g.rows; p.C = s.K; p.L = words;
             p.A = static_cast<const uint16_t*>(z.data); p.lda = z.ld;
             p.B = static_cast<const uint16_t*>(b.data); p.ldb = b.ld;
             p.before = first > 0 ? held : nullptr; p.before_ld = s.K;
@@ -376,7 +407,11 @@ int run_grad(const gemm_cross_entropy_grad_args& a, hipStream_t stream) {
             if (st != GEMM_OK) return st;
         }
     }
-    return GEMM_OK;
+    if (!a.dA || s.M == 0 || g.parts == 1) return GEMM_OK;
+    const LossFold fold{s.M, s.K, held, back, a.dA, a.ldda, a.a_grad_type == GEMM_OUTPUT_F32};
+    const dim3 blocks((unsigned)ceil_div(s.M * ceil_div(s.K, 8), 256));
+    return s.input_type == GEMM_INPUT_BF16 ? launch(loss_fold_kernel<kInputBf16>, blocks, 256, stream, fold)
+                                           : launch(loss_fold_kernel<kInputF16>, blocks, 256, stream, fold);
 }
 
 }  // namespace

@@ -49,6 +49,21 @@ __device__ inline RowPiece join(const RowPiece& a, const RowPiece& b) {
     return RowPiece{most, a.sum * exp_below(a.most, most) + b.sum * exp_below(b.most, most)};
 }
 
+// One value of the four lanes l % 16, 16 + l % 16, ... that hold a row's
+// columns, the same in all of them: a swap puts the odd rows of 16 (then the
+// upper half) of one copy into the even rows (the lower half) of the other.
+template <class Op>
+__device__ inline float over_columns(float x, Op op) {
+    const uint32_t bits = __builtin_bit_cast(uint32_t, x);
+    const auto rows = __builtin_amdgcn_permlane16_swap(bits, bits, false, false);
+    // (into variables first: a bit cast of a vector's element takes the vector's first)
+    const uint32_t even = rows[0], odd = rows[1];
+    const uint32_t two = __builtin_bit_cast(uint32_t, op(__builtin_bit_cast(float, even), __builtin_bit_cast(float, odd)));
+    const auto halves = __builtin_amdgcn_permlane32_swap(two, two, false, false);
+    const uint32_t low = halves[0], high = halves[1];
+    return op(__builtin_bit_cast(float, low), __builtin_bit_cast(float, high));
+}
+
 struct LossRowsProblem : LinearProblem {
     static constexpr int EPILOGUE = kEpilogueRows;
     Targets targets;
@@ -56,61 +71,82 @@ struct LossRowsProblem : LinearProblem {
     RowPiece* pieces;      // a wave's columns of row r, slot s at pieces + s * R + r: rows of a slot lie together
     float* at_target;      // the target's logit of each row that has one
 
-    // Block i of a wave's results: row lane % 16, columns 16 j + 4 (lane / 16) + v.
+    // Block i of a wave's results: row lane % 16, columns 16 j + 4 (lane / 16) + v.  Nothing overlaps this arithmetic
+    // (65536 logits a tile: a subtraction, a product, an exp2 and an addition of each), so what is rare stands in
+    // branches: masks in tiles at the vocabulary's end, the search for a target where a row has one here.
     template <int MI, int NI>
     __device__ void rows_epilogue(floatx4 (&z)[MI][NI], int64_t row0, int64_t row_end, int64_t col0, int width,
                                   int lane) const {
         const int64_t slot = (first + col0) / width;
         const int left = C - col0 >= 16 * NI ? 16 * NI : C > col0 ? (int)(C - col0) : 0;  // columns inside
         const int c = 4 * (lane / 16);
+        int goal[MI];  // the row's target within the wave's columns, if 0 to left - 1
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             const int64_t row = row0 + 16 * i + lane % 16;
-            const bool inside = row < row_end;
-            const int target = inside ? targets.column(row, words) : -1;
-            const int goal = target < 0 ? -1 : (int)(target - first - col0);  // within the wave's columns, if 0 to left - 1
-            if (left < 16 * NI) {
+            const int target = row < row_end ? targets.column(row, words) : -1;
+            const int64_t at = target - first - col0;
+            goal[i] = target >= 0 && at >= 0 && at < left ? (int)at : -1;
+        }
+        if (left < 16 * NI) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int j = 0; j < NI; ++j)
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
                         if (16 * j + c + v >= left) z[i][j][v] = -__builtin_inff();
-            }
-            RowPiece p{z[i][0][0], 0.0f};
+        }
+        // (all blocks' maxima, then all sums: each step has MI independent chains to overlap)
+        float most[MI], sum[MI];
+        bool any = false;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            most[i] = z[i][0][0];
 #pragma unroll
             for (int j = 0; j < NI; ++j)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) p.most = fmaxf(p.most, z[i][j][v]);
-            p.most = fmaxf(p.most, __shfl_xor(p.most, 16));
-            p.most = fmaxf(p.most, __shfl_xor(p.most, 32));
-            float hit = 0.0f;
-            bool found = false;
+                for (int v = 0; v < 4; ++v) most[i] = fmaxf(most[i], z[i][j][v]);
+            any = any || goal[i] >= 0;
+        }
+#pragma unroll
+        for (int i = 0; i < MI; ++i) most[i] = over_columns(most[i], [](float x, float y) { return fmaxf(x, y); });
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const float from = most[i] == -__builtin_inff() ? 0.0f : most[i];
+            float part[4] = {};
 #pragma unroll
             for (int j = 0; j < NI; ++j)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    p.sum += exp_below(z[i][j][v], p.most);
-                    if (goal == 16 * j + c + v) {
-                        hit = z[i][j][v];
-                        found = true;
-                    }
-                }
-            p.sum += __shfl_xor(p.sum, 16);
-            p.sum += __shfl_xor(p.sum, 32);
-            if (inside && lane < 16) pieces[slot * R + row] = p;
-            if (found && goal < left) at_target[row] = hit;
+                for (int v = 0; v < 4; ++v) part[v] += __builtin_amdgcn_exp2f((z[i][j][v] - from) * kLog2e);
+            sum[i] = (part[0] + part[1]) + (part[2] + part[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            sum[i] = over_columns(sum[i], [](float x, float y) { return x + y; });
+            const int64_t row = row0 + 16 * i + lane % 16;
+            if (row < row_end && lane < 16) pieces[slot * R + row] = RowPiece{most[i], sum[i]};
+        }
+        if (__ballot(any)) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (goal[i] == 16 * j + c + v) at_target[row0 + 16 * i + lane % 16] = z[i][j][v];
         }
     }
 };
 
 // lse and loss of `rows` rows (a power of two up to 32) per workgroup: the
-// row's slots in strides, each thread's joined in ascending order, the
-// threads' by halves.  loss = (most - target's logit) + log(sum): the
+// row's slots in strides, each thread's joined in ascending order, then a
+// wave's by halves and the waves' in ascending order.  loss = (most - target's logit) + log(sum): the
 // difference of two logits and a logarithm of at least one, so that a small
 // loss keeps its digits; lse itself is rounded once more.
 constexpr int kLossJoinThreads = 1024;
 __device__ inline void loss_join(const LossRowsProblem& p, int64_t slots, int rows, float* loss, float* lse) {
-    __shared__ RowPiece shared[kLossJoinThreads];
+    __shared__ RowPiece shared[kLossJoinThreads / kWave][32];
     const int r = threadIdx.x & (rows - 1), first = threadIdx.x / rows, strides = kLossJoinThreads / rows;
     const int64_t row = (int64_t)blockIdx.x * rows + r;
     RowPiece all{-__builtin_inff(), 0.0f};
@@ -126,13 +162,13 @@ __device__ inline void loss_join(const LossRowsProblem& p, int64_t slots, int ro
         }
         for (; s < slots; s += strides) all = join(all, from[s * p.R]);
     }
-    for (int half = strides / 2; half > 0; half /= 2) {
-        shared[threadIdx.x] = all;
-        __syncthreads();
-        if (first < half) all = join(all, shared[threadIdx.x + half * rows]);
-        __syncthreads();
-    }
-    if (first == 0 && row < p.R) {
+    for (int d = rows; d < kWave; d *= 2)
+        all = join(all, RowPiece{__shfl_xor(all.most, d), __shfl_xor(all.sum, d)});
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    if (lane < rows) shared[wave][lane] = all;
+    __syncthreads();
+    if (wave == 0 && lane < rows && row < p.R) {
+        for (int w = 1; w < kLossJoinThreads / kWave; ++w) all = join(all, shared[w][lane]);
         const float log_sum = logf(all.sum);
         lse[row] = all.most + log_sum;
         if (loss) loss[row] = p.targets.column(row, p.words) < 0 ? 0.0f : (all.most - p.at_target[row]) + log_sum;
@@ -146,9 +182,10 @@ __device__ inline void loss_join(const LossRowsProblem& p, int64_t slots, int ro
 // dZ is multiplied by the power of two that takes the largest |dloss| to
 // [2^13, 2^14), an exact step that the two gradients' epilogues take back.
 struct LossRow {
-    float lse, scale;  // scale: dloss times the power of two; 0 without a target
+    float lse, scale;  // scale: dloss times the power of two; without a target infinity and 0, which make zeros
     int32_t target, pad;
 };
+constexpr int kLossBeginThreads = 256;
 struct LossPrepare {
     int64_t rows, words;
     Targets targets;
@@ -156,11 +193,13 @@ struct LossPrepare {
     LossRow* row;
     float* back;  // one over the power of two
 };
-constexpr int kLossPrepareThreads = 1024;
-__device__ inline void loss_prepare(const LossPrepare& p) {
-    __shared__ float most[kLossPrepareThreads / kWave];
+// By the first `blocks` workgroups, each of which reads all of dloss.
+__device__ inline void loss_prepare(const LossPrepare& p, uint32_t blocks) {
+    if (blockIdx.x >= blocks) return;
+    __shared__ float most[kLossBeginThreads / kWave];
     float m = 0.0f;
-    for (int64_t r = threadIdx.x; r < p.rows; r += kLossPrepareThreads)
+#pragma unroll 4
+    for (int64_t r = threadIdx.x; r < p.rows; r += kLossBeginThreads)
         if (p.targets.column(r, p.words) >= 0) m = fmaxf(m, fabsf(p.dloss[r]));
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
@@ -168,7 +207,7 @@ __device__ inline void loss_prepare(const LossPrepare& p) {
     __syncthreads();
     m = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kLossPrepareThreads / kWave; ++w) m = fmaxf(m, most[w]);
+    for (int w = 0; w < kLossBeginThreads / kWave; ++w) m = fmaxf(m, most[w]);
     int up = 0;  // (nothing to hold, or nothing that can be held: as it is)
     if (m > 0.0f && m < __builtin_inff()) {
         int exponent;
@@ -178,18 +217,27 @@ __device__ inline void loss_prepare(const LossPrepare& p) {
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.back = ldexpf(1.0f, -up);
     const float scale = ldexpf(1.0f, up);
-    for (int64_t r = (int64_t)blockIdx.x * kLossPrepareThreads + threadIdx.x; r < p.rows;
-         r += (int64_t)gridDim.x * kLossPrepareThreads) {
+    for (int64_t r = (int64_t)blockIdx.x * kLossBeginThreads + threadIdx.x; r < p.rows;
+         r += (int64_t)blocks * kLossBeginThreads) {
         const int target = p.targets.column(r, p.words);
-        p.row[r] = LossRow{p.lse[r], target < 0 ? 0.0f : p.dloss[r] * scale, target, 0};
+        p.row[r] = target < 0 ? LossRow{__builtin_inff(), 0.0f, -1, 0} : LossRow{p.lse[r], p.dloss[r] * scale, target, 0};
     }
 }
 
 // A piece's dZ: ep.out has rows of whole 16 bytes, zeros past the piece.
+//
+// Rounded to 16 bits, an entry is off by up to 2^-8 (bf16).  Over many tokens
+// that is random and as large as the result's own rounding; of one token it is
+// the target's entry alone, and twice the result's error.  Up to
+// kSplitTokens tokens dZ is therefore held in two parts, what was rounded off
+// in as many rows again: dB's contraction over the tokens has two rows for
+// each and still fits one tile of 64, and dA's rows are joined afterwards.
+constexpr int kSplitTokens = 32;
 struct LossSlopeProblem : LinearProblem {
     static constexpr int EPILOGUE = kEpilogueValues;
     const LossRow* row;
     int64_t first;  // the piece's first column
+    int64_t rest;   // bytes from a value to what was rounded off it; 0: not kept
 };
 // A wave reads its rows' values once, a row or two per lane, and passes them
 // on by lane: loads between the epilogue's stores would wait for them.
@@ -202,7 +250,7 @@ struct EpilogueRows<LossSlopeProblem> {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int64_t r = row0 + h * kWave + lane;
-            held[h] = LossRow{0.0f, 0.0f, -1, 0};
+            held[h] = LossRow{__builtin_inff(), 0.0f, -1, 0};
             if (h * kWave + lane < rows && r < row_end) held[h] = p.row[r];
         }
     }
@@ -217,14 +265,29 @@ struct EpilogueRows<LossSlopeProblem> {
     template <int TYPE>
     __device__ void finish(const LossSlopeProblem& p, const EpilogueBase& base, const EpilogueLane& at, int64_t,
                            int64_t col, int64_t left, float (&z)[8]) const {
-        const int64_t goal = now.target - p.first - col;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float d = __builtin_amdgcn_exp2f((z[e] - now.lse) * kLog2e) - (goal == e ? 1.0f : 0.0f);
-            // (a row without target adds nothing, whatever its logits; what lies past the piece is read by the products)
-            z[e] = now.target >= 0 && e < left ? d * now.scale : 0.0f;
+        for (int e = 0; e < 8; ++e) z[e] = __builtin_amdgcn_exp2f((z[e] - now.lse) * kLog2e);
+        const int64_t goal = now.target - p.first - col;
+        if (now.target >= 0 && goal >= 0 && goal < 8) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (goal == e) z[e] -= 1.0f;
         }
-        store8(reinterpret_cast<uint16_t*>(base.out + at.out), Row8::narrow<TYPE>(z), 8);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] *= now.scale;
+        if (left < 8) {  // what lies past the piece is read by the products
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] = e < left ? z[e] : 0.0f;
+        }
+        const Row8 high = Row8::narrow<TYPE>(z);
+        store8(reinterpret_cast<uint16_t*>(base.out + at.out), high, 8);
+        if (p.rest) {
+            float h[8];
+            high.widen<TYPE>(h);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] -= h[e];
+            store8(reinterpret_cast<uint16_t*>(base.out + at.out + p.rest), Row8::narrow<TYPE>(z), 8);
+        }
     }
 };
 
@@ -285,25 +348,62 @@ struct EpilogueRows<LossTokensGradProblem> {
     }
 };
 
+// dA from the sums of its rows' two parts.
+struct LossFold {
+    int64_t rows, cols;
+    const float* held;  // 2 rows x cols
+    const float* back;
+    void* out;
+    int64_t ldo;
+    int32_t out_f32;
+};
+template <int TYPE>
+__device__ inline void loss_fold(const LossFold& p) {
+    const int64_t groups = (p.cols + 7) / 8, i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= p.rows * groups) return;
+    const int64_t row = i / groups, col = i % groups * 8, left = p.cols - col;
+    const float back = *p.back;
+    float z[8], rest[8];
+    load8(z, p.held + row * p.cols + col, left);
+    load8(rest, p.held + (p.rows + row) * p.cols + col, left);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = (z[e] + rest[e]) * back;
+    if (p.out_f32)
+        store8(static_cast<float*>(p.out) + row * p.ldo + col, z, left);
+    else
+        store8(static_cast<uint16_t*>(p.out) + row * p.ldo + col, Row8::narrow<TYPE>(z), left);
+}
+
 // Copies a matrix to rows of whole 16 bytes, zeros past their width; with
-// `row`, rows without a target as zeros, so that nothing they hold reaches dB.
+// targets, rows without one as zeros, so that nothing they hold reaches dB.
 struct LossPack {
     const uint16_t* src;
     int64_t rows, cols, ld;
     uint16_t* dst;
     int64_t ldd;
+    int32_t copies;   // one below the other, two at most
     Targets targets;  // at == nullptr: every row
     int64_t words;
 };
 __device__ inline void loss_pack(const LossPack& j) {
-    const int64_t groups = j.ldd / 8, total = j.rows * groups;
+    const int64_t groups = j.ldd / 8, total = j.copies * j.rows * groups;
     for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int64_t row = i / groups, col = i % groups * 8;
+        // (64-bit divisions would take longer than the bytes)
+        const int64_t to = total <= 0x7fffffff ? (int64_t)((uint32_t)i / (uint32_t)groups) : i / groups;
+        const int64_t col = (i - to * groups) * 8, row = to < j.rows ? to : to - j.rows;
         Row8 v{};
         if (!j.targets.at || j.targets.column(row, j.words) >= 0) v = load8(j.src + row * j.ld + col, j.cols - col);
-        *reinterpret_cast<u32x4*>(j.dst + row * j.ldd + col) = v.w;
+        *reinterpret_cast<u32x4*>(j.dst + to * j.ldd + col) = v.w;
     }
 }
+
+// What comes before the products, in one launch: copies, and the rows' values
+// in the row of workgroups after theirs.
+struct LossBegin {
+    LossPack pack[2];
+    int32_t packs;
+    LossPrepare prepare;
+};
 
 // ---- launches, one translation unit per type ------------------------------------------------
 // `kmajor`: B's words are rows (b_transposed).

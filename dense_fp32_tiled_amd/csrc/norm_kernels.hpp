@@ -305,28 +305,41 @@ __global__ __launch_bounds__(Shape::THREADS) void norm_grad_kernel(NormProblem p
     float dweight[CHUNKS][8] = {}, dbias[CHUNKS][8] = {};
     const int64_t step = (int64_t)gridDim.x * Shape::ROWS;
     int at = 0;
-    for (int64_t row = (int64_t)blockIdx.x * Shape::ROWS + part; row < p.rows; row += step) {
+    // The next row is read before this one's sums are joined, so that loads are under way throughout.
+    struct RowReads {
         V dy[CHUNKS], total[CHUNKS], stream[CHUNKS];
+        float mean, rstd;
+    };
+    auto read = [&](RowReads& r, int64_t row) {
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
             const int64_t left = p.cols - column(c) * 8;
-            dy[c].template load<WHOLE>(static_cast<const E*>(p.y) + row * p.ldy + column(c) * 8, left);
-            total[c].template load<WHOLE>(static_cast<const E*>(p.total) + row * p.ldt + column(c) * 8, left);
+            r.dy[c].template load<WHOLE>(static_cast<const E*>(p.y) + row * p.ldy + column(c) * 8, left);
+            r.total[c].template load<WHOLE>(static_cast<const E*>(p.total) + row * p.ldt + column(c) * 8, left);
         }
         if (p.dstream) {
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c)
-                stream[c].template load<WHOLE>(static_cast<const E*>(p.dstream) + row * p.lds + column(c) * 8,
-                                               p.cols - column(c) * 8);
+                r.stream[c].template load<WHOLE>(static_cast<const E*>(p.dstream) + row * p.lds + column(c) * 8,
+                                                 p.cols - column(c) * 8);
         }
-        const float mean = p.mean[row], rstd = p.rstd[row];
+        r.mean = p.mean[row];
+        r.rstd = p.rstd[row];
+    };
+    int64_t row = (int64_t)blockIdx.x * Shape::ROWS + part;
+    RowReads next;
+    if (row < p.rows) read(next, row);
+    for (; row < p.rows; row += step) {
+        const RowReads now = next;
+        if (row + step < p.rows) read(next, row + step);
+        const float mean = now.mean, rstd = now.rstd;
         float g[CHUNKS][8], u[CHUNKS][8], sums[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
             const int64_t left = p.cols - column(c) * 8;
             float w[8];
-            dy[c].widen(g[c]);
-            total[c].widen(u[c]);
+            now.dy[c].widen(g[c]);
+            now.total[c].widen(u[c]);
             if (p.weight) weight[c].widen(w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -345,7 +358,7 @@ __global__ __launch_bounds__(Shape::THREADS) void norm_grad_kernel(NormProblem p
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
             float add[8];
-            if (p.dstream) stream[c].widen(add);
+            if (p.dstream) now.stream[c].widen(add);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 g[c][e] = (g[c][e] - m - u[c][e] * mu) * rstd;

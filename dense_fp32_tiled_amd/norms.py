@@ -85,6 +85,9 @@ def gemm_dropout(value_type, rows, cols, p, seed, offset, step, X, ldx, residual
                                       stream)
 
 
+_NORM_GRADS = frozenset(("x", "residual", "weight", "bias"))
+
+
 # ---- torch convenience --------------------------------------------------------------------
 def _value_type(t, name):
     if pr.torch is None:
@@ -127,7 +130,9 @@ def dropout(x, p: float, seed: int, offset: int = 0, residual=None, step=None, o
     pres, ldr = (None, 0) if residual is None else pr._matrix(residual, "residual", rows, cols, dtype, device)
     if out is None:
         out = pr.torch.empty(rows, cols, dtype=dtype, device=device)
-    po, ldo = pr._matrix(out, "out", rows, cols, dtype, device)
+        po, ldo = out.data_ptr(), cols if cols > 0 else 1
+    else:
+        po, ldo = pr._matrix(out, "out", rows, cols, dtype, device)
     pr._run(dft.library().gemm_dropout, "gemm_dropout", device, kind, rows, cols, p, seed, offset, at, px, ldx, pres,
             ldr, po, ldo)
     return out
@@ -147,30 +152,34 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, p: f
             return layer_norm(x, weight, bias, eps, residual, p, seed, offset, step, out, total)
     rows, cols = x.shape if x.dim() == 2 else (-1, -1)
     dtype = x.dtype
-    g = LayerNormArgs(value_type=kind, eps=eps, p=p, seed=seed, offset=offset, rows=rows, cols=cols)
-    g.x, g.ldx = pr._matrix(x, "x", rows, cols, dtype, device)
-    g.step = _counter(p, seed, offset, step, device)
-    if weight is not None:
-        g.weight = pr._list(weight, "weight", (cols,), dtype, device)
-    if bias is not None:
-        g.bias = pr._list(bias, "bias", (cols,), dtype, device)
-    empty = pr.torch.empty
+    px, ldx = pr._matrix(x, "x", rows, cols, dtype, device)
+    at = _counter(p, seed, offset, step, device)
+    pw = None if weight is None else pr._list(weight, "weight", (cols,), dtype, device)
+    pb = None if bias is None else pr._list(bias, "bias", (cols,), dtype, device)
+    empty, ld = pr.torch.empty, cols if cols > 0 else 1
+    pres = pt = None
+    ldr = ldt = ldy = ld
     if residual is not None or p > 0:
         if residual is not None:
-            g.residual, g.ldr = pr._matrix(residual, "residual", rows, cols, dtype, device)
+            pres, ldr = pr._matrix(residual, "residual", rows, cols, dtype, device)
         if total is None:
             total = empty(rows, cols, dtype=dtype, device=device)
-        g.total, g.ldt = pr._matrix(total, "total", rows, cols, dtype, device)
+            pt = total.data_ptr()
+        else:
+            pt, ldt = pr._matrix(total, "total", rows, cols, dtype, device)
     elif total is not None:
         raise ValueError("total is x itself without residual and dropout")
     else:
         total = x
     if out is None:
         out = empty(rows, cols, dtype=dtype, device=device)
-    g.y, g.ldy = pr._matrix(out, "out", rows, cols, dtype, device)
-    mean, rstd = empty(2, rows, dtype=pr._f32, device=device).unbind(0)
-    g.mean, g.rstd = mean.data_ptr(), rstd.data_ptr()
-    pr._run(dft.library().gemm_layer_norm, "gemm_layer_norm", device, g)
+        py = out.data_ptr()
+    else:
+        py, ldy = pr._matrix(out, "out", rows, cols, dtype, device)
+    mean, rstd = empty(rows, dtype=pr._f32, device=device), empty(rows, dtype=pr._f32, device=device)
+    pr._run(dft.library().gemm_layer_norm, "gemm_layer_norm", device,
+            LayerNormArgs(kind, eps, p, seed, offset, at, rows, cols, px, ldx, pres, ldr, pw, pb, pt, ldt, py, ldy,
+                          mean.data_ptr(), rstd.data_ptr()))
     return out, NormState(total, mean, rstd)
 
 
@@ -184,39 +193,36 @@ def layer_norm_grad(dy, state: NormState, weight=None, dtotal=None, p: float = 0
     if stream is not None:
         with pr._current(stream, device):
             return layer_norm_grad(dy, state, weight, dtotal, p, seed, offset, step, want, workspace)
-    want = frozenset(want)
-    if not want <= {"x", "residual", "weight", "bias"}:
-        raise ValueError(f"want names 'x', 'residual', 'weight' and 'bias', not "
-                         f"{sorted(want - {'x', 'residual', 'weight', 'bias'})}")
+    if not _NORM_GRADS.issuperset(want):
+        raise ValueError(f"want names 'x', 'residual', 'weight' and 'bias', not {sorted(set(want) - _NORM_GRADS)}")
     rows, cols = dy.shape if dy.dim() == 2 else (-1, -1)
     dtype = dy.dtype
-    g = LayerNormGradArgs(value_type=kind, p=p, seed=seed, offset=offset, rows=rows, cols=cols)
-    g.dY, g.ldy = pr._matrix(dy, "dy", rows, cols, dtype, device)
-    g.step = _counter(p, seed, offset, step, device)
+    py, ldy = pr._matrix(dy, "dy", rows, cols, dtype, device)
+    at = _counter(p, seed, offset, step, device)
     total, mean, rstd = state
-    g.total, g.ldt = pr._matrix(total, "state.total", rows, cols, dtype, device)
-    g.mean = pr._list(mean, "state.mean", (rows,), pr._f32, device)
-    g.rstd = pr._list(rstd, "state.rstd", (rows,), pr._f32, device)
-    if weight is not None:
-        g.weight = pr._list(weight, "weight", (cols,), dtype, device)
-    if dtotal is not None:
-        g.dstream, g.lds = pr._matrix(dtotal, "dtotal", rows, cols, dtype, device)
-    empty = pr.torch.empty
-    dx = dresidual = dweight = dbias = None
+    pt, ldt = pr._matrix(total, "state.total", rows, cols, dtype, device)
+    pm = pr._list(mean, "state.mean", (rows,), pr._f32, device)
+    ps = pr._list(rstd, "state.rstd", (rows,), pr._f32, device)
+    pw = None if weight is None else pr._list(weight, "weight", (cols,), dtype, device)
+    pd, lds = (None, 0) if dtotal is None else pr._matrix(dtotal, "dtotal", rows, cols, dtype, device)
+    empty, ld = pr.torch.empty, cols if cols > 0 else 1
+    dx = dresidual = dweight = dbias = pdx = pdr = pdw = pdb = None
     if "residual" in want or (p == 0 and "x" in want):
         dresidual = empty(rows, cols, dtype=dtype, device=device)
-        g.dtotal, g.lddt = dresidual.data_ptr(), max(cols, 1)
+        pdr = dresidual.data_ptr()
     if "x" in want:
         dx = dresidual
         if p > 0:
             dx = empty(rows, cols, dtype=dtype, device=device)
-            g.dx, g.lddx = dx.data_ptr(), max(cols, 1)
+            pdx = dx.data_ptr()
     if "weight" in want:
         dweight = empty(cols, dtype=pr._f32, device=device)
-        g.dweight = dweight.data_ptr()
+        pdw = dweight.data_ptr()
     if "bias" in want:
         dbias = empty(cols, dtype=pr._f32, device=device)
-        g.dbias = dbias.data_ptr()
+        pdb = dbias.data_ptr()
+    g = LayerNormGradArgs(kind, p, seed, offset, at, rows, cols, py, ldy, pt, ldt, pm, ps, pw, pd, lds, pdr, ld, pdx, ld,
+                          pdw, pdb)
     lib = dft.library()
     keep = pr._workspace(g, lib.gemm_layer_norm_grad_workspace_bytes(g, pr._num_cus(device)),
                          "gemm_layer_norm_grad_workspace_bytes", workspace, device)

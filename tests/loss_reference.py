@@ -9,7 +9,8 @@ additions (16 in a lane, two over a wave, a thread's pieces, ten halvings),
 each joining with two more products and exponentials: relative 8u a step is
 taken for all of them, with the row's spread of logits s in 3u s.  dZ is
 rounded to 16 bits: eps / 2, and where it is held scaled, half of the type's
-least step over the scale, which is at least 2^13 / max |dloss|."""
+least step over the scale, which is at least 2^13 / max |dloss|; up to 32 tokens
+it is held in two parts, and what is left is (eps / 2)^2."""
 
 from __future__ import annotations
 
@@ -58,6 +59,8 @@ def gradients(dloss, a, b, targets, lse, a_dtype=None, b_dtype=None, pieces=1):
     off = torch.where(valid[:, None], p_off * g.abs() + 3 * U * dz.abs(), 0.0)
     most = float(g.abs().max()) if M else 0.0
     step = torch.finfo(dtype).eps / 2
+    if M <= 32:
+        step *= step
     off = off + torch.where(valid[:, None], step * (dz.abs() + off) + SMALLEST[dtype] * most / 2 ** 13, 0.0)
     big = dz.abs() + off
     da, db = dz @ B.t(), A.t() @ dz
