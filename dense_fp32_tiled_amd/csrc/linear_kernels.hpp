@@ -885,6 +885,24 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
                 copy_a.next();
             }
             if (T > 0) read_first(at_a, at_b);
+            if constexpr (S == 1) {
+                // One contraction tile at most: nothing is copied behind it.
+                static_assert(!PERSISTENT, "a ring has more places");
+                if (T > 0)
+                    static_for<STEPS>([&](auto ST_) {
+                        constexpr int ST = decltype(ST_)::value, NOW = ST & 1, THEN = NOW ^ 1;
+                        if constexpr (ST + 1 < STEPS) {
+#pragma unroll
+                            for (int j = 0; j < NI; ++j) bf[THEN][j] = read_b.read(lds_b, 0, ST + 1, j);
+                        }
+#pragma unroll
+                        for (int i = 0; i < MI; ++i) {
+#pragma unroll
+                            for (int j = 0; j < NI; ++j) acc[i][j] = Op::mma(bf[NOW][j], af[i], acc[i][j]);
+                            if constexpr (ST + 1 < STEPS) af[i] = read_a.read(lds_a, 0, ST + 1, i);
+                        }
+                    });
+            } else
             for (int64_t t = 0; t < T; ++t) {
                 // places of tile t+1
                 const int next_a = PERSISTENT ? (at_a >= RING - 2 ? at_a + 2 - RING : at_a + 2) : at_a + 1 == S ? 0 : at_a + 1;

@@ -249,6 +249,12 @@ Plan plan_a(const LossSizes& s, int64_t words, int cus) {
 }
 Plan plan_b(const LossSizes& s, int64_t words, int cus) {
     const int64_t rows = parts_of(s) * s.M;
+    // (a single contraction tile: ShortShape's tiles, unless they are more than a launch holds)
+    if (rows <= kShortRows && s.variant == GEMM_LINEAR_AUTO) {
+        const Plan plan = s.b_transposed ? choose(words, s.K, rows, 1, kGroupNone, kDirect, GEMM_LINEAR_128x128, 1, cus)
+                                         : choose(s.K, words, rows, 1, kGroupNone, kDirect, GEMM_LINEAR_128x128, 1, cus);
+        if (plan.found()) return plan;
+    }
     return s.b_transposed ? choose(words, s.K, rows, 1, kGroupNone, kDirect, s.variant, 0, cus)
                           : choose(s.K, words, rows, 1, kGroupNone, kDirect, s.variant, 0, cus);
 }

@@ -405,6 +405,13 @@ struct LossBegin {
     LossPrepare prepare;
 };
 
+// dB of few tokens, at most kShortRows rows of dZ: a single contraction tile,
+// so nothing is copied ahead, a workgroup's operands take 32 KiB and four
+// workgroups fit a CU, whose stores are what bounds it (the shape of two
+// stages keeps two).
+constexpr int kShortRows = kDepth;
+using ShortShape = LinearShape<128, 128, 64, 64, 1, 4>;
+
 // ---- launches, one translation unit per type ------------------------------------------------
 // `kmajor`: B's words are rows (b_transposed).
 #define DFT_LOSS_LAUNCHES(TYPE)                                                                                       \

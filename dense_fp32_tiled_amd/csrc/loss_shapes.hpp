@@ -6,10 +6,9 @@
 
 namespace dft {
 
-template <int TYPE, bool AK, bool BK_, int TILE, class Problem>
-hipError_t launch_loss_tile(const Problem& p, uint32_t tiles_m, uint32_t tiles_n, uint32_t slices, int cus,
-                            hipStream_t stream) {
-    using Shape = typename ShapeOf<TILE>::type;
+template <int TYPE, bool AK, bool BK_, class Shape, class Problem>
+hipError_t launch_loss_shape(const Problem& p, uint32_t tiles_m, uint32_t tiles_n, uint32_t slices, int cus,
+                             hipStream_t stream) {
     Problem problem = p;
     void* args[] = {&problem, &tiles_m, &tiles_n, &slices};
     uint32_t blocks = tiles_m * tiles_n * slices;
@@ -21,10 +20,10 @@ template <int TYPE, bool AK, bool BK_, class Problem>
 hipError_t launch_loss_layout(const Problem& p, LinearTile tile, uint32_t tiles_m, uint32_t tiles_n, uint32_t slices,
                               int cus, hipStream_t stream) {
     switch (tile) {
-        case kTile256: return launch_loss_tile<TYPE, AK, BK_, kTile256>(p, tiles_m, tiles_n, slices, cus, stream);
-        case kTile128: return launch_loss_tile<TYPE, AK, BK_, kTile128>(p, tiles_m, tiles_n, slices, cus, stream);
-        case kTile64: return launch_loss_tile<TYPE, AK, BK_, kTile64>(p, tiles_m, tiles_n, slices, cus, stream);
-        default: return launch_loss_tile<TYPE, AK, BK_, kTile32x128>(p, tiles_m, tiles_n, slices, cus, stream);
+        case kTile256: return launch_loss_shape<TYPE, AK, BK_, ShapeOf<kTile256>::type>(p, tiles_m, tiles_n, slices, cus, stream);
+        case kTile128: return launch_loss_shape<TYPE, AK, BK_, ShapeOf<kTile128>::type>(p, tiles_m, tiles_n, slices, cus, stream);
+        case kTile64: return launch_loss_shape<TYPE, AK, BK_, ShapeOf<kTile64>::type>(p, tiles_m, tiles_n, slices, cus, stream);
+        default: return launch_loss_shape<TYPE, AK, BK_, ShapeOf<kTile32x128>::type>(p, tiles_m, tiles_n, slices, cus, stream);
     }
 }
 
