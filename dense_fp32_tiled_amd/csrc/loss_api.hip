@@ -116,10 +116,12 @@ int launch_logits(const LossSizes& s, const Problem& p, LinearTile tile, int cus
 
 // ---- forward ----------------------------------------------------------------------------
 // In the workspace, one after the other: A packed, a piece of B packed, the
-// rows' pieces, the targets' logits.
+// rows' pieces, the targets' logits.  Rows have nothing to do with each other:
+// so many of them at a time that their pieces stay within some 512 MiB.
+constexpr int64_t kRowsAtOnce = 32768;
 struct ForwardPlan {
     bool pack_a, pack_b;
-    int64_t piece, slots;
+    int64_t rows, piece, slots;
     int width;  // columns of a slot: a wave's
     LinearTile tile;
     int64_t a_bytes, b_bytes, pieces_bytes, target_bytes, workspace;
@@ -127,9 +129,10 @@ struct ForwardPlan {
 int wave_columns(LinearTile tile) { return tile == kTile256 || tile == kTile128 ? 64 : 32; }
 
 int plan_forward(const gemm_cross_entropy_args& a, const Matrix& A, const Matrix& B, int cus, ForwardPlan* plan) {
-    const LossSizes s = sizes_of(a);
+    LossSizes s = sizes_of(a);
     ForwardPlan& f = *plan;
     const bool work = s.K > 0;
+    f.rows = std::min(s.M, kRowsAtOnce);
     f.pack_a = work && !whole_rows(A);
     f.pack_b = work && !whole_rows(B);
     // (B as it is: all of it at once)
@@ -138,6 +141,7 @@ int plan_forward(const gemm_cross_entropy_args& a, const Matrix& A, const Matrix
     const Matrix a_read = f.pack_a ? packed(A) : A;
     const Matrix b_piece = piece_of(B, s.b_transposed, 0, f.piece), b_read = f.pack_b ? packed(b_piece) : b_piece;
     if (!copies_fit(kTile256, a_read, true, b_read, s.b_transposed)) return GEMM_ERR_TOO_LARGE;
+    s.M = f.rows;
     const Plan logits = logits_plan(s, f.piece, cus);
     if (!logits.found()) return GEMM_ERR_TOO_LARGE;
     f.tile = logits.tile;
@@ -146,8 +150,8 @@ int plan_forward(const gemm_cross_entropy_args& a, const Matrix& A, const Matrix
     f.slots = round_up(s.N, kTileSizes[f.tile].bn) / f.width;
     f.a_bytes = f.pack_a ? packed_bytes(A) : 0;
     f.b_bytes = f.pack_b ? packed_bytes(b_piece) : 0;
-    f.pieces_bytes = round_up(f.slots * s.M * (int64_t)sizeof(RowPiece), 256);
-    f.target_bytes = round_up(s.M * 4, 256);
+    f.pieces_bytes = round_up(f.slots * f.rows * (int64_t)sizeof(RowPiece), 256);
+    f.target_bytes = round_up(f.rows * 4, 256);
     f.workspace = f.a_bytes + f.b_bytes + f.pieces_bytes + f.target_bytes;
     return GEMM_OK;
 }
@@ -193,7 +197,7 @@ int run_forward(const gemm_cross_entropy_args& a, hipStream_t stream) {
     LossRowsProblem p{};
     p.pieces = static_cast<RowPiece*>(space.take(f.pieces_bytes));
     p.at_target = static_cast<float*>(space.take(f.target_bytes));
-    p.targets = Targets{a.loss ? a.targets : nullptr, a.target_type == GEMM_TARGET_I64};  // (loss alone reads them)
+    p.targets.wide = a.target_type == GEMM_TARGET_I64;
     p.words = s.N;
     const Targets every{nullptr, 0};
     LossBegin jobs{};
@@ -203,23 +207,37 @@ int run_forward(const gemm_cross_entropy_args& a, hipStream_t stream) {
         jobs.pack[jobs.packs++] = pack_job(A, to, 1, every, 0);
         A = to;
     }
-    for (int64_t first = 0; first < s.N; first += f.piece) {
-        const int64_t words = std::min(f.piece, s.N - first);
-        Matrix b = piece_of(B, s.b_transposed, first, words);
-        if (f.pack_b) {
-            Matrix to = packed(b);
-            to.data = b_space;
-            jobs.pack[jobs.packs++] = pack_job(b, to, 1, every, 0);
-            b = to;
+    // (a single piece of B is packed once)
+    const bool one = f.piece >= s.N;
+    Matrix packed_b{};
+    for (int64_t row = 0; row < s.M; row += f.rows) {
+        LossSizes block = s;
+        block.M = std::min(f.rows, s.M - row);
+        Matrix x = A;
+        x.rows = block.M;
+        x.data = static_cast<const char*>(A.data) + row * A.ld * 2;
+        p.targets.at = a.loss ? static_cast<const char*>(a.targets) + row * target_bytes(a.target_type) : nullptr;
+        for (int64_t first = 0; first < s.N; first += f.piece) {
+            const int64_t words = std::min(f.piece, s.N - first);
+            Matrix b = piece_of(B, s.b_transposed, first, words);
+            if (f.pack_b && (row == 0 || !one)) {
+                packed_b = packed(b);
+                packed_b.data = b_space;
+                jobs.pack[jobs.packs++] = pack_job(b, packed_b, 1, every, 0);
+            }
+            if (f.pack_b) b = packed_b;
+            if ((st = begin(jobs, false, stream)) != GEMM_OK) return st;
+            jobs.packs = 0;
+            describe_logits(p, block, x, b, words);
+            p.first = first;
+            if ((st = launch_logits(block, p, f.tile, cus, stream)) != GEMM_OK) return st;
         }
-        if ((st = begin(jobs, false, stream)) != GEMM_OK) return st;
-        jobs.packs = 0;
-        describe_logits(p, s, A, b, words);
-        p.first = first;
-        if ((st = launch_logits(s, p, f.tile, cus, stream)) != GEMM_OK) return st;
+        const int rows = join_rows(block.M, f.slots, cus);
+        st = launch(loss_join_kernel, dim3((unsigned)ceil_div(block.M, rows)), kLossJoinThreads, stream, p, f.slots, rows,
+                    a.loss ? a.loss + row : nullptr, a.lse + row);
+        if (st != GEMM_OK) return st;
     }
-    const int rows = join_rows(s.M, f.slots, cus);
-    return launch(loss_join_kernel, dim3((unsigned)ceil_div(s.M, rows)), kLossJoinThreads, stream, p, f.slots, rows, a.loss, a.lse);
+    return GEMM_OK;
 }
 
 // ---- gradients ----------------------------------------------------------------------------

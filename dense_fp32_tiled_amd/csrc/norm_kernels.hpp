@@ -535,7 +535,7 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutProblem p) {
     const uint64_t offset = p.dropout.drop ? dropout_offset(p.dropout) : 0;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += stride) {
         // (64-bit divisions would take as long as the generator)
-        const int64_t row = total <= 0xffffffff ? (uint32_t)i / (uint32_t)chunks : i / chunks;
+        const int64_t row = p.rows == 1 ? 0 : total <= 0xffffffff ? (int64_t)((uint32_t)i / (uint32_t)chunks) : i / chunks;
         const int64_t chunk = i - row * chunks, left = p.cols - chunk * 8;
         V in, add;
         in.template load<WHOLE>(static_cast<const E*>(p.x) + row * p.ldx + chunk * 8, left);

@@ -776,8 +776,9 @@ typedef struct {
 int gemm_cross_entropy(const gemm_cross_entropy_args *args, void *stream);
 
 /* Bytes gemm_cross_entropy needs on a device with num_cus compute units: two
- * values for every 32 or 64 words of a token, and packed operands.  Pure host
- * call; a negative gemm_status on bad arguments. */
+ * values for every 32 or 64 words of a token (of 32768 tokens at most, which
+ * are taken at a time), and packed operands.  Pure host call; a negative
+ * gemm_status on bad arguments. */
 int64_t gemm_cross_entropy_workspace_bytes(const gemm_cross_entropy_args *args, int32_t num_cus);
 
 typedef struct {

@@ -314,3 +314,52 @@ def test_streams_and_graphs():
         want = both()
         for _, held in graphs:
             assert all(torch.equal(x, y) for x, y in zip(held, want)), n
+
+
+@pytest.mark.parametrize("size", [(40000, 300, 24), (33000, 301, 25), (65536 + 3, 1000, 8)], ids=lambda s: "x".join(map(str, s)))
+def test_more_tokens_than_are_taken_at_once(size):
+    M, N, K = size
+    a, b, t, g = (x.cuda() for x in problem(M, N, K, torch.float16, 8))
+    for piece in (0, 256):
+        loss, lse = dft.linear_cross_entropy(a, b, t, piece=piece)
+        want = ref.forward(a, b, t)
+        assert_within(lse, [x.cpu() for x in want["lse"]], "lse")
+        assert_within(loss, [x.cpu() for x in want["loss"]], "loss")
+        grads = dft.linear_cross_entropy_grad(g, a, b, t, lse, piece=piece)
+        want = ref.gradients(g, a, b, t, lse, pieces=4)
+        for got, name in ((grads.a, "a"), (grads.b, "b")):
+            assert bool(((got.double() - want[name][0]).abs() <= want[name][1]).all()), name
+
+
+@pytest.mark.parametrize("transposed", [False, True], ids=["columns", "rows"])
+def test_places_past_32_bits(transposed):
+    """A vocabulary's matrix of more than 2^32 bytes and 2^31 values: the loss, the tokens' gradient, and the words' at both ends."""
+    M, N, K = 3, 540_000, 4096
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    a = torch.randn(M, K, device="cuda", generator=gen).bfloat16()
+    b = torch.empty((N, K) if transposed else (K, N), device="cuda", dtype=torch.bfloat16)
+    for part in b.chunk(16):
+        part.copy_(torch.randn(part.shape, device="cuda", generator=gen) * K ** -0.5)
+    b = b.t() if transposed else b
+    t = torch.tensor([0, N - 1, 300_000], device="cuda")
+    g = torch.tensor([0.5, 0.25, 1.0], device="cuda")
+    loss, lse = dft.linear_cross_entropy(a, b, t)
+    grads = dft.linear_cross_entropy_grad(g, a, b, t, lse)
+    pieces = [slice(i, min(i + 60_000, N)) for i in range(0, N, 60_000)]
+    wide = a.double()
+    z = torch.cat([wide @ b[:, p].double() for p in pieces], 1)
+    e = (K + 2) * 2 * 2.0 ** -24 * float((wide.abs() @ b[:, pieces[0]].double().abs()).max()) * 1.5  # (any other word's, at most)
+    exact = torch.logsumexp(z, 1)
+    tol = 2 * e + 8 * 2.0 ** -24 * (N / 32 + 100)
+    assert bool(((lse - exact).abs() <= tol).all())
+    assert bool(((loss - (exact - z[torch.arange(M), t])).abs() <= tol).all())
+    dz = torch.exp(z - lse.double()[:, None])
+    dz[torch.arange(M), t] -= 1
+    dz *= g.double()[:, None]
+    da = sum(dz[:, p] @ b[:, p].double().t() for p in pieces)
+    # dZ in two parts is exact beside its logits' e; da sums N products of it, and both are rounded once
+    size = sum(dz[:, p].abs() @ b[:, p].double().abs().t() for p in pieces)
+    assert bool(((grads.a.double() - da).abs() <= 2 * (e + N * 2.0 ** -23) * size + da.abs() * 2.0 ** -8 + 2.0 ** -30).all())
+    for p in (pieces[0], slice(299_990, 300_010), pieces[-1]):
+        want, size = wide.t() @ dz[:, p], wide.abs().t() @ dz[:, p].abs()
+        assert bool(((grads.b[:, p].double() - want).abs() <= 2 * e * size + want.abs() * 2.0 ** -8 + 2.0 ** -30).all()), p
