@@ -44,26 +44,44 @@ int launch(void (*kernel)(Args...), dim3 grid, int threads, hipStream_t stream, 
 constexpr int64_t kMostBlocks = (int64_t)1 << 21;
 
 // ---- shapes ---------------------------------------------------------------------------
-// The narrowest shape that holds a row: a wave of its own up to 1024 columns
-// (no barriers), then four to sixteen waves with at most 16 values per lane,
-// so that a row's loads, sums and results stay in registers at four waves per
-// SIMD or more.
-constexpr int64_t kWidestShape = 16384;
+// The narrowest shape that holds a row, so that its loads, sums and results
+// stay in registers at four waves per SIMD: forward a wave of its own (no
+// barriers) up to 1024 columns, 512 of 32-bit values, then four to sixteen
+// waves with at most 16 values per lane (8 of 32 bits).  The gradient's kernel
+// holds a row, the next one and the columns' sums: 8 values per lane, and in
+// the widest shape 16 with the sums in LDS.  Rows of fewer than 8 columns and
+// of more than the widest shape go to the kernels that read a row again.
+constexpr int64_t kNarrowest = 8;
+int64_t widest(int type) { return type == GEMM_VALUE_F32 ? 8192 : 16384; }
+bool in_registers(int type, int64_t cols) { return cols >= kNarrowest && cols <= widest(type); }
+
+#define DFT_SHAPE(...)                                                                          \
+    if (cols <= NormShape<__VA_ARGS__>::COLS)                                                   \
+        return cols % 8 == 0 ? Run<TYPE, NormShape<__VA_ARGS__>, true>::run(args...)            \
+                             : Run<TYPE, NormShape<__VA_ARGS__>, false>::run(args...);
 template <template <int, class, bool> class Run, int TYPE, class... Args>
 int with_shape(int64_t cols, Args... args) {
-    const bool whole = cols % 8 == 0;
-#define DFT_SHAPE(W, C)                                                                              \
-    if (cols <= NormShape<W, C>::COLS)                                                                \
-        return whole ? Run<TYPE, NormShape<W, C>, true>::run(args...) : Run<TYPE, NormShape<W, C>, false>::run(args...);
+    constexpr bool WIDE = TYPE == kValueF32;
     DFT_SHAPE(1, 1)
-    DFT_SHAPE(1, 2)
-    DFT_SHAPE(4, 1)
-    DFT_SHAPE(4, 2)
-    DFT_SHAPE(8, 2)
-    DFT_SHAPE(16, 2)
-#undef DFT_SHAPE
-    return GEMM_ERR_TOO_LARGE;  // (not reached: wider rows have kernels of their own)
+    if constexpr (Run<TYPE, NormShape<1, 1>, true>::GRADIENT) {
+        DFT_SHAPE(4, 1)
+        DFT_SHAPE(8, 1)
+        DFT_SHAPE(16, 1, WIDE)
+        if constexpr (!WIDE) { DFT_SHAPE(16, 2, true) }
+    } else if constexpr (WIDE) {
+        DFT_SHAPE(4, 1)
+        DFT_SHAPE(8, 1)
+        DFT_SHAPE(16, 1)
+    } else {
+        DFT_SHAPE(1, 2)
+        DFT_SHAPE(4, 1)
+        DFT_SHAPE(4, 2)
+        DFT_SHAPE(8, 2)
+        DFT_SHAPE(16, 2)
+    }
+    return GEMM_ERR_TOO_LARGE;  // (not reached)
 }
+#undef DFT_SHAPE
 template <template <int, class, bool> class Run, class... Args>
 int with_type(int type, int64_t cols, Args... args) {
     if (type == GEMM_VALUE_BF16) return with_shape<Run, kInputBf16>(cols, args...);
@@ -73,6 +91,7 @@ int with_type(int type, int64_t cols, Args... args) {
 
 template <int TYPE, class Shape, bool WHOLE>
 struct RunNorm {
+    static constexpr bool GRADIENT = false;
     static int run(const NormProblem* p, hipStream_t stream) {
         const int64_t blocks = std::min(ceil_div(p->rows, Shape::ROWS), kMostBlocks);
         return launch(norm_kernel<TYPE, Shape, WHOLE>, dim3((unsigned)blocks), Shape::THREADS, stream, *p);
@@ -83,19 +102,21 @@ struct RunNorm {
 // many rows as it takes, since each leaves a row of sums to join.
 template <int TYPE, class Shape, bool WHOLE>
 struct GradPlaces {
+    static constexpr bool GRADIENT = true;
     static int run(int64_t rows, int cus) {
         return (int)std::min<int64_t>(ceil_div(rows, Shape::ROWS), (int64_t)cus * (1024 / Shape::THREADS));
     }
 };
 template <int TYPE, class Shape, bool WHOLE>
 struct RunGrad {
+    static constexpr bool GRADIENT = true;
     static int run(const NormProblem* p, hipStream_t stream) {
         return launch(norm_grad_kernel<TYPE, Shape, WHOLE>, dim3((unsigned)p->places), Shape::THREADS, stream, *p);
     }
 };
 int grad_places(int type, int64_t rows, int64_t cols, int cus) {
-    // wide rows: the columns' sums, a workgroup for every 2048 columns of a place
-    if (cols > kWidestShape) return (int)std::min<int64_t>(rows, 256);
+    // rows that are read again: the columns' sums, a workgroup for every 2048 columns of a place
+    if (!in_registers(type, cols)) return (int)std::min<int64_t>(rows, 256);
     return with_type<GradPlaces>(type, cols, rows, cus);
 }
 
@@ -132,7 +153,7 @@ int run_norm(const gemm_layer_norm_args& a, hipStream_t stream) {
     p.total = const_cast<void*>(total.data); p.ldt = a.ldt;
     p.y = a.y; p.ldy = a.ldy;
     p.mean = a.mean; p.rstd = a.rstd;
-    if (a.cols <= kWidestShape) return with_type<RunNorm>(a.value_type, a.cols, (const NormProblem*)&p, stream);
+    if (in_registers(a.value_type, a.cols)) return with_type<RunNorm>(a.value_type, a.cols, (const NormProblem*)&p, stream);
     const dim3 grid((unsigned)std::min(a.rows, kMostBlocks));
     if (a.value_type == GEMM_VALUE_BF16) return launch(norm_wide_kernel<kInputBf16>, grid, kWideThreads, stream, p);
     if (a.value_type == GEMM_VALUE_F16) return launch(norm_wide_kernel<kInputF16>, grid, kWideThreads, stream, p);
@@ -156,7 +177,7 @@ int64_t check_grad(const gemm_layer_norm_grad_args& a, int* drop) {
     if (*drop < 0) return GEMM_ERR_UNSUPPORTED;
     int st = check_sizes(a.rows, a.cols);
     if (st != GEMM_OK) return st;
-    if (a.cols > kWidestShape && a.cols > (int64_t)0xffff * 2048) return GEMM_ERR_TOO_LARGE;  // (the columns' grid)
+    if (a.cols > (int64_t)0xffff * 2048) return GEMM_ERR_TOO_LARGE;  // (the columns' grid)
     if (a.workspace_bytes < 0) return GEMM_ERR_WORKSPACE;
     const int64_t size = value_bytes(a.value_type);
     const auto matrix = [&](const void* p, int64_t ld) { return Matrix{p, a.rows, a.cols, ld, size}; };
@@ -198,7 +219,7 @@ int run_grad(const gemm_layer_norm_grad_args& a, hipStream_t stream) {
     p.places = grad_places(a.value_type, a.rows, a.cols, cus);
     p.partial = a.dweight || a.dbias ? static_cast<float*>(a.workspace) : nullptr;
     if (a.rows > 0) {
-        if (a.cols <= kWidestShape)
+        if (in_registers(a.value_type, a.cols))
             st = with_type<RunGrad>(a.value_type, a.cols, (const NormProblem*)&p, stream);
         else if (a.value_type == GEMM_VALUE_BF16)
             st = run_wide_grad<kInputBf16>(p, stream);

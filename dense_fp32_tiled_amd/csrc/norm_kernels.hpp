@@ -50,11 +50,15 @@ struct NormProblem {
 };
 
 // A row is WAVES waves' work, CHUNKS chunks of eight per lane; waves that
-// share no row stand in one workgroup of at least four.
-template <int WAVES_, int CHUNKS_>
+// share no row stand in one workgroup of at least four.  SUMS_IN_LDS: where the
+// gradient's kernel keeps the columns' sums, since the registers do not hold
+// them beside a row and the next.
+template <int WAVES_, int CHUNKS_, bool SUMS_IN_LDS_ = false>
 struct NormShape {
     static constexpr int WAVES = WAVES_, CHUNKS = CHUNKS_, COLS = WAVES * kWave * 8 * CHUNKS;
+    static constexpr bool SUMS_IN_LDS = SUMS_IN_LDS_;
     static constexpr int ROWS = WAVES >= 4 ? 1 : 4 / WAVES, THREADS = WAVES * ROWS * kWave;
+    static constexpr int MIN_WAVES = 4;  // per SIMD: sixteen per CU
 };
 
 // Sums of N values over a row's waves, the same in every lane.  `at` alternates
@@ -92,63 +96,47 @@ __device__ inline NormStatistics norm_statistics(float near, float shift, float 
 }
 
 template <int TYPE, class Shape, bool WHOLE>
-__global__ __launch_bounds__(Shape::THREADS) void norm_kernel(NormProblem p) {
+__global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void norm_kernel(NormProblem p) {
     using V = Values8<TYPE>;
     using E = typename V::element;
     constexpr int WAVES = Shape::WAVES, CHUNKS = Shape::CHUNKS;
     __shared__ float shared[2][WAVES][2];
-    const int lane = threadIdx.x % (WAVES * kWave), part = threadIdx.x / (WAVES * kWave);
-    const int64_t chunks = (p.cols + 7) / 8;
+    const int lane = threadIdx.x % (WAVES * kWave), cols = (int)p.cols, chunks = (cols + 7) / 8;
+    const int part = __builtin_amdgcn_readfirstlane(threadIdx.x / (WAVES * kWave));
     const uint64_t offset = p.dropout.drop ? dropout_offset(p.dropout) : 0;
-    const float n = (float)p.cols;
+    const float n = (float)cols;
+    auto column = [&](int c) { return (lane + c * WAVES * kWave) * 8; };
     for (int64_t first = (int64_t)blockIdx.x * Shape::ROWS; first < p.rows; first += (int64_t)gridDim.x * Shape::ROWS) {
         const int64_t row = first + part;
         if (WAVES < 4 && row >= p.rows) break;  // (whole waves: nothing is waited for together)
-        const E* x = static_cast<const E*>(p.x) + row * p.ldx;
-        const E* residual = p.residual ? static_cast<const E*>(p.residual) + row * p.ldr : nullptr;
-        E* total = p.total ? static_cast<E*>(p.total) + row * p.ldt : nullptr;
         V in[CHUNKS], add[CHUNKS], weight[CHUNKS], bias[CHUNKS];
+        // (what is not given has values that change nothing: branches in the arithmetic would keep what they choose from
+        // in registers, both chunks' at once)
+        auto read = [&](V (&to)[CHUNKS], const void* from, int64_t ld, float instead) {
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) {
-            const int64_t chunk = lane + c * WAVES * kWave, left = p.cols - chunk * 8;
-            in[c].template load<WHOLE>(x + chunk * 8, left);
-        }
-        if (p.residual) {
+            for (int c = 0; c < CHUNKS; ++c) to[c] = all8<V>(instead);
+            if (from) {
 #pragma unroll
-            for (int c = 0; c < CHUNKS; ++c) {
-                const int64_t chunk = lane + c * WAVES * kWave;
-                add[c].template load<WHOLE>(residual + chunk * 8, p.cols - chunk * 8);
+                for (int c = 0; c < CHUNKS; ++c)
+                    to[c].template load_at<WHOLE>(static_cast<const E*>(from) + row * ld, column(c), cols);
             }
-        }
-        if (p.weight) {
-#pragma unroll
-            for (int c = 0; c < CHUNKS; ++c) {
-                const int64_t chunk = lane + c * WAVES * kWave;
-                weight[c].template load<WHOLE>(static_cast<const E*>(p.weight) + chunk * 8, p.cols - chunk * 8);
-            }
-        }
-        if (p.bias) {
-#pragma unroll
-            for (int c = 0; c < CHUNKS; ++c) {
-                const int64_t chunk = lane + c * WAVES * kWave;
-                bias[c].template load<WHOLE>(static_cast<const E*>(p.bias) + chunk * 8, p.cols - chunk * 8);
-            }
-        }
+        };
+        read(in, p.x, p.ldx, 0.0f);
+        read(add, p.residual, p.ldr, 0.0f);
+        read(weight, p.weight, 0, 1.0f);
+        read(bias, p.bias, 0, 0.0f);
         float t[CHUNKS][8], sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
-            const int64_t chunk = lane + c * WAVES * kWave, left = p.cols - chunk * 8;
             in[c].widen(t[c]);
             if (p.total) {
-                if (p.dropout.drop) drop8(p.dropout, offset, (uint64_t)(row * chunks + chunk), t[c]);
-                if (p.residual) {
-                    float r[8];
-                    add[c].widen(r);
+                if (p.dropout.drop) drop8(p.dropout, offset, (uint64_t)(row * chunks + column(c) / 8), t[c]);
+                float r[8];
+                add[c].widen(r);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) t[c][e] += r[e];
-                }
+                for (int e = 0; e < 8; ++e) t[c][e] += r[e];
                 const V kept = V::narrow(t[c]);
-                kept.template store<WHOLE>(total + chunk * 8, left);
+                kept.template store_at<WHOLE>(static_cast<E*>(p.total) + row * p.ldt, column(c), cols);
                 kept.widen(t[c]);
             }
 #pragma unroll
@@ -159,7 +147,7 @@ __global__ __launch_bounds__(Shape::THREADS) void norm_kernel(NormProblem p) {
         float off[2] = {0.0f, 0.0f};  // sums of the deviations and of their squares
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
-            const int64_t left = p.cols - (lane + c * WAVES * kWave) * 8;
+            const int left = cols - column(c);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 t[c][e] -= near;
@@ -174,20 +162,14 @@ __global__ __launch_bounds__(Shape::THREADS) void norm_kernel(NormProblem p) {
             if (p.mean) p.mean[row] = s.mean;
             if (p.rstd) p.rstd[row] = s.rstd;
         }
-        E* y = static_cast<E*>(p.y) + row * p.ldy;
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
-            const int64_t chunk = lane + c * WAVES * kWave, left = p.cols - chunk * 8;
             float w[8], b[8];
-            if (p.weight) weight[c].widen(w);
-            if (p.bias) bias[c].widen(b);
+            weight[c].widen(w);
+            bias[c].widen(b);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                t[c][e] = (t[c][e] - s.shift) * s.rstd;
-                if (p.weight) t[c][e] *= w[e];
-                if (p.bias) t[c][e] += b[e];
-            }
-            V::narrow(t[c]).template store<WHOLE>(y + chunk * 8, left);
+            for (int e = 0; e < 8; ++e) t[c][e] = (t[c][e] - s.shift) * s.rstd * w[e] + b[e];
+            V::narrow(t[c]).template store_at<WHOLE>(static_cast<E*>(p.y) + row * p.ldy, column(c), cols);
         }
     }
 }
@@ -212,19 +194,19 @@ __global__ __launch_bounds__(kWideThreads) void norm_wide_kernel(NormProblem p) 
         V v;
         for (int64_t chunk = threadIdx.x; chunk < chunks; chunk += kWideThreads) {
             const int64_t left = p.cols - chunk * 8;
-            v.template load<false>(x + chunk * 8, left);
+            v.load(x + chunk * 8, left);
             v.widen(t);
             if (p.total) {
                 if (p.dropout.drop) drop8(p.dropout, offset, (uint64_t)(row * chunks + chunk), t);
                 if (p.residual) {
                     float r[8];
-                    v.template load<false>(residual + chunk * 8, left);
+                    v.load(residual + chunk * 8, left);
                     v.widen(r);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) t[e] += r[e];
                 }
                 v = V::narrow(t);
-                v.template store<false>(total + chunk * 8, left);
+                v.store(total + chunk * 8, left);
                 v.widen(t);
             }
 #pragma unroll
@@ -235,7 +217,7 @@ __global__ __launch_bounds__(kWideThreads) void norm_wide_kernel(NormProblem p) 
         const E* kept = p.total ? total : x;  // (each thread reads back what it wrote)
         for (int64_t chunk = threadIdx.x; chunk < chunks; chunk += kWideThreads) {
             const int64_t left = p.cols - chunk * 8;
-            v.template load<false>(kept + chunk * 8, left);
+            v.load(kept + chunk * 8, left);
             v.widen(t);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -253,59 +235,89 @@ __global__ __launch_bounds__(kWideThreads) void norm_wide_kernel(NormProblem p) 
         for (int64_t chunk = threadIdx.x; chunk < chunks; chunk += kWideThreads) {
             const int64_t left = p.cols - chunk * 8;
             float w[8];
-            v.template load<false>(kept + chunk * 8, left);
+            v.load(kept + chunk * 8, left);
             v.widen(t);
 #pragma unroll
             for (int e = 0; e < 8; ++e) t[e] = (t[e] - near - s.shift) * s.rstd;
             if (p.weight) {
-                v.template load<false>(static_cast<const E*>(p.weight) + chunk * 8, left);
+                v.load(static_cast<const E*>(p.weight) + chunk * 8, left);
                 v.widen(w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) t[e] *= w[e];
             }
             if (p.bias) {
-                v.template load<false>(static_cast<const E*>(p.bias) + chunk * 8, left);
+                v.load(static_cast<const E*>(p.bias) + chunk * 8, left);
                 v.widen(w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) t[e] += w[e];
             }
-            V::narrow(t).template store<false>(static_cast<E*>(p.y) + row * p.ldy + chunk * 8, left);
+            V::narrow(t).store(static_cast<E*>(p.y) + row * p.ldy + chunk * 8, left);
         }
     }
 }
 
 // ---- gradients ------------------------------------------------------------------------
 // Eight columns of one row's results: dtotal and, through the mask, dx.
-template <int TYPE, bool WHOLE>
-__device__ inline void norm_grad_store(const NormProblem& p, uint64_t offset, int64_t row, int64_t chunk, float (&d)[8]) {
+// `store(matrix's row, values)` stores them.
+template <int TYPE, class Store>
+__device__ inline void norm_grad_store(const NormProblem& p, uint64_t offset, int64_t row, int64_t chunk, float (&d)[8],
+                                       Store store) {
     using V = Values8<TYPE>;
     using E = typename V::element;
-    const int64_t left = p.cols - chunk * 8;
-    if (p.dtotal) V::narrow(d).template store<WHOLE>(static_cast<E*>(p.dtotal) + row * p.lddt + chunk * 8, left);
+    if (p.dtotal) store(static_cast<E*>(p.dtotal) + row * p.lddt, V::narrow(d));
     if (p.dx) {
         if (p.dropout.drop) drop8(p.dropout, offset, (uint64_t)(row * ((p.cols + 7) / 8) + chunk), d);
-        V::narrow(d).template store<WHOLE>(static_cast<E*>(p.dx) + row * p.lddx + chunk * 8, left);
+        store(static_cast<E*>(p.dx) + row * p.lddx, V::narrow(d));
     }
 }
 
 template <int TYPE, class Shape, bool WHOLE>
-__global__ __launch_bounds__(Shape::THREADS) void norm_grad_kernel(NormProblem p) {
+__global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void norm_grad_kernel(NormProblem p) {
     using V = Values8<TYPE>;
     using E = typename V::element;
     constexpr int WAVES = Shape::WAVES, CHUNKS = Shape::CHUNKS;
     __shared__ float shared[2][WAVES][2];
-    const int lane = threadIdx.x % (WAVES * kWave), part = threadIdx.x / (WAVES * kWave);
+    const int lane = threadIdx.x % (WAVES * kWave), cols = (int)p.cols;
+    const int part = __builtin_amdgcn_readfirstlane(threadIdx.x / (WAVES * kWave));
     const uint64_t offset = p.dropout.drop ? dropout_offset(p.dropout) : 0;
-    const float each = 1.0f / (float)p.cols;
-    auto column = [&](int c) { return (int64_t)(lane + c * WAVES * kWave); };  // (in chunks of eight)
+    const float each = 1.0f / (float)cols;
+    auto column = [&](int c) { return (lane + c * WAVES * kWave) * 8; };
+    // (as in norm_kernel, what is not given has values that change nothing)
     V weight[CHUNKS];
 #pragma unroll
-    for (int c = 0; c < CHUNKS; ++c)
-        if (p.weight) weight[c].template load<WHOLE>(static_cast<const E*>(p.weight) + column(c) * 8, p.cols - column(c) * 8);
+    for (int c = 0; c < CHUNKS; ++c) weight[c] = all8<V>(1.0f);
+    if (p.weight) {
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) weight[c].template load_at<WHOLE>(static_cast<const E*>(p.weight), column(c), cols);
+    }
+    // The columns' sums: a lane's own, in registers or in LDS, four values an access.
+    constexpr bool IN_LDS = Shape::SUMS_IN_LDS;
+    __shared__ floatx4 held[IN_LDS ? CHUNKS * 4 : 1][IN_LDS ? Shape::THREADS : 1];
     float dweight[CHUNKS][8] = {}, dbias[CHUNKS][8] = {};
+    auto keep = [&](int c) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            held[4 * c + h][threadIdx.x] = floatx4{dweight[c][4 * h], dweight[c][4 * h + 1], dweight[c][4 * h + 2], dweight[c][4 * h + 3]};
+            held[4 * c + 2 + h][threadIdx.x] = floatx4{dbias[c][4 * h], dbias[c][4 * h + 1], dbias[c][4 * h + 2], dbias[c][4 * h + 3]};
+        }
+    };
+    auto fetch = [&](int c) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const floatx4 w = held[4 * c + h][threadIdx.x], b = held[4 * c + 2 + h][threadIdx.x];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                dweight[c][4 * h + e] = w[e];
+                dbias[c][4 * h + e] = b[e];
+            }
+        }
+    };
+    if constexpr (IN_LDS) {
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) keep(c);
+    }
     const int64_t step = (int64_t)gridDim.x * Shape::ROWS;
     int at = 0;
-    // The next row is read before this one's sums are joined, so that loads are under way throughout.
     struct RowReads {
         V dy[CHUNKS], total[CHUNKS], stream[CHUNKS];
         float mean, rstd;
@@ -313,58 +325,68 @@ __global__ __launch_bounds__(Shape::THREADS) void norm_grad_kernel(NormProblem p
     auto read = [&](RowReads& r, int64_t row) {
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
-            const int64_t left = p.cols - column(c) * 8;
-            r.dy[c].template load<WHOLE>(static_cast<const E*>(p.y) + row * p.ldy + column(c) * 8, left);
-            r.total[c].template load<WHOLE>(static_cast<const E*>(p.total) + row * p.ldt + column(c) * 8, left);
+            r.dy[c].template load_at<WHOLE>(static_cast<const E*>(p.y) + row * p.ldy, column(c), cols);
+            r.total[c].template load_at<WHOLE>(static_cast<const E*>(p.total) + row * p.ldt, column(c), cols);
         }
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) r.stream[c] = all8<V>(0.0f);
         if (p.dstream) {
 #pragma unroll
             for (int c = 0; c < CHUNKS; ++c)
-                r.stream[c].template load<WHOLE>(static_cast<const E*>(p.dstream) + row * p.lds + column(c) * 8,
-                                                 p.cols - column(c) * 8);
+                r.stream[c].template load_at<WHOLE>(static_cast<const E*>(p.dstream) + row * p.lds, column(c), cols);
         }
         r.mean = p.mean[row];
         r.rstd = p.rstd[row];
     };
+    // The next row is read before this one's sums are joined, so that loads are under way throughout.  For the
+    // registers' sake a row stays as it was read, and what the sums and the results need of it is computed twice.
     int64_t row = (int64_t)blockIdx.x * Shape::ROWS + part;
     RowReads next;
     if (row < p.rows) read(next, row);
     for (; row < p.rows; row += step) {
-        const RowReads now = next;
+        RowReads now = next;
         if (row + step < p.rows) read(next, row + step);
         const float mean = now.mean, rstd = now.rstd;
-        float g[CHUNKS][8], u[CHUNKS][8], sums[2] = {0.0f, 0.0f};
+        float sums[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
-            const int64_t left = p.cols - column(c) * 8;
-            float w[8];
-            now.dy[c].widen(g[c]);
-            now.total[c].widen(u[c]);
-            if (p.weight) weight[c].widen(w);
+            const int left = cols - column(c);
+            float g[8], u[8], w[8];
+            now.dy[c].widen(g);
+            now.total[c].widen(u);
+            weight[c].afresh();
+            weight[c].widen(w);
+            if constexpr (IN_LDS) fetch(c);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 // (past the row dy is zero, and u finite)
-                u[c][e] = (WHOLE ? left > 0 : e < left) ? (u[c][e] - mean) * rstd : 0.0f;
-                dweight[c][e] += g[c][e] * u[c][e];
-                dbias[c][e] += g[c][e];
-                if (p.weight) g[c][e] *= w[e];
-                sums[0] += g[c][e];
-                sums[1] += g[c][e] * u[c][e];
+                u[e] = (WHOLE ? left > 0 : e < left) ? (u[e] - mean) * rstd : 0.0f;
+                dweight[c][e] += g[e] * u[e];
+                dbias[c][e] += g[e];
+                g[e] *= w[e];
+                sums[0] += g[e];
+                sums[1] += g[e] * u[e];
             }
+            if constexpr (IN_LDS) keep(c);
         }
         row_sums<WAVES, 2>(sums, shared, at);
         at ^= 1;
         const float m = sums[0] * each, mu = sums[1] * each;
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
-            float add[8];
-            if (p.dstream) now.stream[c].widen(add);
+            float g[8], u[8], w[8], add[8];
+            now.dy[c].afresh();
+            now.total[c].afresh();
+            weight[c].afresh();
+            now.dy[c].widen(g);
+            now.total[c].widen(u);
+            weight[c].widen(w);
+            now.stream[c].widen(add);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                g[c][e] = (g[c][e] - m - u[c][e] * mu) * rstd;
-                if (p.dstream) g[c][e] += add[e];
-            }
-            if (p.cols > column(c) * 8) norm_grad_store<TYPE, WHOLE>(p, offset, row, column(c), g[c]);
+            for (int e = 0; e < 8; ++e) g[e] = (g[e] * w[e] - m - (u[e] - mean) * rstd * mu) * rstd + add[e];
+            if (column(c) < cols)
+                norm_grad_store<TYPE>(p, offset, row, column(c) / 8, g,
+                                      [&](E* to, const V& v) { v.template store_at<WHOLE>(to, column(c), cols); });
         }
     }
     if (!p.partial) return;
@@ -375,8 +397,8 @@ __global__ __launch_bounds__(Shape::THREADS) void norm_grad_kernel(NormProblem p
         for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                sums[part][0][column(c) * 8 + e] = dweight[c][e];
-                sums[part][1][column(c) * 8 + e] = dbias[c][e];
+                sums[part][0][column(c) + e] = dweight[c][e];
+                sums[part][1][column(c) + e] = dbias[c][e];
             }
         __syncthreads();
         for (int i = threadIdx.x; i < 2 * Shape::COLS; i += Shape::THREADS) {
@@ -384,16 +406,17 @@ __global__ __launch_bounds__(Shape::THREADS) void norm_grad_kernel(NormProblem p
             float v = 0.0f;
 #pragma unroll
             for (int r = 0; r < Shape::ROWS; ++r) v += sums[r][which][col];
-            if (col < p.cols) p.partial[((int64_t)which * p.places + blockIdx.x) * p.cols + col] = v;
+            if (col < cols) p.partial[((int64_t)which * p.places + blockIdx.x) * p.cols + col] = v;
         }
     } else {
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
-            const int64_t left = p.cols - column(c) * 8;
-            float* to = p.partial + (int64_t)blockIdx.x * p.cols + column(c) * 8;
+            const int left = cols - column(c);
+            float* to = p.partial + (int64_t)blockIdx.x * p.cols;
+            if constexpr (IN_LDS) fetch(c);
             if (left > 0) {
-                store8(to, dweight[c], WHOLE ? 8 : left);
-                store8(to + (int64_t)p.places * p.cols, dbias[c], WHOLE ? 8 : left);
+                store8(to + column(c), dweight[c], WHOLE ? 8 : left);
+                store8(to + (int64_t)p.places * p.cols + column(c), dbias[c], WHOLE ? 8 : left);
             }
         }
     }
@@ -441,15 +464,15 @@ __global__ __launch_bounds__(kWideThreads) void norm_grad_wide_kernel(NormProble
         float sums[2] = {0.0f, 0.0f}, g[8], u[8];
         auto read = [&](int64_t chunk, int64_t left) {
             V v;
-            v.template load<false>(static_cast<const E*>(p.y) + row * p.ldy + chunk * 8, left);
+            v.load(static_cast<const E*>(p.y) + row * p.ldy + chunk * 8, left);
             v.widen(g);
-            v.template load<false>(static_cast<const E*>(p.total) + row * p.ldt + chunk * 8, left);
+            v.load(static_cast<const E*>(p.total) + row * p.ldt + chunk * 8, left);
             v.widen(u);
 #pragma unroll
             for (int e = 0; e < 8; ++e) u[e] = e < left ? (u[e] - mean) * rstd : 0.0f;
             if (p.weight) {
                 float w[8];
-                v.template load<false>(static_cast<const E*>(p.weight) + chunk * 8, left);
+                v.load(static_cast<const E*>(p.weight) + chunk * 8, left);
                 v.widen(w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) g[e] *= w[e];
@@ -474,12 +497,12 @@ __global__ __launch_bounds__(kWideThreads) void norm_grad_wide_kernel(NormProble
             if (p.dstream) {
                 V v;
                 float add[8];
-                v.template load<false>(static_cast<const E*>(p.dstream) + row * p.lds + chunk * 8, left);
+                v.load(static_cast<const E*>(p.dstream) + row * p.lds + chunk * 8, left);
                 v.widen(add);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) g[e] += add[e];
             }
-            norm_grad_store<TYPE, false>(p, offset, row, chunk, g);
+            norm_grad_store<TYPE>(p, offset, row, chunk, g, [&](E* to, const V& v) { v.store(to + chunk * 8, left); });
         }
     }
 }
@@ -497,9 +520,9 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(NormProblem p) {
         const float mean = p.mean[row], rstd = p.rstd[row];
         V v;
         float d[8], u[8];
-        v.template load<false>(static_cast<const E*>(p.y) + row * p.ldy + chunk * 8, left);
+        v.load(static_cast<const E*>(p.y) + row * p.ldy + chunk * 8, left);
         v.widen(d);
-        v.template load<false>(static_cast<const E*>(p.total) + row * p.ldt + chunk * 8, left);
+        v.load(static_cast<const E*>(p.total) + row * p.ldt + chunk * 8, left);
         v.widen(u);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -538,8 +561,9 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutProblem p) {
         const int64_t row = p.rows == 1 ? 0 : total <= 0xffffffff ? (int64_t)((uint32_t)i / (uint32_t)chunks) : i / chunks;
         const int64_t chunk = i - row * chunks, left = p.cols - chunk * 8;
         V in, add;
-        in.template load<WHOLE>(static_cast<const E*>(p.x) + row * p.ldx + chunk * 8, left);
-        if (p.residual) add.template load<WHOLE>(static_cast<const E*>(p.residual) + row * p.ldr + chunk * 8, left);
+        const int64_t inside = WHOLE ? 8 : left;
+        in.load(static_cast<const E*>(p.x) + row * p.ldx + chunk * 8, inside);
+        if (p.residual) add.load(static_cast<const E*>(p.residual) + row * p.ldr + chunk * 8, inside);
         float v[8];
         in.widen(v);
         if (p.dropout.drop) drop8(p.dropout, offset, (uint64_t)i, v);
@@ -549,7 +573,7 @@ __global__ __launch_bounds__(256) void dropout_kernel(DropoutProblem p) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += r[e];
         }
-        V::narrow(v).template store<WHOLE>(static_cast<E*>(p.y) + row * p.ldy + chunk * 8, left);
+        V::narrow(v).store(static_cast<E*>(p.y) + row * p.ldy + chunk * 8, inside);
     }
 }
 

@@ -36,7 +36,8 @@ def stream():
 # rows, cols, pitch beyond the width, first element's place
 SIZES = [(1, 1, 0, 0), (3, 7, 2, 1), (5, 64, 0, 0), (17, 512, 8, 8), (16, 513, 0, 1), (9, 1024, 0, 0), (6, 1025, 1, 0),
          (7, 2048, 0, 3), (5, 2056, 0, 0), (12, 4096, 0, 0), (4, 4099, 3, 1), (3, 8192, 0, 0), (2, 8193, 0, 0),
-         (4, 16384, 16, 0), (3, 16385, 0, 1), (2, 40000, 0, 0), (1200, 24, 0, 0), (1100, 1536, 0, 0)]
+         (4, 16384, 16, 0), (3, 16385, 0, 1), (2, 40000, 0, 0), (1200, 24, 0, 0), (1100, 1536, 0, 0), (6, 8, 0, 0),
+         (9, 9, 0, 1), (5, 15, 2, 0), (3, 2049, 0, 0), (600, 8200, 0, 0), (3, 16383, 0, 1), (700, 4095, 1, 0)]
 IDS = ["x".join(map(str, s)) for s in SIZES]
 
 
