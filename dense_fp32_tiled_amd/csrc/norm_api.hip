@@ -45,15 +45,21 @@ constexpr int64_t kMostBlocks = (int64_t)1 << 21;
 
 // ---- shapes ---------------------------------------------------------------------------
 // The narrowest shape that holds a row, so that its loads, sums and results
-// stay in registers at four waves per SIMD: forward a wave of its own (no
-// barriers) up to 1024 columns, 512 of 32-bit values, then four to sixteen
-// waves with at most 16 values per lane (8 of 32 bits).  The gradient's kernel
-// holds a row, the next one and the columns' sums: 8 values per lane, and in
-// the widest shape 16 with the sums in LDS.  Rows of fewer than 8 columns and
-// of more than the widest shape go to the kernels that read a row again.
-constexpr int64_t kNarrowest = 8;
-int64_t widest(int type) { return type == GEMM_VALUE_F32 ? 8192 : 16384; }
-bool in_registers(int type, int64_t cols) { return cols >= kNarrowest && cols <= widest(type); }
+// stay in registers at four waves per SIMD or more.  Forward a wave of its own
+// up to 1024 columns (no barriers), then four or eight waves.  Eight waves with
+// twice the values per lane lead over sixteen, which leave a CU one workgroup
+// (8192 columns of 32 bits, 8192 rows: 191 against 235 us; 16384 of bf16, 4096
+// rows: 99 against 126), but for ragged rows of that width they would spill;
+// at 4096 columns of 32 bits eight waves lead over four (16384 rows: 196
+// against 204).  The gradient's kernel holds a row, the next one and the
+// columns' sums: 8 values per lane, and in the widest shapes the sums in LDS.
+// Rows of fewer than 8 columns and of more than the widest shape go to the
+// kernels that read a row again.
+constexpr int64_t kNarrowest = 8, kWidest = 16384;
+bool in_registers(int64_t cols) { return cols >= kNarrowest && cols <= kWidest; }
+bool grad_in_registers(int type, int64_t cols) {
+    return in_registers(cols) && (type != GEMM_VALUE_F32 || cols <= 8192);
+}
 
 #define DFT_SHAPE(...)                                                                          \
     if (cols <= NormShape<__VA_ARGS__>::COLS)                                                   \
@@ -68,16 +74,21 @@ int with_shape(int64_t cols, Args... args) {
         DFT_SHAPE(8, 1)
         DFT_SHAPE(16, 1, WIDE)
         if constexpr (!WIDE) { DFT_SHAPE(16, 2, true) }
-    } else if constexpr (WIDE) {
-        DFT_SHAPE(4, 1)
-        DFT_SHAPE(8, 1)
-        DFT_SHAPE(16, 1)
     } else {
         DFT_SHAPE(1, 2)
         DFT_SHAPE(4, 1)
-        DFT_SHAPE(4, 2)
+        if constexpr (WIDE) {
+            DFT_SHAPE(8, 1)
+        } else {
+            DFT_SHAPE(4, 2)
+        }
         DFT_SHAPE(8, 2)
-        DFT_SHAPE(16, 2)
+        if constexpr (WIDE) {
+            DFT_SHAPE(16, 2)
+        } else if (cols <= kWidest) {
+            return cols % 8 == 0 ? Run<TYPE, NormShape<8, 4>, true>::run(args...)
+                                 : Run<TYPE, NormShape<16, 2>, false>::run(args...);
+        }
     }
     return GEMM_ERR_TOO_LARGE;  // (not reached)
 }
@@ -116,7 +127,7 @@ struct RunGrad {
 };
 int grad_places(int type, int64_t rows, int64_t cols, int cus) {
     // rows that are read again: the columns' sums, a workgroup for every 2048 columns of a place
-    if (!in_registers(type, cols)) return (int)std::min<int64_t>(rows, 256);
+    if (!grad_in_registers(type, cols)) return (int)std::min<int64_t>(rows, 256);
     return with_type<GradPlaces>(type, cols, rows, cus);
 }
 
@@ -153,7 +164,7 @@ int run_norm(const gemm_layer_norm_args& a, hipStream_t stream) {
     p.total = const_cast<void*>(total.data); p.ldt = a.ldt;
     p.y = a.y; p.ldy = a.ldy;
     p.mean = a.mean; p.rstd = a.rstd;
-    if (in_registers(a.value_type, a.cols)) return with_type<RunNorm>(a.value_type, a.cols, (const NormProblem*)&p, stream);
+    if (in_registers(a.cols)) return with_type<RunNorm>(a.value_type, a.cols, (const NormProblem*)&p, stream);
     const dim3 grid((unsigned)std::min(a.rows, kMostBlocks));
     if (a.value_type == GEMM_VALUE_BF16) return launch(norm_wide_kernel<kInputBf16>, grid, kWideThreads, stream, p);
     if (a.value_type == GEMM_VALUE_F16) return launch(norm_wide_kernel<kInputF16>, grid, kWideThreads, stream, p);
@@ -219,7 +230,7 @@ int run_grad(const gemm_layer_norm_grad_args& a, hipStream_t stream) {
     p.places = grad_places(a.value_type, a.rows, a.cols, cus);
     p.partial = a.dweight || a.dbias ? static_cast<float*>(a.workspace) : nullptr;
     if (a.rows > 0) {
-        if (in_registers(a.value_type, a.cols))
+        if (grad_in_registers(a.value_type, a.cols))
             st = with_type<RunGrad>(a.value_type, a.cols, (const NormProblem*)&p, stream);
         else if (a.value_type == GEMM_VALUE_BF16)
             st = run_wide_grad<kInputBf16>(p, stream);

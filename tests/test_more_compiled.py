@@ -6,8 +6,8 @@ report.  CPU only: the code is cross-compiled here.
   whole 160 KiB of LDS, and their contraction loop one wait for copies, which
   leaves the four youngest under way; the shape for a single contraction tile
   keeps four waves per SIMD and 32 KiB.
-* The norm's gradient keeps the waves per SIMD that its grid counts on (16 per
-  CU).
+* The norm keeps four waves per SIMD or more, which its gradient's grid counts
+  on (16 per CU).
 * M0 belongs to the direct copies alone, and no packed fp32 instruction is
   emitted (the build disables them)."""
 
@@ -39,9 +39,9 @@ def big_kernels(names):
 
 def test_no_kernel_spills(compiled):
     _, report = compiled
-    # norm, its gradient and dropout: three types; the loss's products: two types of 8 logits' kernels of each pass and 13 of the
-    # gradients
-    assert len(report) >= 3 * (6 * 2 * 2 + 3 + 2) + 2 * (16 + 13)
+    # the norm's shapes, its gradient's, rows that are read again, dropout and the join; the loss's logits of both passes, the
+    # gradients' products with what joins their slices, and what stands around them
+    assert len(report) >= 3 * 12 + (10 + 10 + 8) + 3 * 3 + 3 * 2 + 1 + 2 * (16 + 5 + 8 + 4) + 4
     assert not {k: v["scratch"] for k, v in report.items() if v.get("scratch", 0) != 0}
 
 
@@ -58,8 +58,8 @@ def test_tiles_keep_their_occupancy(compiled):
             short += 1
         elif "linear_tile_kernel" in name:
             assert r["lds"] <= 80 * 1024 and r["occupancy"] >= 2, name
-        elif "norm_grad_kernel" in name:
-            assert r["occupancy"] >= (3 if "NormShapeILi1ELi2E" in name else 4), (name, r)
+        elif "norm_grad_kernel" in name or "norm_kernel" in name:
+            assert r["occupancy"] >= 4, (name, r)
     assert short == 2
 
 
