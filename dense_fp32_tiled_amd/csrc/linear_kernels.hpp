@@ -577,10 +577,11 @@ struct LinearShape {
 struct TilePlace {
     int64_t row, col;
 };
-__device__ inline TilePlace place_of_block(uint32_t block, uint32_t blocks, uint32_t tiles_m, uint32_t tiles_n,
-                                           uint32_t high) {
+__device__ inline uint32_t number_on_xcds(uint32_t block, uint32_t blocks) {
     const uint32_t xcd = block % 8, each = blocks / 8, more = blocks % 8;
-    const uint32_t id = xcd * each + (xcd < more ? xcd : more) + block / 8;
+    return xcd * each + (xcd < more ? xcd : more) + block / 8;
+}
+__device__ inline TilePlace place_of_number(uint32_t id, uint32_t tiles_m, uint32_t tiles_n, uint32_t high) {
     const uint32_t panel = high * tiles_n, p = id / panel, in = id % panel;
     const uint32_t rows = tiles_m - high * p < high ? tiles_m - high * p : high;
     return TilePlace{high * p + in % rows, in / rows};
@@ -684,10 +685,13 @@ struct LinearWork {
     int64_t partial_ld; //   partial + row * partial_ld + column
     bool none;          // past the last group's tiles
 };
-template <bool AK, bool BK_, int BM, int BN>
+// ON_XCDS: tiles go to the XCDs by their number; else `tile` is a place in the
+// panels' order (the caller has given consecutive ones to an XCD).
+template <bool AK, bool BK_, int BM, int BN, bool ON_XCDS = true>
 __device__ inline LinearWork linear_work(const LinearProblem& p, uint32_t tile, uint32_t tiles_m, uint32_t tiles_n,
                                          uint32_t y) {
-    const TilePlace place = place_of_block(tile, tiles_m * tiles_n, tiles_m, tiles_n, panel_rows<BM>(p));
+    const uint32_t number = ON_XCDS ? number_on_xcds(tile, tiles_m * tiles_n) : tile;
+    const TilePlace place = place_of_number(number, tiles_m, tiles_n, panel_rows<BM>(p));
     LinearWork w{place.row * BM, p.R, place.col * BN, 0, p.L, p.A, p.B, nullptr, p.C, false};
     if (p.axis == kGroupRows) {
         const GroupTile gt = find_group_tile(p.offsets, p.groups, p.R, BM, place.row);
@@ -782,6 +786,12 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
     // rows 347 -> 288, but dA of 512 rows 248 -> 269, and calls of up to 20 us 0.4 to 2 us more.
     const uint32_t tiles = tiles_m * tiles_n, total = tiles * grid_y;
     auto work_of = [&](uint32_t id) {
+        if constexpr (!LAYER) {
+            // A slice's tiles read the same rows of both operands: they go to one XCD, whose L2 then reads them once.
+            const uint32_t number = number_on_xcds(id, total);
+            return linear_work<AK, BK_, BM, BN, false>(problem_again<Problem>(), number % tiles, tiles_m, tiles_n,
+                                                       number / tiles);
+        }
         return linear_work<AK, BK_, BM, BN>(problem_again<Problem>(), id % tiles, tiles_m, tiles_n, id / tiles);
     };
     // The share of tile number id, or the next that exists (grouped rows may need fewer tiles than were counted for

@@ -244,6 +244,26 @@ def test_gradient_against_differences():
         assert abs(float(terms.sum()) - slope) <= 0.02 * float(terms.square().sum().sqrt()) + 1e-6, (float(terms.sum()), slope)
 
 
+@pytest.mark.parametrize("transposed", [False, True], ids=["columns", "rows"])
+@pytest.mark.parametrize("size", [SIZES[k] for k in (1, 5, 6, 9)], ids=lambda s: "x".join(map(str, s[:3])))
+def test_reads_only_what_was_copied(size, transposed, monkeypatch):
+    """The debug build, whose LDS holds NaN before the first copy: the same results, every tile."""
+    from dense_fp32_tiled_amd import build
+
+    M, N, K, pad, offset = size
+    a, b, t, g = problem(M, N, K, torch.bfloat16, M + N)
+    poison = dft.library(build.POISON_LIB)
+    for variant in range(dft.LINEAR_COUNT):
+        kw = dict(transposed=transposed, pad=pad, offset=offset, variant=variant)
+        clean = run_forward(a, b, t, **kw)
+        clean += run_grad(g, a, b, t, clean[1], **kw)
+        with monkeypatch.context() as patch:
+            patch.setattr(dft, "library", lambda path=None: poison)
+            dirty = run_forward(a, b, t, **kw)
+            dirty += run_grad(g, a, b, t, dirty[1], **kw)
+        assert all(torch.equal(x, y) for x, y in zip(clean, dirty)), variant
+
+
 def test_no_tokens_no_width_and_lse_alone():
     b = torch.randn(16, 50, device="cuda").bfloat16()
     a, t = torch.zeros(0, 16, device="cuda").bfloat16(), torch.zeros(0, dtype=torch.int64, device="cuda")
