@@ -21,10 +21,11 @@ __global__ __launch_bounds__(kLossJoinThreads) void loss_join_kernel(LossRowsPro
 }
 constexpr uint32_t kPrepareBlocks = 64;
 __global__ __launch_bounds__(kLossBeginThreads) void loss_begin_kernel(LossBegin p) {
-    if ((int)blockIdx.y < p.packs)
-        loss_pack(p.pack[blockIdx.y]);
-    else
+    const int job = (int)gridDim.y - p.packs;  // 1 with the rows' values, else 0
+    if ((int)blockIdx.y < job)
         loss_prepare(p.prepare, gridDim.x < kPrepareBlocks ? gridDim.x : kPrepareBlocks);
+    else
+        loss_pack(p.pack[blockIdx.y - job]);
 }
 template <int TYPE>
 __global__ __launch_bounds__(256) void loss_fold_kernel(LossFold p) {

@@ -391,14 +391,15 @@ __device__ inline void loss_pack(const LossPack& j) {
         // (64-bit divisions would take longer than the bytes)
         const int64_t to = total <= 0x7fffffff ? (int64_t)((uint32_t)i / (uint32_t)groups) : i / groups;
         const int64_t col = (i - to * groups) * 8, row = to < j.rows ? to : to - j.rows;
-        Row8 v{};
-        if (!j.targets.at || j.targets.column(row, j.words) >= 0) v = load8(j.src + row * j.ld + col, j.cols - col);
+        Row8 v = load8(j.src + row * j.ld + col, j.cols - col);  // (on its way together with the target)
+        if (j.targets.at && j.targets.column(row, j.words) < 0) v = Row8{};
         *reinterpret_cast<u32x4*>(j.dst + to * j.ldd + col) = v.w;
     }
 }
 
-// What comes before the products, in one launch: copies, and the rows' values
-// in the row of workgroups after theirs.
+// What comes before the products, in one launch: the rows' values, in the
+// first row of workgroups so that they do not begin when the copies end, and
+// copies.
 struct LossBegin {
     LossPack pack[2];
     int32_t packs;
