@@ -16,6 +16,11 @@
 // second pass over the registers, so a mean far from zero costs no digits.
 // The gradient of weight and bias is summed in registers over the rows that a
 // workgroup takes, and joined over the workgroups in a fixed order.
+//
+// Measured with the residual stream, bf16 (a large copy here runs at 5.1 TB/s):
+// 16384 x 4096 with dropout 97 us (5.5 TB/s of 537 MB), its gradients 132 us
+// (5.1 TB/s of 671 MB) and 5 us for the join; 4096 x 16384 99 and 119 us without
+// dropout; rows aligned to nothing, 16384 x 4095, 132 and 156 us.
 #pragma once
 
 #include "dropout.hpp"
@@ -95,6 +100,8 @@ __device__ inline NormStatistics norm_statistics(float near, float shift, float 
     return NormStatistics{near + shift, shift, 1.0f / sqrtf((variance < 0.0f ? 0.0f : variance) + eps)};
 }
 
+// One row at a time per Shape::WAVES waves, one workgroup per row or four: the
+// rows of the launch, rather than loads ahead, keep the memory busy.
 template <int TYPE, class Shape, bool WHOLE>
 __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void norm_kernel(NormProblem p) {
     using V = Values8<TYPE>;
@@ -271,6 +278,9 @@ __device__ inline void norm_grad_store(const NormProblem& p, uint64_t offset, in
     }
 }
 
+// A workgroup works through every gridDim.x-th row (sixteen waves per CU) and
+// keeps the columns' sums of dy u and dy; 149 us in place of 132 for 16384 x
+// 4096 without the next row's loads ahead.
 template <int TYPE, class Shape, bool WHOLE>
 __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void norm_grad_kernel(NormProblem p) {
     using V = Values8<TYPE>;
@@ -423,7 +433,8 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void norm_grad_ke
 }
 
 // dweight and dbias over the workgroups' sums: 32 columns by 32 strides of
-// places per workgroup, the strides' sums added in ascending order.
+// places per workgroup, the strides' sums added in ascending order.  512 places
+// of 4096 columns 5 us (16 columns by 64 strides 7.5: lines half used).
 constexpr int kNormJoinCols = 32, kNormJoinStrides = 32;
 __global__ __launch_bounds__(kNormJoinCols * kNormJoinStrides) void norm_join_kernel(NormProblem p) {
     __shared__ float sums[kNormJoinStrides][kNormJoinCols + 1];
@@ -549,7 +560,8 @@ struct DropoutProblem {
 
 // A thread takes a chunk of eight, or every stride-th where a launch does not
 // hold them all.  Rows that lie without gaps in whole chunks come as one row:
-// their chunks count on from row to row.
+// their chunks count on from row to row.  8192 x 16384 bf16 96-100 us (5.4-5.6
+// TB/s of 537 MB): the generator's ten rounds stay under the bytes.
 template <int TYPE, bool WHOLE>
 __global__ __launch_bounds__(256) void dropout_kernel(DropoutProblem p) {
     using V = Values8<TYPE>;

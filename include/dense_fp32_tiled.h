@@ -729,8 +729,8 @@ int gemm_dropout(int value_type, int64_t rows, int64_t cols, double p, uint64_t 
  *     dZ[t][w] = (exp(Z[t][w] - lse[t]) - (w == targets[t])) * dloss[t]
  *     dA = dZ @ B^T,   dB = A^T @ dZ
  * The gradients compute Z again, a piece of the vocabulary at a time; a piece's
- * dZ lies in the workspace, rounded to the input type (times the power of two
- * that makes the largest |dloss| about 2^14, so that fp16 holds small
+ * dZ lies in the workspace, rounded to the input type (times the factor that
+ * makes the largest |dloss| about 2^14, so that fp16 holds small
  * probabilities), and dA's sums over the pieces are fp32.
  *
  * Conventions are those at the top of this header, and:
