@@ -896,9 +896,10 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
             }
             if (T > 0) read_first(at_a, at_b);
             if constexpr (S == 1) {
-                // One contraction tile at most: nothing is copied behind it.
+                // One place: a tile is copied when the one before it has been multiplied, while the CU's other
+                // workgroups have theirs.
                 static_assert(!PERSISTENT, "a ring has more places");
-                if (T > 0)
+                for (int64_t t = 0; t < T; ++t) {
                     static_for<STEPS>([&](auto ST_) {
                         constexpr int ST = decltype(ST_)::value, NOW = ST & 1, THEN = NOW ^ 1;
                         if constexpr (ST + 1 < STEPS) {
@@ -912,6 +913,17 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void linear_tile_
                             if constexpr (ST + 1 < STEPS) af[i] = read_a.read(lds_a, 0, ST + 1, i);
                         }
                     });
+                    if (t + 1 < T) {
+                        __syncthreads();  // every wave has read the tile
+                        copy_a.issue(lds_a, 0);
+                        copy_b.issue(lds_b, 0);
+                        copy_a.next();
+                        copy_b.next();
+                        wait_vector_memory();
+                        __syncthreads();
+                        read_first(0, 0);
+                    }
+                }
             } else
             for (int64_t t = 0; t < T; ++t) {
                 // places of tile t+1

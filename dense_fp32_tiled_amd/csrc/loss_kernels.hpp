@@ -416,7 +416,7 @@ struct LossBegin {
 // so nothing is copied ahead, a workgroup's operands take 32 KiB and four
 // workgroups fit a CU, whose stores are what bounds it (the shape of two
 // stages keeps two).  32768 words by 4096, 24 tokens: 101 -> 58 us.
-constexpr int kShortRows = kDepth;
+constexpr int kShortRows = 512;
 using ShortShape = LinearShape<128, 128, 64, 64, 1, 4>;
 
 // ---- launches, one translation unit per type ------------------------------------------------
