@@ -95,9 +95,24 @@ int begin(const LossBegin& jobs, bool prepare, hipStream_t stream) {
                   kLossBeginThreads, stream, jobs);
 }
 
+// A product's plan, with kTileShort where that leads (loss_kernels.hpp): of one
+// contraction tile always, else where every CU has two of its tiles or more, up
+// to `depth` and wherever 128x128 with two places is the choice.
+constexpr int64_t kShortLogits = 704, kShortRows = 512;
+Plan with_short(Plan plan, int64_t R, int64_t C, int64_t L, int64_t depth, int variant, int cus) {
+    const int64_t tiles = ceil_div(R, ShortShape::BM) * ceil_div(C, ShortShape::BN);
+    if (variant != GEMM_LINEAR_AUTO || R <= 64 || C <= 64 || tiles > kMaxTiles || plan.splits > 1) return plan;
+    const bool many = tiles >= 2 * cus && (L <= depth || plan.tile == kTile128);
+    if (!many && L > kTileDepth) return plan;
+    plan.tile = kTileShort;
+    plan.us = 0;  // (found)
+    return plan;
+}
+
 // The tile of a piece's logits: never sliced, since its epilogue needs whole sums.
 Plan logits_plan(const LossSizes& s, int64_t words, int cus) {
-    return choose(s.M, words, s.K, 1, kGroupNone, kDirect, s.variant, 1, cus);
+    return with_short(choose(s.M, words, s.K, 1, kGroupNone, kDirect, s.variant, 1, cus), s.M, words, s.K, kShortLogits,
+                      s.variant, cus);
 }
 
 void describe_logits(LinearProblem& p, const LossSizes& s, const Matrix& a, const Matrix& b, int64_t words) {
@@ -108,7 +123,7 @@ void describe_logits(LinearProblem& p, const LossSizes& s, const Matrix& a, cons
 }
 template <class Problem>
 int launch_logits(const LossSizes& s, const Problem& p, LinearTile tile, int cus, hipStream_t stream) {
-    const TileSize size = kTileSizes[tile];
+    const TileSize size = loss_tile_size(tile);
     const uint32_t m = (uint32_t)ceil_div(p.R, size.bm), n = (uint32_t)ceil_div(p.C, size.bn);
     const bool k = s.b_transposed != 0;
     return status(s.input_type == GEMM_INPUT_BF16 ? launch_loss_bf16(p, k, tile, m, n, 1, cus, stream)
@@ -127,7 +142,7 @@ struct ForwardPlan {
     LinearTile tile;
     int64_t a_bytes, b_bytes, pieces_bytes, target_bytes, workspace;
 };
-int wave_columns(LinearTile tile) { return tile == kTile256 || tile == kTile128 ? 64 : 32; }
+int wave_columns(LinearTile tile) { return tile == kTile64 || tile == kTile32x128 ? 32 : 64; }
 
 int plan_forward(const gemm_cross_entropy_args& a, const Matrix& A, const Matrix& B, int cus, ForwardPlan* plan) {
     LossSizes s = sizes_of(a);
@@ -148,7 +163,7 @@ int plan_forward(const gemm_cross_entropy_args& a, const Matrix& A, const Matrix
     f.tile = logits.tile;
     f.width = wave_columns(f.tile);
     // (whole tiles of columns: the last one's waves past the vocabulary leave empty slots)
-    f.slots = round_up(s.N, kTileSizes[f.tile].bn) / f.width;
+    f.slots = round_up(s.N, loss_tile_size(f.tile).bn) / f.width;
     f.a_bytes = f.pack_a ? packed_bytes(A) : 0;
     f.b_bytes = f.pack_b ? packed_bytes(b_piece) : 0;
     f.pieces_bytes = round_up(f.slots * f.rows * (int64_t)sizeof(RowPiece), 256);
@@ -267,15 +282,8 @@ Plan plan_a(const LossSizes& s, int64_t words, int cus) {
     return choose(parts_of(s) * s.M, s.K, words, 1, kGroupNone, kDirect, s.variant, 0, cus);
 }
 Plan plan_b(const LossSizes& s, int64_t words, int cus) {
-    const int64_t rows = parts_of(s) * s.M;
-    // (a single contraction tile: ShortShape's tiles, unless they are more than a launch holds)
-    if (rows <= kShortRows && s.variant == GEMM_LINEAR_AUTO) {
-        const Plan plan = s.b_transposed ? choose(words, s.K, rows, 1, kGroupNone, kDirect, GEMM_LINEAR_128x128, 1, cus)
-                                         : choose(s.K, words, rows, 1, kGroupNone, kDirect, GEMM_LINEAR_128x128, 1, cus);
-        if (plan.found()) return plan;
-    }
-    return s.b_transposed ? choose(words, s.K, rows, 1, kGroupNone, kDirect, s.variant, 0, cus)
-                          : choose(s.K, words, rows, 1, kGroupNone, kDirect, s.variant, 0, cus);
+    const int64_t rows = parts_of(s) * s.M, R = s.b_transposed ? words : s.K, C = s.b_transposed ? s.K : words;
+    return with_short(choose(R, C, rows, 1, kGroupNone, kDirect, s.variant, 0, cus), R, C, rows, kShortRows, s.variant, cus);
 }
 // Slices of a product, of all of it or of its last round.
 int64_t rest_bytes(const Plan& plan, int64_t R, int64_t C, int64_t L, int cus) {
@@ -347,7 +355,7 @@ int check_grad(const gemm_cross_entropy_grad_args& a, Matrix* A, Matrix* B, Matr
 
 template <class Problem>
 int launch_product(const LossSizes& s, Problem& p, const Plan& plan, void* rest, int cus, hipStream_t stream) {
-    const TileSize size = kTileSizes[plan.tile];
+    const TileSize size = loss_tile_size(plan.tile);
     const uint32_t m = (uint32_t)ceil_div(p.R, size.bm), n = (uint32_t)ceil_div(p.C, size.bn);
     p.groups = 1; p.axis = kGroupNone; p.splits = plan.splits; p.slice = plan.slice;
     p.partial = static_cast<float*>(rest);

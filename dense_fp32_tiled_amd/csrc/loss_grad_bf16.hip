@@ -7,8 +7,6 @@ namespace dft {
 // dB, or its transpose: dZ and A both run along the output.
 hipError_t launch_loss_bf16(const LossWordsGradProblem& p, bool, LinearTile tile, uint32_t tiles_m, uint32_t tiles_n,
                            uint32_t slices, int cus, hipStream_t stream) {
-    if (tile == kTile128 && p.L <= kShortRows)
-        return launch_loss_shape<kInputBf16, false, false, ShortShape>(p, tiles_m, tiles_n, 1, cus, stream);
     const hipError_t e = launch_loss_layout<kInputBf16, false, false>(p, tile, tiles_m, tiles_n, slices, cus, stream);
     return e == hipSuccess ? launch_loss_join<kInputBf16>(p, tiles_m, tiles_n, cus, stream) : e;
 }

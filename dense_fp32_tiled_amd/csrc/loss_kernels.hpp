@@ -71,6 +71,7 @@ __device__ inline float over_columns(float x, Op op) {
 
 struct LossRowsProblem : LinearProblem {
     static constexpr int EPILOGUE = kEpilogueRows;
+    static constexpr bool SHORT = true;  // may take kTileShort
     Targets targets;
     int64_t first, words;  // the piece's first column, and columns in all
     RowPiece* pieces;      // a wave's columns of row r, slot s at pieces + s * R + r: rows of a slot lie together
@@ -241,6 +242,7 @@ __device__ inline void loss_prepare(const LossPrepare& p, uint32_t blocks) {
 constexpr int kSplitTokens = 32;
 struct LossSlopeProblem : LinearProblem {
     static constexpr int EPILOGUE = kEpilogueValues;
+    static constexpr bool SHORT = true;
     const LossRow* row;
     int64_t first;  // the piece's first column
     int64_t rest;   // bytes from a value to what was rounded off it; 0: not kept
@@ -303,10 +305,12 @@ struct EpilogueRows<LossSlopeProblem> {
 // fit the registers of the first's 256x256 kernel.)
 struct LossWordsGradProblem : LinearProblem {
     static constexpr int EPILOGUE = kEpilogueValues;
+    static constexpr bool SHORT = true;
     const float* back;
 };
 struct LossTokensGradProblem : LinearProblem {
     static constexpr int EPILOGUE = kEpilogueValues;
+    static constexpr bool SHORT = false;
     const float* before;  // or nullptr; rows before_ld apart
     int64_t before_ld;
     const float* back;    // nullptr: another piece follows
@@ -412,12 +416,21 @@ struct LossBegin {
     LossPrepare prepare;
 };
 
-// dB of few tokens, at most kShortRows rows of dZ: a single contraction tile,
-// so nothing is copied ahead, a workgroup's operands take 32 KiB and four
-// workgroups fit a CU, whose stores are what bounds it (the shape of two
-// stages keeps two).  32768 words by 4096, 24 tokens: 101 -> 58 us.
-constexpr int kShortRows = 512;
+// One more tile for short contractions: 128x128 with one place of LDS, which
+// is copied into when it has been multiplied.  Its operands take 32 KiB, so
+// four workgroups fit a CU in place of two, and one's copies, beginning and
+// epilogue pass while the others multiply.  Forward against the best of the
+// other tiles: 1094 tokens by 75472 words, 224 deep, 69 against 90 us, 5680 by
+// 40672, 480 deep, 250 against 283, but 473 by 25184, 728 deep, 36 against 33
+// and 7198 by 66880, 1512 deep, 1418 against 1250; never more than 128x128 with
+// two places where there are two tiles or more for every CU.  dB of 24 tokens
+// by 32768 words, 4096 wide, 58 against 88 us, both gradients of 512 tokens by
+// 50000 words, 1024 wide, 209 against 229.
+constexpr LinearTile kTileShort = (LinearTile)kTileCount;
 using ShortShape = LinearShape<128, 128, 64, 64, 1, 4>;
+constexpr TileSize loss_tile_size(LinearTile tile) {
+    return tile == kTileShort ? TileSize{ShortShape::BM, ShortShape::BN} : kTileSizes[tile];
+}
 
 // ---- launches, one translation unit per type ------------------------------------------------
 // `kmajor`: B's words are rows (b_transposed).

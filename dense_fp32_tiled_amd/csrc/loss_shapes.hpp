@@ -19,6 +19,8 @@ hipError_t launch_loss_shape(const Problem& p, uint32_t tiles_m, uint32_t tiles_
 template <int TYPE, bool AK, bool BK_, class Problem>
 hipError_t launch_loss_layout(const Problem& p, LinearTile tile, uint32_t tiles_m, uint32_t tiles_n, uint32_t slices,
                               int cus, hipStream_t stream) {
+    if constexpr (Problem::SHORT)
+        if (tile == kTileShort) return launch_loss_shape<TYPE, AK, BK_, ShortShape>(p, tiles_m, tiles_n, slices, cus, stream);
     switch (tile) {
         case kTile256: return launch_loss_shape<TYPE, AK, BK_, ShapeOf<kTile256>::type>(p, tiles_m, tiles_n, slices, cus, stream);
         case kTile128: return launch_loss_shape<TYPE, AK, BK_, ShapeOf<kTile128>::type>(p, tiles_m, tiles_n, slices, cus, stream);

@@ -132,7 +132,10 @@ def test_fp32_gradients_and_one_alone(kind, types):
 # sizes of whole rounds of the largest tiles: many per workgroup, a last round that is cut along the contraction, several
 # pieces, and rows longer than one step of the join
 LARGE = [(4096, 8192, 128, False, 0), (5000, 8192, 4096, True, 0), (5000, 8192, 4096, False, 2048), (2, 150000, 512, True, 0),
-         (1500, 40001, 520, False, 8192)]
+         (1500, 40001, 520, False, 8192),
+         # short contractions of many tiles: of the logits, of dB, of both; one contraction tile
+         (130, 70001, 72, False, 0), (300, 40000, 136, True, 0), (520, 14003, 200, False, 0), (520, 14000, 712, True, 0),
+         (66, 3000, 64, True, 256), (100, 900, 63, False, 0), (4, 40000, 1000, False, 0)]
 
 
 @pytest.mark.parametrize("size", LARGE, ids=lambda s: "x".join(map(str, s)))
