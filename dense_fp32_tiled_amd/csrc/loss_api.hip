@@ -24,8 +24,10 @@ __global__ __launch_bounds__(kLossBeginThreads) void loss_begin_kernel(LossBegin
     const int job = (int)gridDim.y - p.packs;  // 1 with the rows' values, else 0
     if ((int)blockIdx.y < job)
         loss_prepare(p.prepare, gridDim.x < kPrepareBlocks ? gridDim.x : kPrepareBlocks);
+    else if (p.each == 1)
+        loss_pack<1>(p.pack[blockIdx.y - job]);
     else
-        loss_pack(p.pack[blockIdx.y - job]);
+        loss_pack<kPackGroups>(p.pack[blockIdx.y - job]);
 }
 template <int TYPE>
 __global__ __launch_bounds__(256) void loss_fold_kernel(LossFold p) {
@@ -85,12 +87,13 @@ LossPack pack_job(const Matrix& from, const Matrix& to, int32_t copies, const Ta
                     static_cast<uint16_t*>(const_cast<void*>(to.data)), to.ld, copies, targets, words};
 }
 // Copies, and the rows' values if they are wanted.
-int begin(const LossBegin& jobs, bool prepare, hipStream_t stream) {
+int begin(LossBegin& jobs, bool prepare, hipStream_t stream) {
     if (jobs.packs == 0 && !prepare) return GEMM_OK;
     int64_t most = 1;
     for (int i = 0; i < jobs.packs; ++i) most = std::max(most, jobs.pack[i].copies * jobs.pack[i].rows * (jobs.pack[i].ldd / 8));
     if (prepare) most = std::max(most, std::min<int64_t>(jobs.prepare.rows, kPrepareBlocks * kLossBeginThreads));
-    return launch(loss_begin_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(most, kLossBeginThreads), 65536),
+    jobs.each = most <= kBeginBlocks * kLossBeginThreads ? 1 : kPackGroups;
+    return launch(loss_begin_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(most, kLossBeginThreads * jobs.each), 65536),
                                           (unsigned)jobs.packs + (prepare ? 1 : 0)),
                   kLossBeginThreads, stream, jobs);
 }

@@ -395,15 +395,34 @@ struct LossPack {
     Targets targets;  // at == nullptr: every row
     int64_t words;
 };
+// EACH accesses of a thread, under way together: 513 rows of 32001 odd columns
+// and 1000 of 513 take 12 us with four against 15 with one (8: 13); up to
+// kBeginBlocks workgroups, which the card holds at once, one (40 rows of 4096:
+// the call 2 us longer with four).
+constexpr int kPackGroups = 4;
+constexpr int64_t kBeginBlocks = 2048;
+template <int EACH>
 __device__ inline void loss_pack(const LossPack& j) {
     const int64_t groups = j.ldd / 8, total = j.copies * j.rows * groups;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        // (64-bit divisions would take longer than the bytes)
-        const int64_t to = total <= 0x7fffffff ? (int64_t)((uint32_t)i / (uint32_t)groups) : i / groups;
-        const int64_t col = (i - to * groups) * 8, row = to < j.rows ? to : to - j.rows;
-        Row8 v = load8(j.src + row * j.ld + col, j.cols - col);  // (on its way together with the target)
-        if (j.targets.at && j.targets.column(row, j.words) < 0) v = Row8{};
-        *reinterpret_cast<u32x4*>(j.dst + to * j.ldd + col) = v.w;
+    const int64_t span = (int64_t)kLossBeginThreads * EACH;  // a workgroup's
+    for (int64_t i0 = blockIdx.x * span + threadIdx.x; i0 < total; i0 += gridDim.x * span) {
+        Row8 v[EACH];
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) {
+            const int64_t i = i0 + k * kLossBeginThreads;
+            v[k] = Row8{};
+            if (i >= total) continue;
+            // (64-bit divisions would take longer than the bytes)
+            const int64_t to = total <= 0x7fffffff ? (int64_t)((uint32_t)i / (uint32_t)groups) : i / groups;
+            const int64_t col = (i - to * groups) * 8, row = to < j.rows ? to : to - j.rows;
+            v[k] = load8(j.src + row * j.ld + col, j.cols - col);  // (on its way together with the target)
+            if (j.targets.at && j.targets.column(row, j.words) < 0) v[k] = Row8{};
+        }
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) {  // (rows of dst lie one after the other)
+            const int64_t i = i0 + k * kLossBeginThreads;
+            if (i < total) *reinterpret_cast<u32x4*>(j.dst + i * 8) = v[k].w;
+        }
     }
 }
 
@@ -412,7 +431,7 @@ __device__ inline void loss_pack(const LossPack& j) {
 // copies.
 struct LossBegin {
     LossPack pack[2];
-    int32_t packs;
+    int32_t packs, each;
     LossPrepare prepare;
 };
 
