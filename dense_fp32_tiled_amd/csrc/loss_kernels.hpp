@@ -74,7 +74,8 @@ struct LossRowsProblem : LinearProblem {
     static constexpr bool SHORT = true;  // may take kTileShort
     Targets targets;
     int64_t first, words;  // the piece's first column, and columns in all
-    RowPiece* pieces;      // a wave's columns of row r, slot s at pieces + s * R + r: rows of a slot lie together
+    RowPiece* pieces;      // a wave's columns of row r, slot s: pieces[r * row_step + s * slot_step]
+    int64_t row_step, slot_step;
     float* at_target;      // the target's logit of each row that has one
 
     // Block i of a wave's results: row lane % 16, columns 16 j + 4 (lane / 16) + v.  Nothing overlaps this arithmetic
@@ -131,7 +132,7 @@ struct LossRowsProblem : LinearProblem {
         for (int i = 0; i < MI; ++i) {
             sum[i] = over_columns(sum[i], [](float x, float y) { return x + y; });
             const int64_t row = row0 + 16 * i + lane % 16;
-            if (row < row_end && lane < 16) pieces[slot * R + row] = RowPiece{most[i], sum[i]};
+            if (row < row_end && lane < 16) pieces[row * row_step + slot * slot_step] = RowPiece{most[i], sum[i]};
         }
         if (__ballot(any)) {
 #pragma unroll
@@ -158,16 +159,16 @@ __device__ inline void loss_join(const LossRowsProblem& p, int64_t slots, int ro
     const int64_t row = (int64_t)blockIdx.x * rows + r;
     RowPiece all{-__builtin_inff(), 0.0f};
     if (row < p.R) {
-        const RowPiece* from = p.pieces + row;
+        const RowPiece* from = p.pieces + row * p.row_step;
         int64_t s = first;
         for (; s + 3 * strides < slots; s += 4 * strides) {  // four reads under way at a time
             RowPiece four[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) four[k] = from[(s + k * strides) * p.R];
+            for (int k = 0; k < 4; ++k) four[k] = from[(s + k * strides) * p.slot_step];
 #pragma unroll
             for (int k = 0; k < 4; ++k) all = join(all, four[k]);
         }
-        for (; s < slots; s += strides) all = join(all, from[s * p.R]);
+        for (; s < slots; s += strides) all = join(all, from[s * p.slot_step]);
     }
     for (int d = rows; d < kWave; d *= 2)
         all = join(all, RowPiece{__shfl_xor(all.most, d), __shfl_xor(all.sum, d)});
