@@ -105,12 +105,16 @@ def _value_type(t, name):
 
 
 def _counter(p, seed, offset, step, device):
-    """Device pointer of step, after checks of what draws the mask."""
+    """The seed and step's device pointer, after checks of what draws the mask."""
     if not 0 <= p <= 1:
         raise ValueError(f"p must lie in [0, 1], not {p}")
+    if seed is None:
+        if p > 0:
+            raise ValueError("dropout needs a seed (calls of one seed and offset drop the same elements)")
+        seed = 0
     if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
         raise ValueError("seed and offset must be unsigned 64-bit numbers")
-    return None if step is None else pr._list(step, "step", (1,), pr.torch.int64, device)
+    return seed, None if step is None else pr._list(step, "step", (1,), pr.torch.int64, device)
 
 
 def dropout(x, p: float, seed: int, offset: int = 0, residual=None, step=None, out=None, stream=None):
@@ -126,7 +130,7 @@ def dropout(x, p: float, seed: int, offset: int = 0, residual=None, step=None, o
     rows, cols = x.shape if x.dim() == 2 else (-1, -1)
     dtype = x.dtype
     px, ldx = pr._matrix(x, "x", rows, cols, dtype, device)
-    at = _counter(p, seed, offset, step, device)
+    seed, at = _counter(p, seed, offset, step, device)
     pres, ldr = (None, 0) if residual is None else pr._matrix(residual, "residual", rows, cols, dtype, device)
     if out is None:
         out = pr.torch.empty(rows, cols, dtype=dtype, device=device)
@@ -138,14 +142,14 @@ def dropout(x, p: float, seed: int, offset: int = 0, residual=None, step=None, o
     return out
 
 
-def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, p: float = 0.0, seed: int = 0,
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, p: float = 0.0, seed: int | None = None,
                offset: int = 0, step=None, out=None, total=None, stream=None):
     """(y, NormState): each row of total = dropout(x) + residual normalised, times weight plus bias, by
     gemm_layer_norm.
 
     x, residual: rows x cols of one type; weight, bias: cols values of it.  Without residual and with p = 0, total is
     x itself; else it is rounded to the type and stored, in ``total`` if given (which may be x or residual itself).
-    p, seed, offset and step as in ``dropout``."""
+    p, seed, offset and step as in ``dropout``; a p above 0 needs the seed."""
     kind, device = _value_type(x, "x"), pr._gpu(x, "x")
     if stream is not None:
         with pr._current(stream, device):
@@ -153,7 +157,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, p: f
     rows, cols = x.shape if x.dim() == 2 else (-1, -1)
     dtype = x.dtype
     px, ldx = pr._matrix(x, "x", rows, cols, dtype, device)
-    at = _counter(p, seed, offset, step, device)
+    seed, at = _counter(p, seed, offset, step, device)
     pw = None if weight is None else pr._list(weight, "weight", (cols,), dtype, device)
     pb = None if bias is None else pr._list(bias, "bias", (cols,), dtype, device)
     empty, ld = pr.torch.empty, cols if cols > 0 else 1
@@ -183,8 +187,9 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, residual=None, p: f
     return out, NormState(total, mean, rstd)
 
 
-def layer_norm_grad(dy, state: NormState, weight=None, dtotal=None, p: float = 0.0, seed: int = 0, offset: int = 0,
-                    step=None, want=("x", "residual", "weight", "bias"), workspace=None, stream=None) -> NormGrads:
+def layer_norm_grad(dy, state: NormState, weight=None, dtotal=None, p: float = 0.0, seed: int | None = None,
+                    offset: int = 0, step=None, want=("x", "residual", "weight", "bias"), workspace=None,
+                    stream=None) -> NormGrads:
     """Gradients of layer_norm for y's gradient dy and, where total is used elsewhere too, ``dtotal``, total's
     gradient from there, by gemm_layer_norm_grad.  x's and the residual's are of dy's type (one tensor without
     dropout), weight's and bias's float32.  ``want`` names the ones computed; p, seed, offset and step are the
@@ -198,7 +203,7 @@ def layer_norm_grad(dy, state: NormState, weight=None, dtotal=None, p: float = 0
     rows, cols = dy.shape if dy.dim() == 2 else (-1, -1)
     dtype = dy.dtype
     py, ldy = pr._matrix(dy, "dy", rows, cols, dtype, device)
-    at = _counter(p, seed, offset, step, device)
+    seed, at = _counter(p, seed, offset, step, device)
     total, mean, rstd = state
     pt, ldt = pr._matrix(total, "state.total", rows, cols, dtype, device)
     pm = pr._list(mean, "state.mean", (rows,), pr._f32, device)
