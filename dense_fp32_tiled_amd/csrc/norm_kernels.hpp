@@ -95,6 +95,19 @@ __device__ inline void row_sums(float (&v)[N], float (*shared)[WAVES][N], int at
 struct NormStatistics {
     float mean, shift, rstd;
 };
+// The rounded mean that deviations are taken from.  Of 16-bit values it is cut
+// to 16 significant bits, so that values of up to 256 times its size have exact
+// deviations: from a full mean those of one exponent are all rounded the same
+// way, which put the mean off by up to two units (16 x 4096 bf16: 1.3e-7 of it
+// in the 2-norm, 3e-8 so).  The variance loses nothing by the larger shift s:
+// values on a grid of step g whose mean lies s from it have a variance of at
+// least s (g - s), and g is 64 s or more.
+template <int TYPE>
+__device__ inline float near_mean(float mean) {
+    if constexpr (TYPE == kValueF32) return mean;
+    const uint32_t bits = __builtin_bit_cast(uint32_t, mean);
+    return __builtin_bit_cast(float, (bits + 0x80u) & ~0xffu);
+}
 __device__ inline NormStatistics norm_statistics(float near, float shift, float square, float eps) {
     const float variance = square - shift * shift;
     return NormStatistics{near + shift, shift, 1.0f / sqrtf((variance < 0.0f ? 0.0f : variance) + eps)};
@@ -150,7 +163,7 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void norm_kernel(
             for (int e = 0; e < 8; ++e) sum[0] += t[c][e];  // (zeros past the row)
         }
         row_sums<WAVES, 2>(sum, shared, 0);
-        const float near = sum[0] / n;
+        const float near = near_mean<TYPE>(sum[0] / n);
         float off[2] = {0.0f, 0.0f};  // sums of the deviations and of their squares
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
@@ -220,7 +233,7 @@ __global__ __launch_bounds__(kWideThreads) void norm_wide_kernel(NormProblem p) 
             for (int e = 0; e < 8; ++e) sum[0] += e < left ? t[e] : 0.0f;
         }
         row_sums<WAVES, 2>(sum, shared, 0);
-        const float near = sum[0] / n;
+        const float near = near_mean<TYPE>(sum[0] / n);
         const E* kept = p.total ? total : x;  // (each thread reads back what it wrote)
         for (int64_t chunk = threadIdx.x; chunk < chunks; chunk += kWideThreads) {
             const int64_t left = p.cols - chunk * 8;
