@@ -553,6 +553,7 @@ struct OperandRead {
 template <class Problem>
 struct EpilogueRows {
     __device__ void load(const Problem&, int64_t, int64_t, int, int) {}
+    __device__ void load_one(const Problem&, int64_t) {}  // where a lane has one row
     __device__ void of_row(int, int) {}
     template <int TYPE>
     __device__ void finish(const Problem&, const EpilogueBase&, const EpilogueLane&, int64_t, int64_t, int64_t,
@@ -1150,8 +1151,11 @@ __global__ __launch_bounds__(kJoinThreads) void linear_join_kernel(Problem p) {
         if (slice0 == 0 && left > 0) {
             if constexpr (Problem::EPILOGUE == kEpilogueLayer)
                 epilogue8<TYPE>(p.ep, bias, residual, base, none, left, z);
-            else
-                EpilogueRows<Problem>{}.template finish<TYPE>(p, base, none, row, col, left, z);
+            else {
+                EpilogueRows<Problem> values;
+                values.load_one(p, row);
+                values.template finish<TYPE>(p, base, none, row, col, left, z);
+            }
         }
     }
 }
@@ -1189,8 +1193,11 @@ __global__ __launch_bounds__(256) void linear_tail_kernel(Problem p, uint32_t ti
         }
         if constexpr (Problem::EPILOGUE == kEpilogueLayer)
             epilogue8<TYPE>(p.ep, bias, residual, base, none, left, z);
-        else
-            EpilogueRows<Problem>{}.template finish<TYPE>(p, base, none, row, col, left, z);
+        else {
+            EpilogueRows<Problem> values;
+            values.load_one(p, row);
+            values.template finish<TYPE>(p, base, none, row, col, left, z);
+        }
     }
 }
 

@@ -19,11 +19,16 @@ __global__ __launch_bounds__(kLossJoinThreads) void loss_join_kernel(LossRowsPro
                                                                      float* loss, float* lse) {
     loss_join(p, slots, rows, loss, lse);
 }
-constexpr uint32_t kPrepareBlocks = 64;
+// Workgroups for the rows' values: a row to each thread, of fp16 to each wave.
+uint32_t prepare_blocks(const LossPrepare& p) {
+    const int64_t blocks = p.A ? std::min<int64_t>((p.rows + kLossBeginWaves - 1) / kLossBeginWaves, kMostLifts)
+                               : std::min<int64_t>((p.rows + kLossBeginThreads - 1) / kLossBeginThreads, 64);
+    return (uint32_t)std::max<int64_t>(blocks, 1);
+}
 __global__ __launch_bounds__(kLossBeginThreads) void loss_begin_kernel(LossBegin p) {
     const int job = (int)gridDim.y - p.packs;  // 1 with the rows' values, else 0
     if ((int)blockIdx.y < job)
-        loss_prepare(p.prepare, gridDim.x < kPrepareBlocks ? gridDim.x : kPrepareBlocks);
+        loss_prepare(p.prepare, p.prepare_blocks);
     else if (p.each == 1)
         loss_pack<1>(p.pack[blockIdx.y - job]);
     else
@@ -84,14 +89,18 @@ int check_sizes(const LossSizes& s) {
 
 LossPack pack_job(const Matrix& from, const Matrix& to, int32_t copies, const Targets& targets, int64_t words) {
     return LossPack{static_cast<const uint16_t*>(from.data), from.rows, from.cols, from.ld,
-                    static_cast<uint16_t*>(const_cast<void*>(to.data)), to.ld, copies, targets, words};
+                    static_cast<uint16_t*>(const_cast<void*>(to.data)), to.ld, copies, targets, words, nullptr, nullptr,
+                    0, nullptr};
 }
 // Copies, and the rows' values if they are wanted.
 int begin(LossBegin& jobs, bool prepare, hipStream_t stream) {
     if (jobs.packs == 0 && !prepare) return GEMM_OK;
     int64_t most = 1;
     for (int i = 0; i < jobs.packs; ++i) most = std::max(most, jobs.pack[i].copies * jobs.pack[i].rows * (jobs.pack[i].ldd / 8));
-    if (prepare) most = std::max(most, std::min<int64_t>(jobs.prepare.rows, kPrepareBlocks * kLossBeginThreads));
+    if (prepare) {
+        jobs.prepare_blocks = prepare_blocks(jobs.prepare);  // (fewer than the grid has, also with kPackGroups)
+        most = std::max(most, (int64_t)jobs.prepare_blocks * kLossBeginThreads);
+    }
     jobs.each = most <= kBeginBlocks * kLossBeginThreads ? 1 : kPackGroups;
     return launch(loss_begin_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(most, kLossBeginThreads * jobs.each), 65536),
                                           (unsigned)jobs.packs + (prepare ? 1 : 0)),
@@ -265,18 +274,21 @@ int run_forward(const gemm_cross_entropy_args& a, hipStream_t stream) {
 }
 
 // ---- gradients ----------------------------------------------------------------------------
-// In the workspace: the rows' values and the scale, A packed (always: rows
-// without a target are zeros in it), a piece of B packed, a piece's dZ, dA's
-// sums over the pieces, and the slices of the product that runs.
+// In the workspace: the rows' values, the scale and the lifts, A packed (always:
+// rows without a target are zeros in it), in fp16 A's rows times their powers
+// for dB, a piece of B packed, a piece's dZ, dA's sums over the pieces, and the
+// slices of the product that runs.
 struct GradPlan {
     bool pack_b, a_held;
+    bool shifted;   // dZ's rows have powers of two of their own (fp16)
     int parts;      // dZ's: 2 for few tokens
     int64_t rows;   // of dZ: tokens times parts
     int64_t piece;
     LinearTile tile;
     Plan a, b;  // the gradients' products of a whole piece
-    int64_t rows_bytes, a_bytes, b_bytes, slope_bytes, held_bytes, rest_bytes, workspace;
+    int64_t rows_bytes, a_bytes, shifted_bytes, b_bytes, slope_bytes, held_bytes, rest_bytes, workspace;
 };
+constexpr int64_t kLiftBytes = kMostLifts * 4;
 // Words of a piece: dZ of 512 MiB, so that a piece is many rounds of tiles and
 // dA's sums are read and written again a few times only, and for many tokens
 // still 4096 words.
@@ -304,6 +316,7 @@ int plan_grad(const gemm_cross_entropy_grad_args& a, const Matrix& A, const Matr
     g = GradPlan{};
     g.parts = parts_of(s);
     g.rows = g.parts * s.M;
+    g.shifted = s.input_type == GEMM_INPUT_F16;
     g.pack_b = s.K > 0 && !whole_rows(B);
     g.piece = s.piece > 0 ? s.piece : words_at_once(s.M);
     if (s.piece == 0 && g.pack_b)  // (what is packed counts too, four times over: it is not used again)
@@ -323,8 +336,9 @@ int plan_grad(const gemm_cross_entropy_grad_args& a, const Matrix& A, const Matr
     if (!logits.found() || !g.a.found() || !g.b.found()) return GEMM_ERR_TOO_LARGE;
     g.tile = logits.tile;
     g.a_held = a.dA && (s.N > g.piece || g.parts > 1);
-    g.rows_bytes = round_up(s.M * (int64_t)sizeof(LossRow), 256) + 256;
-    g.a_bytes = packed_bytes(a_read);
+    g.rows_bytes = round_up(s.M * (int64_t)sizeof(LossRow), 256) + 256 + kLiftBytes;
+    g.a_bytes = packed_bytes(g.shifted ? packed(A) : a_read);
+    g.shifted_bytes = g.shifted && a.dB ? packed_bytes(a_read) : 0;
     g.b_bytes = g.pack_b ? packed_bytes(b_piece) : 0;
     g.slope_bytes = packed_bytes(slope);
     g.held_bytes = g.a_held ? round_up(g.rows * s.K * 4, 256) : 0;
@@ -337,7 +351,7 @@ int plan_grad(const gemm_cross_entropy_grad_args& a, const Matrix& A, const Matr
             g.rest_bytes = std::max(g.rest_bytes, rest_bytes(plan_b(s, words, cus), R, C, g.rows, cus));
         }
     }
-    g.workspace = g.rows_bytes + g.a_bytes + g.b_bytes + g.slope_bytes + g.held_bytes + g.rest_bytes;
+    g.workspace = g.rows_bytes + g.a_bytes + g.shifted_bytes + g.b_bytes + g.slope_bytes + g.held_bytes + g.rest_bytes;
     return GEMM_OK;
 }
 
@@ -390,17 +404,27 @@ int run_grad(const gemm_cross_entropy_grad_args& a, hipStream_t stream) {
     const Targets targets{a.targets, a.target_type == GEMM_TARGET_I64};
     Space space{static_cast<char*>(a.workspace)};
     char* const rows = static_cast<char*>(space.take(g.rows_bytes));
-    float* const back = reinterpret_cast<float*>(rows + g.rows_bytes - 256);
+    LossBack* const back = reinterpret_cast<LossBack*>(rows + g.rows_bytes - kLiftBytes - 256);
+    int32_t* const lifts = reinterpret_cast<int32_t*>(rows + g.rows_bytes - kLiftBytes);
+    const LossRow* const row = reinterpret_cast<const LossRow*>(rows);
     Matrix x = packed(A);
     x.data = space.take(g.a_bytes);
+    Matrix by_tokens = x;  // what dB's sum over the tokens reads
+    if (g.shifted) by_tokens.data = space.take(g.shifted_bytes);
     void* const b_space = space.take(g.b_bytes);
     void* const slopes = space.take(g.slope_bytes);
     float* const held = static_cast<float*>(space.take(g.held_bytes));
     void* const rest = space.take(g.rest_bytes);
     LossBegin jobs{};
-    jobs.prepare = LossPrepare{s.M, s.N, targets, a.lse, a.dloss, reinterpret_cast<LossRow*>(rows), back};
-    jobs.pack[jobs.packs++] = pack_job(A, x, g.parts, targets, s.N);
-    x.rows = g.rows;
+    jobs.prepare = LossPrepare{s.M, s.N, targets, a.lse, a.dloss, reinterpret_cast<LossRow*>(rows), back, nullptr, 0, 0,
+                               lifts};
+    if (g.shifted) {
+        jobs.prepare.A = static_cast<const uint16_t*>(A.data);
+        jobs.prepare.lda = A.ld;
+        jobs.prepare.width = s.K;
+    }
+    jobs.pack[jobs.packs++] = pack_job(A, x, g.shifted ? 1 : g.parts, targets, s.N);
+    by_tokens.rows = g.rows;
     for (int64_t first = 0; first < s.N; first += g.piece) {
         const int64_t words = std::min(g.piece, s.N - first);
         Matrix b = piece_of(B, kmajor, first, words);
@@ -412,12 +436,21 @@ int run_grad(const gemm_cross_entropy_grad_args& a, hipStream_t stream) {
         }
         if ((st = begin(jobs, first == 0, stream)) != GEMM_OK) return st;
         jobs.packs = 0;
+        if (first == 0 && g.shifted && a.dB) {
+            LossBegin shift{};
+            LossPack& job = shift.pack[shift.packs++] = pack_job(A, by_tokens, g.parts, targets, s.N);
+            job.row = row;
+            job.lifts = lifts;
+            job.count = s.M > 0 ? (int32_t)prepare_blocks(jobs.prepare) : 0;
+            job.back = back;
+            if ((st = begin(shift, false, stream)) != GEMM_OK) return st;
+        }
         const Matrix z{slopes, g.rows, words, round_up(words, 8), 2};
         if (s.M > 0) {
             LossSlopeProblem p{};
             describe_logits(p, s, x, b, words);
             p.ep.out = slopes; p.ep.ldo = z.ld;
-            p.row = reinterpret_cast<const LossRow*>(rows);
+            p.row = row;
             p.first = first;
             p.rest = g.parts > 1 ? s.M * z.ld * 2 : 0;
             if ((st = launch_logits(s, p, g.tile, cus, stream)) != GEMM_OK) return st;
@@ -425,7 +458,7 @@ int run_grad(const gemm_cross_entropy_grad_args& a, hipStream_t stream) {
         if (a.dB) {
             const Matrix out = piece_of(dB, kmajor, first, words);
             LossWordsGradProblem p{};
-            const Matrix &left = kmajor ? z : x, &right = kmajor ? x : z;
+            const Matrix &left = kmajor ? z : by_tokens, &right = kmajor ? by_tokens : z;
             p.R = kmajor ? words : s.K; p.C = kmajor ? s.K : words; p.L = g.rows;
             p.A = static_cast<const uint16_t*>(left.data); p.lda = left.ld;
             p.B = static_cast<const uint16_t*>(right.data); p.ldb = right.ld;
@@ -442,6 +475,7 @@ int run_grad(const gemm_cross_entropy_grad_args& a, hipStream_t stream) {
             p.B = static_cast<const uint16_t*>(b.data); p.ldb = b.ld;
             p.before = first > 0 ? held : nullptr; p.before_ld = s.K;
             p.back = last ? back : nullptr;
+            p.row = last && g.shifted ? row : nullptr;
             p.ep.out = last ? a.dA : held; p.ep.ldo = last ? a.ldda : s.K;
             p.ep.out_f32 = !last || a.a_grad_type == GEMM_OUTPUT_F32;
             st = launch_product(s, p, plan_a(s, words, cus), rest, cus, stream);
@@ -449,7 +483,7 @@ int run_grad(const gemm_cross_entropy_grad_args& a, hipStream_t stream) {
         }
     }
     if (!a.dA || s.M == 0 || g.parts == 1) return GEMM_OK;
-    const LossFold fold{s.M, s.K, held, back, a.dA, a.ldda, a.a_grad_type == GEMM_OUTPUT_F32};
+    const LossFold fold{s.M, s.K, held, back, row, a.dA, a.ldda, a.a_grad_type == GEMM_OUTPUT_F32};
     const dim3 blocks((unsigned)ceil_div(s.M * ceil_div(s.K, 8), 256));
     return s.input_type == GEMM_INPUT_BF16 ? launch(loss_fold_kernel<kInputBf16>, blocks, 256, stream, fold)
                                            : launch(loss_fold_kernel<kInputF16>, blocks, 256, stream, fold);

@@ -194,42 +194,127 @@ __device__ inline void loss_join(const LossRowsProblem& p, int64_t slots, int ro
 // power of two by half as much as what lies just above (181 tokens of
 // weights even between 0 and 1 / 181 = 1.41 * 2^-8: the targets' entries off by
 // 1.7e-3 of their norm in bf16 with a power of two, 1.5e-3 so).
+//
+// In fp16 a token of far less weight would lose its row of dA all the same
+// (256 tokens of 131072 words, one in eight 1e8 times as heavy as the others:
+// the light ones' rows off by 16 % of their norm, 24 tokens at 1e6 by 1e-3).
+// So each row is held at the factor times a power of two of its own, 2^j, that
+// takes its |dloss| into [2^13, 2^14).  dA's rows are multiplied by 2^-j in the
+// epilogue.  In dB's sum over the tokens 2^-j goes to the row of A, in a copy of
+// its own, and that copy is lifted by one power of two, 2^lift, the largest that
+// no row overflows with: a row is then below fp16's normal numbers only where it
+// has 2^-29 of the largest |dloss| times |A| left.  bf16 has fp32's range: j = 0.
+// It costs fp16 a pass over A and a launch: 1000 tokens x 32001 words x 1000 265
+// us against 258, 24 x 4096 x 512 35 against 32.
 struct LossRow {
-    float lse, scale;  // scale: dloss times the factor; without a target infinity and 0, which make zeros
-    int32_t target, pad;
+    float lse, scale;  // scale: dloss times the factor and 2^j; without a target infinity and 0, which make zeros
+    int32_t target;
+    float shrink;      // 2^-j
+};
+struct LossBack {
+    float factor, lift;  // one over each
 };
 constexpr float kLargestSlope = 16352.0f;  // 2^14 (1 - 2^-9)
-constexpr int kLossBeginThreads = 256;
+constexpr int kMostShift = 40;             // of j: what fp16 holds of a row that is 2^-40 of the largest is nothing
+constexpr int kLossBeginThreads = 256, kLossBeginWaves = kLossBeginThreads / kWave;
+constexpr int kMostLifts = kLossBeginThreads;
 struct LossPrepare {
     int64_t rows, words;
     Targets targets;
     const float *lse, *dloss;
     LossRow* row;
-    float* back;  // one over the factor
+    LossBack* back;
+    const uint16_t* A;  // fp16's; nullptr: j = 0 and lift = 0
+    int64_t lda, width;
+    int32_t* lifts;     // the largest lift of each workgroup's rows
 };
-// By the first `blocks` workgroups, each of which reads all of dloss.
+__device__ inline float power_of_two(int n) { return __builtin_bit_cast(float, (uint32_t)(127 + n) << 23); }
+__device__ inline int exponent_of(float v) { return (int)(__builtin_bit_cast(uint32_t, v) >> 23 & 0xff) - 127; }
+// The largest shift of a row whose largest entry is `slope`, from 0 to kMostShift (the largest for 0, and for NaN).
+__device__ inline int row_shift(float slope) {
+    const int j = exponent_of(kLargestSlope / slope);
+    return j < 0 ? 0 : j < kMostShift ? j : kMostShift;
+}
+// By the first `blocks` workgroups, each of which reads all of dloss; of fp16, a wave reads a row of A.
 __device__ inline void loss_prepare(const LossPrepare& p, uint32_t blocks) {
     if (blockIdx.x >= blocks) return;
-    __shared__ float most[kLossBeginThreads / kWave];
+    __shared__ float most[kLossBeginWaves];
+    __shared__ int least[kLossBeginWaves];
+    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
     float m = 0.0f;
 #pragma unroll 4
     for (int64_t r = threadIdx.x; r < p.rows; r += kLossBeginThreads)
         if (p.targets.column(r, p.words) >= 0) m = fmaxf(m, fabsf(p.dloss[r]));
 #pragma unroll
     for (int d = 1; d < kWave; d *= 2) m = fmaxf(m, __shfl_xor(m, d));
-    if (threadIdx.x % kWave == 0) most[threadIdx.x / kWave] = m;
+    if (lane == 0) most[wave] = m;
     __syncthreads();
     m = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kLossBeginThreads / kWave; ++w) m = fmaxf(m, most[w]);
+    for (int w = 0; w < kLossBeginWaves; ++w) m = fmaxf(m, most[w]);
     float scale = 1.0f;  // (nothing to hold, or nothing that can be held: as it is)
     if (m > 0.0f && m < __builtin_inff()) scale = fminf(kLargestSlope / m, 0x1p126f);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.back = 1.0f / scale;
-    for (int64_t r = (int64_t)blockIdx.x * kLossBeginThreads + threadIdx.x; r < p.rows;
-         r += (int64_t)blocks * kLossBeginThreads) {
-        const int target = p.targets.column(r, p.words);
-        p.row[r] = target < 0 ? LossRow{__builtin_inff(), 0.0f, -1, 0} : LossRow{p.lse[r], p.dloss[r] * scale, target, 0};
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.back = LossBack{1.0f / scale, 1.0f};
+    const LossRow none{__builtin_inff(), 0.0f, -1, 1.0f};
+    if (!p.A) {
+        for (int64_t r = (int64_t)blockIdx.x * kLossBeginThreads + threadIdx.x; r < p.rows;
+             r += (int64_t)blocks * kLossBeginThreads) {
+            const int target = p.targets.column(r, p.words);
+            p.row[r] = target < 0 ? none : LossRow{p.lse[r], p.dloss[r] * scale, target, 1.0f};
+        }
+        return;
     }
+    int lift = kMostShift;
+    for (int64_t r = (int64_t)blockIdx.x * kLossBeginWaves + wave; r < p.rows; r += (int64_t)blocks * kLossBeginWaves) {
+        const int target = p.targets.column(r, p.words);
+        if (target < 0) {
+            if (lane == 0) p.row[r] = none;
+            continue;
+        }
+        int largest = 0;  // of the row's magnitudes, as bits
+        for (int64_t col = lane * 8; col < p.width; col += kWave * 8) {
+            const Row8 v = load8(p.A + r * p.lda + col, p.width - col);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int low = (int)(v.w[e] & 0x7fffu), high = (int)(v.w[e] >> 16 & 0x7fffu);
+                largest = largest > low ? largest : low;
+                largest = largest > high ? largest : high;
+            }
+        }
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2) {
+            const int other = __shfl_xor(largest, d);
+            largest = largest > other ? largest : other;
+        }
+        const float slope = p.dloss[r] * scale;
+        const int j = row_shift(fabsf(slope));
+        // (a row of zeros has room for any lift, and one with an infinity or NaN as much as its other values may need)
+        const int top = largest < 0x7c00 ? exponent_of((float)__builtin_bit_cast(_Float16, (uint16_t)largest)) : 15;
+        lift = lift < j + 15 - top ? lift : j + 15 - top;
+        if (lane == 0) p.row[r] = LossRow{p.lse[r], slope * power_of_two(j), target, power_of_two(-j)};
+    }
+    if (lane == 0) least[wave] = lift;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int w = 1; w < kLossBeginWaves; ++w) lift = lift < least[w] ? lift : least[w];
+        p.lifts[blockIdx.x] = lift;
+    }
+}
+// The lift of all rows, by every thread of a workgroup.
+__device__ inline int common_lift(const int32_t* lifts, int count) {
+    __shared__ int least[kLossBeginWaves];
+    int lift = (int)threadIdx.x < count ? lifts[threadIdx.x] : kMostShift;
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        const int other = __shfl_xor(lift, d);
+        lift = lift < other ? lift : other;
+    }
+    if (threadIdx.x % kWave == 0) least[threadIdx.x / kWave] = lift;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kLossBeginWaves; ++w) lift = lift < least[w] ? lift : least[w];
+    return lift;
 }
 
 // A piece's dZ: ep.out has rows of whole 16 bytes, zeros past the piece.
@@ -259,7 +344,7 @@ struct EpilogueRows<LossSlopeProblem> {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int64_t r = row0 + h * kWave + lane;
-            held[h] = LossRow{__builtin_inff(), 0.0f, -1, 0};
+            held[h] = LossRow{__builtin_inff(), 0.0f, -1, 1.0f};
             if (h * kWave + lane < rows && r < row_end) held[h] = p.row[r];
         }
     }
@@ -302,19 +387,20 @@ struct EpilogueRows<LossSlopeProblem> {
 
 // A gradient's product.  dB's piece is whole: scaled back and stored.  dA's is
 // added to the sums of the pieces before it (fp32), and scaled back where it
-// is the last.  (Of two types: what the second has beside the first would not
+// is the last, by each row's own power of two (fp16) and by the factor.  (Of two types: what the second has beside the first would not
 // fit the registers of the first's 256x256 kernel.)
 struct LossWordsGradProblem : LinearProblem {
     static constexpr int EPILOGUE = kEpilogueValues;
     static constexpr bool SHORT = true;
-    const float* back;
+    const LossBack* back;
 };
 struct LossTokensGradProblem : LinearProblem {
     static constexpr int EPILOGUE = kEpilogueValues;
     static constexpr bool SHORT = false;
     const float* before;  // or nullptr; rows before_ld apart
     int64_t before_ld;
-    const float* back;    // nullptr: another piece follows
+    const LossBack* back;  // nullptr: another piece follows
+    const LossRow* row;    // nullptr: no powers of the rows' own, or another piece follows
 };
 template <int TYPE>
 __device__ inline void store_gradient(const LinearEpilogue& ep, const EpilogueBase& base, const EpilogueLane& at,
@@ -327,20 +413,38 @@ __device__ inline void store_gradient(const LinearEpilogue& ep, const EpilogueBa
 template <>
 struct EpilogueRows<LossWordsGradProblem> {
     __device__ void load(const LossWordsGradProblem&, int64_t, int64_t, int, int) {}
+    __device__ void load_one(const LossWordsGradProblem&, int64_t) {}
     __device__ void of_row(int, int) {}
     template <int TYPE>
     __device__ void finish(const LossWordsGradProblem& p, const EpilogueBase& base, const EpilogueLane& at, int64_t,
                            int64_t, int64_t left, float (&z)[8]) const {
-        const float back = *p.back;
+        // (a product by a power of two first: of both factors it might lie below fp32's numbers)
+        const LossBack back = *p.back;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] *= back;
+        for (int e = 0; e < 8; ++e) z[e] = z[e] * back.lift * back.factor;
         store_gradient<TYPE>(p.ep, base, at, left, z);
     }
 };
+// (the rows' powers as LossSlopeProblem has its rows' values)
 template <>
 struct EpilogueRows<LossTokensGradProblem> {
-    __device__ void load(const LossTokensGradProblem&, int64_t, int64_t, int, int) {}
-    __device__ void of_row(int, int) {}
+    float held[2], now = 1.0f;
+    bool rows;
+    __device__ void load(const LossTokensGradProblem& p, int64_t row0, int64_t row_end, int count, int lane) {
+        rows = p.row;
+        if (!rows) return;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t r = row0 + h * kWave + lane;
+            held[h] = h * kWave + lane < count && r < row_end ? p.row[r].shrink : 1.0f;
+        }
+    }
+    __device__ void load_one(const LossTokensGradProblem& p, int64_t row) {
+        if (p.row) now = p.row[row].shrink;
+    }
+    __device__ void of_row(int m, int r) {
+        if (rows) now = __shfl(m < kWave ? held[0] : held[1], (m + r) % kWave);
+    }
     template <int TYPE>
     __device__ void finish(const LossTokensGradProblem& p, const EpilogueBase& base, const EpilogueLane& at, int64_t row,
                            int64_t col, int64_t left, float (&z)[8]) const {
@@ -351,9 +455,9 @@ struct EpilogueRows<LossTokensGradProblem> {
             for (int e = 0; e < 8; ++e) z[e] += add[e];
         }
         if (p.back) {
-            const float back = *p.back;
+            const float back = p.back->factor;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] *= back;
+            for (int e = 0; e < 8; ++e) z[e] = z[e] * now * back;
         }
         store_gradient<TYPE>(p.ep, base, at, left, z);
     }
@@ -363,7 +467,8 @@ struct EpilogueRows<LossTokensGradProblem> {
 struct LossFold {
     int64_t rows, cols;
     const float* held;  // 2 rows x cols
-    const float* back;
+    const LossBack* back;
+    const LossRow* row;
     void* out;
     int64_t ldo;
     int32_t out_f32;
@@ -373,12 +478,12 @@ __device__ inline void loss_fold(const LossFold& p) {
     const int64_t groups = (p.cols + 7) / 8, i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= p.rows * groups) return;
     const int64_t row = i / groups, col = i % groups * 8, left = p.cols - col;
-    const float back = *p.back;
+    const float back = p.back->factor, shrink = p.row[row].shrink;
     float z[8], rest[8];
     load8(z, p.held + row * p.cols + col, left);
     load8(rest, p.held + (p.rows + row) * p.cols + col, left);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) z[e] = (z[e] + rest[e]) * back;
+    for (int e = 0; e < 8; ++e) z[e] = (z[e] + rest[e]) * shrink * back;
     if (p.out_f32)
         store8(static_cast<float*>(p.out) + row * p.ldo + col, z, left);
     else
@@ -386,7 +491,8 @@ __device__ inline void loss_fold(const LossFold& p) {
 }
 
 // Copies a matrix to rows of whole 16 bytes, zeros past their width; with
-// targets, rows without one as zeros, so that nothing they hold reaches dB.
+// targets, rows without one as zeros, so that nothing they hold reaches dB;
+// with `row` (fp16), each row times its 2^-j and the lift of all.
 struct LossPack {
     const uint16_t* src;
     int64_t rows, cols, ld;
@@ -395,6 +501,10 @@ struct LossPack {
     int32_t copies;   // one below the other, two at most
     Targets targets;  // at == nullptr: every row
     int64_t words;
+    const LossRow* row;
+    const int32_t* lifts;
+    int32_t count;  // of lifts
+    LossBack* back;
 };
 // EACH accesses of a thread, under way together: 513 rows of 32001 odd columns
 // and 1000 of 513 take 12 us with four against 15 with one (8: 13); up to
@@ -406,6 +516,12 @@ template <int EACH>
 __device__ inline void loss_pack(const LossPack& j) {
     const int64_t groups = j.ldd / 8, total = j.copies * j.rows * groups;
     const int64_t span = (int64_t)kLossBeginThreads * EACH;  // a workgroup's
+    float lifted = 1.0f;
+    if (j.row) {
+        const int lift = common_lift(j.lifts, j.count);
+        lifted = power_of_two(lift);
+        if (blockIdx.x == 0 && threadIdx.x == 0) j.back->lift = power_of_two(-lift);
+    }
     for (int64_t i0 = blockIdx.x * span + threadIdx.x; i0 < total; i0 += gridDim.x * span) {
         Row8 v[EACH];
 #pragma unroll
@@ -418,6 +534,14 @@ __device__ inline void loss_pack(const LossPack& j) {
             const int64_t col = (i - to * groups) * 8, row = to < j.rows ? to : to - j.rows;
             v[k] = load8(j.src + row * j.ld + col, j.cols - col);  // (on its way together with the target)
             if (j.targets.at && j.targets.column(row, j.words) < 0) v[k] = Row8{};
+            if (j.row) {
+                const float by = j.row[row].shrink * lifted;
+                float x[8];
+                v[k].template widen<kInputF16>(x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= by;
+                v[k] = Row8::narrow<kInputF16>(x);
+            }
         }
 #pragma unroll
         for (int k = 0; k < EACH; ++k) {  // (rows of dst lie one after the other)
@@ -427,12 +551,14 @@ __device__ inline void loss_pack(const LossPack& j) {
     }
 }
 
-// What comes before the products, in one launch: the rows' values, in the
+// What comes before the products, in one launch (the copy of A for dB in fp16,
+// which needs the rows' values, in another): the rows' values, in the
 // first row of workgroups so that they do not begin when the copies end, and
 // copies.
 struct LossBegin {
     LossPack pack[2];
     int32_t packs, each;
+    uint32_t prepare_blocks;
     LossPrepare prepare;
 };
 

@@ -729,9 +729,13 @@ int gemm_dropout(int value_type, int64_t rows, int64_t cols, double p, uint64_t 
  *     dZ[t][w] = (exp(Z[t][w] - lse[t]) - (w == targets[t])) * dloss[t]
  *     dA = dZ @ B^T,   dB = A^T @ dZ
  * The gradients compute Z again, a piece of the vocabulary at a time; a piece's
- * dZ lies in the workspace, rounded to the input type (times the factor that
- * makes the largest |dloss| about 2^14, so that fp16 holds small
- * probabilities), and dA's sums over the pieces are fp32.
+ * dZ lies in the workspace, rounded to the input type (up to 32 tokens in two
+ * parts, the second what the first left), and dA's sums over the pieces are fp32.
+ * dZ is held times the factor that makes the largest |dloss| about 2^14, so that
+ * fp16 holds small probabilities, and in fp16 each token's times a power of two of
+ * its own, up to 2^40, so that light tokens keep their digits beside heavy ones:
+ * dA's rows keep theirs down to weights of 2^-40 of the largest, dB's terms down to
+ * 2^-24 of the largest |dloss| times largest |A| of a token (2^-40: nothing left).
  *
  * Conventions are those at the top of this header, and:
  *   - A target outside [0, N) is none: the token's loss and gradients are zero,
@@ -809,8 +813,8 @@ typedef struct {
  * gemm_cross_entropy's.  Returns a gemm_status. */
 int gemm_cross_entropy_grad(const gemm_cross_entropy_grad_args *args, void *stream);
 
-/* Bytes gemm_cross_entropy_grad needs: A packed, a piece's dZ, dA's sums where
- * there is more than one piece, packed pieces of B and the products' slices. */
+/* Bytes gemm_cross_entropy_grad needs: A packed (in fp16 twice, where dB is
+ * wanted), a piece's dZ, dA's sums where there is more than one piece, packed pieces of B and the products' slices. */
 int64_t gemm_cross_entropy_grad_workspace_bytes(const gemm_cross_entropy_grad_args *args, int32_t num_cus);
 
 #ifdef __cplusplus
