@@ -12,13 +12,14 @@ from norm_reference import LOW, drop_count
 M64 = (1 << 64) - 1
 
 
-def keep(rows: int, cols: int, p: float, seed: int, offset: int, device="cpu") -> torch.Tensor:
-    """rows x cols factors in float64: 0 where dropped, 65536 / (65536 - drop) where kept."""
+def keep(rows: int, cols: int, p: float, seed: int, offset: int, device="cpu", first: int = 0) -> torch.Tensor:
+    """rows x cols factors in float64: 0 where dropped, 65536 / (65536 - drop) where kept.  `first`: the first row's first
+    block, where it is not the matrix's."""
     drop = drop_count(p)
     if drop == 0:
         return torch.ones(rows, cols, dtype=torch.float64, device=device)
     each = -(-cols // 8)
-    block = torch.arange(rows * each, dtype=torch.int64, device=device)
+    block = torch.arange(first, first + rows * each, dtype=torch.int64, device=device)
     place = offset & M64
     c = [block & LOW, block >> 32 & LOW, torch.full_like(block, place & LOW), torch.full_like(block, place >> 32)]
     k = [seed & LOW, seed >> 32]

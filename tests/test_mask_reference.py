@@ -30,3 +30,8 @@ def test_a_row_under_the_mask_of_another_is_seen():
     assert bool(((value.bfloat16().double() - value).abs() <= tol).all())
     seen = ((wrong.double() - value).abs() > tol).any(1)
     assert not bool(seen[:places].any()) and bool(seen[places:].all())
+
+
+def test_rows_of_a_larger_matrix():
+    whole = mask_reference.keep(9, 41, 0.3, 5, 7)
+    assert torch.equal(mask_reference.keep(3, 41, 0.3, 5, 7, first=6 * 6), whole[6:])
