@@ -776,7 +776,7 @@ int mixed_auto_variant(int64_t M, int64_t N, int64_t K, int num_cus) {
     // The K split over four groups from K = 4096, or when its grid has at
     // most one tile per CU from K = 1024 for 32x64 tiles and K = 2048 for
     // 64x64 (bf16 on one box: 32x64_KS4 11-25 % ahead of the previous pick
-    // on 1-2k-row grids at K = 1024-3072; at 1024^3 64x64_KS4 ran 10 %
+    // on 1-2k-row grids at K = 1k to 3k; at 1024^3 64x64_KS4 ran 10 %
     // behind 64x64_KS2, four K tiles of 64 per group being too few).  Two
     // groups from K = 2048, or K = 1024 on a one-round grid.
     if (K >= 4096 || (K >= 2048 && t64 <= num_cus))

@@ -15,10 +15,11 @@
 // back, of which 2 M N K are the logits again; keeping them instead would take
 // M N values of memory.
 //
-// Measured: 8192 tokens by 131072 words, 4096 deep, bf16: 6.1 ms forward (1.44
-// PFLOP/s; the library's plain product of 8192^3 runs at 1.39-1.61), 19.1 ms
-// back in four pieces: logits 1.62 ms a piece, dB 1.63, dA 1.51 (1.36, 1.35 and
-// 1.46 PFLOP/s).  24 tokens: 183 us (5.9 TB/s of the weights).
+// Measured: 8192 tokens by 131072 words, 4096 deep, bf16, by card: 6.1-6.3 ms
+// forward (1.39-1.44 PFLOP/s; the library's plain product of 8192^3 runs at
+// 1.39-1.61), 19.1-19.7 ms back in four pieces: logits 1.62-1.66 ms a piece, dB
+// 1.63-1.68, dA 1.51-1.54 (1.33-1.36, 1.31-1.35 and 1.43-1.46 PFLOP/s).  24
+// tokens: 181-183 us (5.9 TB/s of the weights).
 #pragma once
 
 #include "linear_shapes.hpp"

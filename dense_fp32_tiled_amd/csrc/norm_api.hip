@@ -110,7 +110,9 @@ struct RunNorm {
 };
 
 // Workgroups of the gradient's kernel: sixteen waves per CU, each with as
-// many rows as it takes, since each leaves a row of sums to join.
+// many rows as it takes, since each leaves a row of sums to join.  That was
+// measured for many rows (16384 x 4096); up to some thousand a place has a row or
+// two, and its sums outweigh them: 1000 x 513 fp32 8.0 us and 5.9 for the join.
 template <int TYPE, class Shape, bool WHOLE>
 struct GradPlaces {
     static constexpr bool GRADIENT = true;

@@ -17,10 +17,12 @@
 // The gradient of weight and bias is summed in registers over the rows that a
 // workgroup takes, and joined over the workgroups in a fixed order.
 //
-// Measured with the residual stream, bf16 (a large copy here runs at 5.1 TB/s):
+// Measured with the residual stream, bf16 (a copy of 1 GiB here runs at 5.1
+// TB/s, which rows from several streams pass):
 // 16384 x 4096 with dropout 97 us (5.5 TB/s of 537 MB), its gradients 132 us
 // (5.1 TB/s of 671 MB) and 5 us for the join; 4096 x 16384 99 and 119 us without
-// dropout; rows aligned to nothing, 16384 x 4095, 132 and 156 us.
+// dropout; rows aligned to nothing, 16384 x 4095, 132 and 156 us.  fp32, 8192 x
+// 8192: 192 us (5.6 TB/s), its gradients 206 (5.2).
 #pragma once
 
 #include "dropout.hpp"
@@ -194,8 +196,10 @@ __global__ __launch_bounds__(Shape::THREADS, Shape::MIN_WAVES) void norm_kernel(
     }
 }
 
-// Rows too wide for the registers: the row is read three times, from the
-// caches after the first.
+// Rows too wide for the registers, and those of fewer than eight columns: the
+// row is read three times, from the caches after the first.  4096 x 20000 bf16
+// with the residual stream 216 us (3.0 TB/s of 655 MB); 2^20 x 4 12.4 ms, a
+// workgroup a row.
 constexpr int kWideThreads = 1024;
 template <int TYPE>
 __global__ __launch_bounds__(kWideThreads) void norm_wide_kernel(NormProblem p) {
@@ -495,8 +499,10 @@ __global__ __launch_bounds__(kNormJoinCols * kNormJoinStrides) void norm_join_ke
     }
 }
 
-// Rows too wide for the registers: the row's sums and results in two passes,
-// and the columns' sums in a kernel of their own.
+// Rows too wide for the registers (or of fewer than eight columns): the row's
+// sums and results in two passes, and the columns' sums in a kernel of their
+// own.  2048 x 16384 fp32 with the stream's gradient 124 + 53 us and 8 for the join
+// (537 MB would take 105), 4096 x 20000 bf16 185 + 73 + 9.
 template <int TYPE>
 __global__ __launch_bounds__(kWideThreads) void norm_grad_wide_kernel(NormProblem p) {
     using V = Values8<TYPE>;
