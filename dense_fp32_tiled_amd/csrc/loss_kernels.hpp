@@ -200,11 +200,14 @@ __device__ inline void loss_join(const LossRowsProblem& p, int64_t slots, int ro
 // (256 tokens of 131072 words, one in eight 1e8 times as heavy as the others:
 // the light ones' rows off by 16 % of their norm, 24 tokens at 1e6 by 1e-3).
 // So each row is held at the factor times a power of two of its own, 2^j, that
-// takes its |dloss| into [2^13, 2^14).  dA's rows are multiplied by 2^-j in the
-// epilogue.  In dB's sum over the tokens 2^-j goes to the row of A, in a copy of
-// its own, and that copy is lifted by one power of two, 2^lift, the largest that
-// no row overflows with: a row is then below fp16's normal numbers only where it
-// has 2^-29 of the largest |dloss| times |A| left.  bf16 has fp32's range: j = 0.
+// takes its |dloss| into [2^13, 2^14) or 2^16 times further up.  dA's rows are
+// multiplied by 2^-j in the epilogue.  In dB's sum over the tokens 2^-j goes to
+// the row of A, in a copy of its own, and that copy is lifted by one power of
+// two, 2^lift, the largest that no row overflows with, 2^15 over the largest |A|
+// or more: what fp16 does not hold of a lowered row is below 2^-24 of the largest
+// |A|.  A larger 2^j would take digits of dB for those of dA; with 2^16 tokens of
+// 1e-9 of the largest weight are as exact as those of 6e-5 are without.  bf16 has
+// fp32's range: j = 0.
 // It costs fp16 a pass over A and a launch: 1000 tokens x 32001 words x 1000 265
 // us against 258, 24 x 4096 x 512 35 against 32.
 struct LossRow {
@@ -216,7 +219,7 @@ struct LossBack {
     float factor, lift;  // one over each
 };
 constexpr float kLargestSlope = 16352.0f;  // 2^14 (1 - 2^-9)
-constexpr int kMostShift = 40;             // of j: what fp16 holds of a row that is 2^-40 of the largest is nothing
+constexpr int kMostShift = 16;             // of j
 constexpr int kLossBeginThreads = 256, kLossBeginWaves = kLossBeginThreads / kWave;
 constexpr int kMostLifts = kLossBeginThreads;
 struct LossPrepare {
@@ -231,7 +234,7 @@ struct LossPrepare {
 };
 __device__ inline float power_of_two(int n) { return __builtin_bit_cast(float, (uint32_t)(127 + n) << 23); }
 __device__ inline int exponent_of(float v) { return (int)(__builtin_bit_cast(uint32_t, v) >> 23 & 0xff) - 127; }
-// The largest shift of a row whose largest entry is `slope`, from 0 to kMostShift (the largest for 0, and for NaN).
+// The largest shift of a row whose largest entry is `slope`, from 0 to kMostShift (that for 0 and NaN).
 __device__ inline int row_shift(float slope) {
     const int j = exponent_of(kLargestSlope / slope);
     return j < 0 ? 0 : j < kMostShift ? j : kMostShift;

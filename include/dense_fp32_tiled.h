@@ -736,9 +736,9 @@ int gemm_dropout(int value_type, int64_t rows, int64_t cols, double p, uint64_t 
  * parts, the second what the first left), and dA's sums over the pieces are fp32.
  * dZ is held times the factor that makes the largest |dloss| about 2^14, so that
  * fp16 holds small probabilities, and in fp16 each token's times a power of two of
- * its own, up to 2^40, so that light tokens keep their digits beside heavy ones:
- * dA's rows keep theirs down to weights of 2^-40 of the largest, dB's terms down to
- * 2^-24 of the largest |dloss| times largest |A| of a token (2^-40: nothing left).
+ * its own, up to 2^16, so that light tokens keep their digits beside heavy ones:
+ * its entries have steps of 2^-37 of the token's |dloss|, or of 2^-54 of the
+ * largest |dloss| where that is more; dB reads A to 2^-24 of the largest |A|.
  *
  * Conventions are those at the top of this header, and:
  *   - A target outside [0, N) is none: the token's loss and gradients are zero,

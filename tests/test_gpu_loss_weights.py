@@ -145,3 +145,26 @@ def test_one_gradient_alone_and_captured(M):
         torch.cuda.synchronize()
         want = both()
         assert torch.equal(held.a, want.a) and torch.equal(held.b, want.b), n
+
+
+@pytest.mark.parametrize("M", [20, 100])
+@pytest.mark.parametrize("ratio", [1e-2, 1e-5, 1e-8])
+def test_words_of_light_tokens_beside_large_values(ratio, M):
+    """A heavy token of large values and sure of its word (any other has e^-40 of it), light ones of small values in
+    features of their own: dB at a light token's feature and target has that token's term alone, -g a (1 - p).  A is held
+    to 2^-24 of its largest value; the target's entry of dZ and the products add 2^-11 and a few 2^-24 each."""
+    N, K, heavy = 5000, 128, 200.0
+    a, b = torch.zeros(M, K, dtype=torch.float16, device="cuda"), torch.zeros(N, K, dtype=torch.float16, device="cuda")
+    small = 0.02 * (1 + torch.arange(1, M, device="cuda") / M)
+    light = torch.arange(1, M, device="cuda")
+    a[0, 0], b[0, 0] = heavy, 0.2
+    a[light, light] = small.half()
+    t = torch.cat([torch.zeros(1, device="cuda").long(), 7 + 40 * light])
+    g = torch.full((M,), ratio, device="cuda")
+    g[0] = 1.0
+    _, lse = dft.linear_cross_entropy(a, b.t(), t)
+    grads = dft.linear_cross_entropy_grad(g, a, b.t(), t, lse, a_dtype=torch.float32, b_dtype=torch.float32)
+    got = grads.b[light, t[light]].double()
+    want = -g[light].double() * a[light, light].double() * (1 - torch.exp(-lse[light].double()))
+    rel = 2.0 ** -24 * heavy / a[light, light].double() + 2.0 ** -11 + 2.0 ** -20
+    assert bool(((got - want).abs() <= rel * want.abs()).all()), ((got / want - 1).abs() / rel).max()
